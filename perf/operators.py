@@ -214,7 +214,7 @@ def prepare(case, seed):
         s["norm"] = torch.empty(2, device="cuda")
         if own:
             import learnable_butterfly_rotation_amd as B
-            s["workspace"] = torch.empty(B.bfly_grad_clip_workspace_bytes(sizes),
+            s["workspace"] = torch.empty(B.bfly_grad_clip_workspace_bytes(len(sizes)),
                                          dtype=torch.uint8, device="cuda")
     return s
 
