@@ -28,6 +28,9 @@
  *   bfly_backward, bfly_kron_backward            dX and the angle gradients
  *   bfly_calib_step, bfly_calib_step_weight      one step of learning the angles
  *   bfly_quant_matmul                            y = (Q x)(W Q^T)^T from the codes
+ *   bfly_rmsnorm, bfly_rmsnorm_backward          the norm in front of a rotated layer
+ *   bfly_lora_matmul                             low-rank adapters beside a product
+ *   bfly_grad_clip                               global gradient norm and clipping
  *   bfly_*_bytes, bfly_status_string, bfly_last_hip_error
  *   bfly_forward_quant_noalloc                   bfly_forward_quant with a fixed scratch
  *   bfly_time_next_forward                       kernel-only timing of the next forward
@@ -427,6 +430,151 @@ bfly_status bfly_quant_matmul(const void* a, bfly_dtype a_dt, const uint8_t* cod
                               const uint16_t* scales, const uint16_t* zeros, void* y,
                               bfly_dtype y_dt, int64_t rows, int32_t n_out, int32_t k,
                               int32_t bits, int32_t group, bfly_qmode mode, void* hip_stream);
+
+/* ---- the norm in front of a layer ----------------------------------------- */
+
+/* Formats of the 8-bit rows of bfly_rmsnorm.  Both take one fp16 scale per
+ * group, scale = fp16(max |y| / top) (saturated at 65504), and store
+ * code = rnd(clamp(y / scale, -top, top)), to nearest, ties to even; a zero
+ * scale gives zero codes.
+ *   BFLY_Q8_INT8 : top = 127, two's-complement bytes (BFLY_SYM_ABSMAX at 8 bits)
+ *   BFLY_Q8_E4M3 : top = 448, OCP 8-bit floats (1 sign, 4 exponent, 3 mantissa bits) */
+typedef enum {
+    BFLY_Q8_INT8 = 0,
+    BFLY_Q8_E4M3 = 1,
+    BFLY_Q8_RANGE_LOW_ = -2147483647 - 1,
+    BFLY_Q8_RANGE_HIGH_ = 2147483647
+} bfly_q8;
+
+/* The residual's addition, the root-mean-square norm and 8-bit quantization
+ * of every row, in one pass:
+ *   h    = x + residual, rounded to x's type (h = x without a residual)
+ *   rstd = (mean_i h_i^2 + eps)^(-1/2)
+ *   y_i  = (h_i * rstd) * weight_i, in fp32
+ * and from the fp32 y the codes and scales.  These are the rows that enter a
+ * rotated layer (y into bfly_forward, bfly_forward_quant or
+ * bfly_quant_matmul); with an orthogonal rotation folded into the residual
+ * stream and weight folded into the next matrix, weight is NULL.
+ *   x        : [rows][n] of x_dt
+ *   residual : [rows][n] of x_dt, or NULL
+ *   h        : [rows][n] of x_dt, or NULL (not stored); needs a residual
+ *   weight   : [n] of w_dt, or NULL (ones)
+ *   y        : [rows][n] of y_dt (rounded to nearest even), or NULL
+ *   codes    : u8 [rows][n], or NULL; scales: fp16 bit patterns
+ *              [rows][n/group], NULL with codes
+ *   rstd     : fp32 [rows], or NULL (what bfly_rmsnorm_backward takes)
+ *   format, group: of the codes; group is n (one scale per row) or 8, 16, 32,
+ *              64, 128, 256 or 512 dividing n.  Not looked at without codes.
+ * At least one of h, y, codes and rstd is asked for.  h may be x or residual;
+ * otherwise y may be x or residual where the types are equal; no other
+ * aliasing.  The sum of squares is held in fp64, so that a code or a scale
+ * next to a rounding border does not depend on the order of the sum.
+ * Any n in [1, 16384] (multiples of 8 take the vector path); eps positive and
+ * finite.  x, residual, h, weight, y and codes 16-byte aligned.  A row that
+ * holds an infinity has rstd = 0; one that holds a NaN has NaN in rstd and y;
+ * the codes and scales of such a row are unspecified.  rows == 0 is a no-op.
+ * Errors: BFLY_ERR_NULL, BFLY_ERR_DTYPE, BFLY_ERR_SIZE (rows < 0, n < 1, eps
+ * not positive and finite), BFLY_ERR_QUANT, BFLY_ERR_ALIGN,
+ * BFLY_ERR_UNSUPPORTED (n > 16384), BFLY_ERR_HIP. */
+bfly_status bfly_rmsnorm(const void* x, bfly_dtype x_dt, const void* residual, void* h,
+                         const void* weight, bfly_dtype w_dt, void* y, bfly_dtype y_dt,
+                         uint8_t* codes, uint16_t* scales, float* rstd, int64_t rows, int32_t n,
+                         float eps, bfly_q8 format, int32_t group, void* hip_stream);
+
+/* Gradients of y = h rstd weight (straight through the quantizer), given
+ * dy = dL/dy and optionally dh, the gradient that reaches h by itself (the
+ * residual stream's):
+ *   g_i     = dy_i * weight_i,  xhat_i = h_i * rstd
+ *   dx_i    = dh_i + (g_i - xhat_i * mean_j(g_j xhat_j)) * rstd
+ *   dweight = sum over rows of dy * xhat, fp32 [n], OVERWRITTEN (zeros when
+ *             rows == 0)
+ * dx is the gradient of x and, the addition passing it on, of the residual.
+ *   h      : [rows][n] of h_dt (the h of bfly_rmsnorm, or its x)
+ *   weight : [n] of w_dt, or NULL (ones)
+ *   rstd   : fp32 [rows] from bfly_rmsnorm
+ *   dy, dh, dx: [rows][n] of g_dt; dh may be NULL; dx may be dy or dh, and h
+ *            where h_dt is g_dt
+ *   dweight: may be NULL (the workspace is then not used and may be NULL)
+ *   workspace: >= bfly_rmsnorm_backward_workspace_bytes(rows, n) bytes of
+ *            device scratch, 16-byte aligned
+ * dweight's sum has a fixed order that depends on (rows, n) only: the same
+ * bits from run to run.  Sizes, alignment and errors as bfly_rmsnorm, plus
+ * BFLY_ERR_WORKSPACE. */
+bfly_status bfly_rmsnorm_backward(const void* h, bfly_dtype h_dt, const void* weight,
+                                  bfly_dtype w_dt, const float* rstd, const void* dy,
+                                  const void* dh, void* dx, bfly_dtype g_dt, float* dweight,
+                                  int64_t rows, int32_t n, void* workspace,
+                                  size_t workspace_bytes, void* hip_stream);
+
+size_t bfly_rmsnorm_backward_workspace_bytes(int64_t rows, int32_t n);
+
+/* ---- low-rank adapters beside a shared product ------------------------------ */
+
+/* y[r] = base[r] + scaling[id] * B_id (A_id x[r]) with id = ids[r], for the
+ * requests of one batch that use different adapters of a shared projection:
+ * base = bfly_quant_matmul's rows, x its activations a (or the rows before
+ * the rotation: the adapters' own basis).
+ *   x       : bf16 [rows][k] (x_dt must be BFLY_BF16)
+ *   ids     : int32 [rows], the row's adapter; an id outside
+ *             [0, n_adapters) is no adapter: y[r] = base[r] (0 without a base)
+ *   lora_a  : bf16 [n_adapters][rank][k]
+ *   lora_b  : bf16 [n_adapters][n_out][rank]
+ *             (adapters of a smaller rank are padded with zeros)
+ *   scaling : fp32 [n_adapters]
+ *   base    : [rows][n_out] of base_dt, or NULL (zeros)
+ *   y       : [rows][n_out] of y_dt; may be base where the types are equal
+ *             (rows without an adapter are then left as they are), no other
+ *             aliasing
+ *   workspace: >= bfly_lora_matmul_workspace_bytes(rows, n_out, k, rank)
+ *             bytes of device scratch, 16-byte aligned; two calls that may
+ *             overlap need one each
+ * Rows of one adapter need not lie together.  A_id x is summed in fp32 and
+ * enters the second product, times scaling, with 16 bits (bf16 y) or 24 (fp32
+ * y); y is rounded once.  A row's result does not depend on the other rows'.
+ * Sizes: k and n_out multiples of 8, k <= 65536, n_out <= 1048576, rank a
+ * multiple of 8 up to 256, rows <= 8388608, n_adapters >= 1.  All pointers
+ * 16-byte aligned but ids and scaling (4).  rows == 0 is a no-op.
+ * Errors: BFLY_ERR_NULL, BFLY_ERR_DTYPE, BFLY_ERR_SIZE (rows < 0 or another
+ * size below 1), BFLY_ERR_UNSUPPORTED, BFLY_ERR_WORKSPACE, BFLY_ERR_ALIGN,
+ * BFLY_ERR_HIP. */
+bfly_status bfly_lora_matmul(const void* x, bfly_dtype x_dt, const int32_t* ids,
+                             const void* lora_a, const void* lora_b, const float* scaling,
+                             const void* base, bfly_dtype base_dt, void* y, bfly_dtype y_dt,
+                             int64_t rows, int32_t n_out, int32_t k, int32_t n_adapters,
+                             int32_t rank, void* workspace, size_t workspace_bytes,
+                             void* hip_stream);
+
+size_t bfly_lora_matmul_workspace_bytes(int64_t rows, int32_t n_out, int32_t k, int32_t rank);
+
+/* ---- global gradient norm and clipping --------------------------------------- */
+
+/* The 2-norm over all elements of `count` tensors (the angle gradients of all
+ * layers, the norms' weight gradients) and every tensor scaled to it:
+ *   norm = sqrt(sum of g^2),  factor = norm > max_norm ? max_norm / norm : 1
+ *   outs[i] = grads[i] * factor
+ *   grads  : host array of device pointers, read before the call returns
+ *   outs   : host array of device pointers, or NULL (in place); outs[i] may
+ *            be grads[i], no other aliasing
+ *   numels : host array of element counts (0: a tensor without elements,
+ *            whose pointers are not looked at)
+ *   dtypes : host array of bfly_dtype values
+ *   norm   : device fp32 [2], receives the norm and the factor
+ *   workspace: >= bfly_grad_clip_workspace_bytes(count) bytes of device
+ *            scratch, 16-byte aligned; two calls that may overlap need one each
+ * Squares are summed in fp64 in an order that depends on the sizes only.  A
+ * norm that is not finite gives factor 1: it is reported in norm[0] and the
+ * gradients are left (copied) as they are.  In place with factor 1 nothing is
+ * written to the gradients.  max_norm > 0 (infinity: only the norm).  The
+ * pointers need their element's alignment only.  count <= 65536, below 2^42
+ * elements in all.  Errors: BFLY_ERR_NULL, BFLY_ERR_SIZE (a negative count or
+ * size, max_norm not positive), BFLY_ERR_DTYPE, BFLY_ERR_UNSUPPORTED,
+ * BFLY_ERR_WORKSPACE, BFLY_ERR_ALIGN, BFLY_ERR_HIP. */
+bfly_status bfly_grad_clip(int32_t count, const void* const* grads, void* const* outs,
+                           const int64_t* numels, const int32_t* dtypes, float max_norm,
+                           float* norm, void* workspace, size_t workspace_bytes,
+                           void* hip_stream);
+
+size_t bfly_grad_clip_workspace_bytes(int32_t count);
 
 /* ---- diagnostics -------------------------------------------------------- */
 

@@ -25,12 +25,17 @@ __all__ = [
     "bfly_calib_workspace_bytes", "bfly_calib_weight_config", "bfly_calib_step_weight",
     "bfly_calib_step_weight_workspace_bytes", "bfly_status_string",
     "bfly_last_hip_error", "bfly_time_next_forward", "bfly_forward_quant_noalloc",
+    "BFLY_Q8_INT8", "BFLY_Q8_E4M3", "bfly_rmsnorm", "bfly_rmsnorm_backward",
+    "bfly_rmsnorm_backward_workspace_bytes", "bfly_lora_matmul",
+    "bfly_lora_matmul_workspace_bytes", "bfly_grad_clip", "bfly_grad_clip_workspace_bytes",
 ]
 
 BFLY_F32 = 0
 BFLY_BF16 = 1
 BFLY_SYM_ABSMAX = 0
 BFLY_ASYM_MINMAX = 1
+BFLY_Q8_INT8 = 0
+BFLY_Q8_E4M3 = 1
 
 STATUS_NAMES = {0: "BFLY_OK", 1: "BFLY_ERR_NULL", 2: "BFLY_ERR_SIZE", 3: "BFLY_ERR_DTYPE",
                 4: "BFLY_ERR_ALIGN", 5: "BFLY_ERR_QUANT", 6: "BFLY_ERR_WORKSPACE",
@@ -99,7 +104,22 @@ def lib():
         L.bfly_status_string.restype = ctypes.c_char_p
         L.bfly_last_hip_error.restype = i32
         L.bfly_time_next_forward.argtypes = [vp, vp]
-        for f in (L.bfly_prepare, L.bfly_prepare_hadamard, L.bfly_forward, L.bfly_forward_quant,
+        ci, f32 = ctypes.c_int, ctypes.c_float
+        L.bfly_rmsnorm.argtypes = [vp, ci, vp, vp, vp, ci, vp, ci, vp, vp, vp, i64, i32, f32, ci,
+                                   i32, vp]
+        L.bfly_rmsnorm_backward.argtypes = [vp, ci, vp, ci, vp, vp, vp, vp, ci, vp, i64, i32, vp,
+                                            sz, vp]
+        L.bfly_rmsnorm_backward_workspace_bytes.argtypes = [i64, i32]
+        L.bfly_rmsnorm_backward_workspace_bytes.restype = sz
+        L.bfly_lora_matmul.argtypes = [vp, ci, vp, vp, vp, vp, vp, ci, vp, ci, i64, i32, i32, i32,
+                                       i32, vp, sz, vp]
+        L.bfly_lora_matmul_workspace_bytes.argtypes = [i64, i32, i32, i32]
+        L.bfly_lora_matmul_workspace_bytes.restype = sz
+        L.bfly_grad_clip.argtypes = [i32, vp, vp, vp, vp, f32, vp, vp, sz, vp]
+        L.bfly_grad_clip_workspace_bytes.argtypes = [i32]
+        L.bfly_grad_clip_workspace_bytes.restype = sz
+        for f in (L.bfly_rmsnorm, L.bfly_rmsnorm_backward, L.bfly_lora_matmul, L.bfly_grad_clip,
+                  L.bfly_prepare, L.bfly_prepare_hadamard, L.bfly_forward, L.bfly_forward_quant,
                   L.bfly_forward_quant_noalloc,
                   L.bfly_kron_forward, L.bfly_kron_forward_wide, L.bfly_quant_matmul,
                   L.bfly_backward,
@@ -159,6 +179,40 @@ def _check(status, where):
 
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
+
+
+def _scratch(device, workspace):
+    """A workspace (None: not given) is contiguous and lies on `device`."""
+    if workspace is not None and (workspace.get_device() != device or
+                                  not workspace.is_contiguous()):
+        raise ValueError("the workspace has to be contiguous and on the first argument's device")
+
+
+def _on(device, stream, call):
+    """call(stream handle) with `device` current: the caller's stream, or
+    torch's current one of that device."""
+    import torch
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return call(_stream(stream))
+    return call(_stream(stream))
+
+
+def _expect(device, **tensors):
+    """Every tensor (None: not given) has its shape, is contiguous and lies on
+    the GPU `device`.  tensors: name=(tensor, shape, dtypes)."""
+    if device < 0:
+        raise ValueError("the tensors have to be on a GPU")
+    for name, (t, shape, dtypes) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype not in dtypes:
+            raise TypeError("%s is %s" % (name, t.dtype))
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError("%s has to be contiguous of shape %s, got %s with strides %s"
+                             % (name, tuple(shape), tuple(t.shape), t.stride()))
+        if t.get_device() != device:
+            raise ValueError("%s is on another device than the first argument" % name)
 
 
 def _table_ws(n, theta, coeffs, workspace, like):
@@ -346,3 +400,128 @@ def bfly_calib_step_weight(x, w, theta, adam_m, adam_v, step: int, cfg: bfly_cal
                                         _ptr(loss), _ptr(workspace),
                                         workspace.numel() * workspace.element_size(),
                                         _stream(stream)), "bfly_calib_step_weight")
+
+
+# ---------------------------------------------------------------------------
+# the norm in front of a layer, adapters beside its product, clipping
+# ---------------------------------------------------------------------------
+
+def _row_types():
+    import torch
+    return torch.float32, torch.bfloat16
+
+
+def _one_byte():
+    import torch
+    return torch.int8, torch.uint8, torch.float8_e4m3fn
+
+
+def bfly_rmsnorm(x, weight, eps, y=None, codes=None, scales=None, residual=None, h=None, rstd=None,
+                 format=BFLY_Q8_INT8, group=None, stream=None) -> None:
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight per row, and y
+    in 8 bits.  x, residual, h: [rows, n] of one type; y: [rows, n] float32 or
+    bfloat16; codes: [rows, n] of one byte an element with scales [rows,
+    n/group] float16 (group None: one scale per row); rstd: [rows] float32;
+    weight: [n] or None (ones).  Outputs that are None are not computed."""
+    import torch
+    rows, n = x.shape
+    if group is None or codes is None:
+        group = n
+    f = _row_types()
+    dev = x.get_device()
+    _expect(dev, x=(x, (rows, n), f), residual=(residual, (rows, n), (x.dtype,)),
+            h=(h, (rows, n), (x.dtype,)), weight=(weight, (n,), f), y=(y, (rows, n), f),
+            codes=(codes, (rows, n), _one_byte()),
+            scales=(scales, (rows, n // group if group > 0 else 0), (torch.float16,)),
+            rstd=(rstd, (rows,), (torch.float32,)))
+    _check(_on(dev, stream, lambda s: lib().bfly_rmsnorm(
+        _ptr(x), _dt(x), _ptr(residual), _ptr(h), _ptr(weight),
+        0 if weight is None else _dt(weight), _ptr(y), 0 if y is None else _dt(y), _ptr(codes),
+        _ptr(scales), _ptr(rstd), rows, n, eps, format, group, s)), "bfly_rmsnorm")
+
+
+def bfly_rmsnorm_backward_workspace_bytes(rows: int, n: int) -> int:
+    return lib().bfly_rmsnorm_backward_workspace_bytes(rows, n)
+
+
+def bfly_rmsnorm_backward(h, weight, rstd, dy, dx, dweight=None, dh=None, workspace=None,
+                          stream=None) -> None:
+    """dx = dh + dL/dh of y = h rstd weight, dweight = sum over rows of its
+    gradient.  h: [rows, n]; dy, dh, dx: [rows, n] of one type; rstd: [rows]
+    and dweight: [n] float32; workspace: a uint8 tensor of
+    bfly_rmsnorm_backward_workspace_bytes (needed with dweight)."""
+    import torch
+    rows, n = h.shape
+    f = _row_types()
+    dev = h.get_device()
+    _expect(dev, h=(h, (rows, n), f), weight=(weight, (n,), f),
+            rstd=(rstd, (rows,), (torch.float32,)), dy=(dy, (rows, n), f),
+            dx=(dx, (rows, n), (dy.dtype,)), dh=(dh, (rows, n), (dy.dtype,)),
+            dweight=(dweight, (n,), (torch.float32,)))
+    _scratch(dev, workspace)
+    _check(_on(dev, stream, lambda s: lib().bfly_rmsnorm_backward(
+        _ptr(h), _dt(h), _ptr(weight), 0 if weight is None else _dt(weight), _ptr(rstd), _ptr(dy),
+        _ptr(dh), _ptr(dx), _dt(dy), _ptr(dweight), rows, n, _ptr(workspace), _nbytes(workspace),
+        s)), "bfly_rmsnorm_backward")
+
+
+def bfly_lora_matmul_workspace_bytes(rows: int, n_out: int, k: int, rank: int) -> int:
+    return lib().bfly_lora_matmul_workspace_bytes(rows, n_out, k, rank)
+
+
+def bfly_lora_matmul(x, ids, lora_a, lora_b, scaling, y, workspace, base=None,
+                     stream=None) -> None:
+    """y = base + scaling[id] * lora_b[id] (lora_a[id] x) per row, id = ids[row]
+    (outside [0, adapters): y = base).  x: [rows, k] bfloat16; ids: [rows]
+    int32; lora_a: [adapters, rank, k], lora_b: [adapters, n_out, rank]
+    bfloat16; scaling: [adapters] float32; base, y: [rows, n_out] float32 or
+    bfloat16 (base None: zeros; y may be base); workspace: a uint8 tensor of
+    bfly_lora_matmul_workspace_bytes."""
+    import torch
+    rows, k = x.shape
+    num, rank = lora_a.shape[:2]
+    n_out = y.shape[1]
+    f, bf = _row_types(), (torch.bfloat16,)
+    dev = x.get_device()
+    _expect(dev, x=(x, (rows, k), bf), ids=(ids, (rows,), (torch.int32,)),
+            lora_a=(lora_a, (num, rank, k), bf), lora_b=(lora_b, (num, n_out, rank), bf),
+            scaling=(scaling, (num,), (torch.float32,)), base=(base, (rows, n_out), f),
+            y=(y, (rows, n_out), f))
+    _scratch(dev, workspace)
+    _check(_on(dev, stream, lambda s: lib().bfly_lora_matmul(
+        _ptr(x), BFLY_BF16, _ptr(ids), _ptr(lora_a), _ptr(lora_b), _ptr(scaling), _ptr(base),
+        0 if base is None else _dt(base), _ptr(y), _dt(y), rows, n_out, k, num, rank,
+        _ptr(workspace), _nbytes(workspace), s)), "bfly_lora_matmul")
+
+
+def bfly_grad_clip_workspace_bytes(count: int) -> int:
+    return lib().bfly_grad_clip_workspace_bytes(count)
+
+
+def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> None:
+    """norm[0] = the 2-norm over all tensors of `grads` (a list; contiguous
+    float32 or bfloat16 of any shape), norm[1] = min(1, max_norm / norm[0]),
+    and every gradient times norm[1], in place or into `outs`.  norm: [2]
+    float32; workspace: a uint8 tensor of bfly_grad_clip_workspace_bytes."""
+    import torch
+    dev = norm.get_device()
+    _expect(dev, norm=(norm, (2,), (torch.float32,)))
+    _scratch(dev, workspace)
+    num = len(grads)
+    if outs is not None and len(outs) != num:
+        raise ValueError("%d gradients and %d outputs" % (num, len(outs)))
+    for i, t in enumerate(grads):
+        if not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError("gradient %d has to be contiguous and on norm's device" % i)
+        if outs is not None:
+            o = outs[i]
+            if o.dtype != t.dtype or o.numel() != t.numel() or not o.is_contiguous() or \
+                    o.get_device() != dev:
+                raise ValueError("output %d has to be like its gradient" % i)
+    ptrs = ctypes.c_void_p * num
+    _check(_on(dev, stream, lambda s: lib().bfly_grad_clip(
+        num, ptrs(*[t.data_ptr() for t in grads]),
+        None if outs is None else ptrs(*[t.data_ptr() for t in outs]),
+        (ctypes.c_int64 * num)(*[t.numel() for t in grads]),
+        (ctypes.c_int32 * num)(*[_dt(t) for t in grads]), max_norm, _ptr(norm), _ptr(workspace),
+        _nbytes(workspace), s)), "bfly_grad_clip")

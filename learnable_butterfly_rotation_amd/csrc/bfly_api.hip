@@ -12,6 +12,9 @@
 #include "bfly_common.h"
 #include "bfly_calib.h"
 #include "bfly_calib_w.h"
+#include "bfly_clip.h"
+#include "bfly_lora.h"
+#include "bfly_norm.h"
 #include "bfly_qgemm.h"
 
 namespace bfly {
@@ -923,6 +926,188 @@ bfly_status bfly_forward_quant_noalloc(const void* x, bfly_dtype x_dt, void* y, 
   const hipError_t e = scratch_address(&table);
   if (e != hipSuccess) return hip_fail(e);
   return forward_run(p, theta, nullptr, table, (hipStream_t)hip_stream);
+}
+
+// The sizes that both norm calls share.
+static bfly_status norm_sizes(int64_t rows, int32_t n) {
+  if (rows < 0 || n < 1) return BFLY_ERR_SIZE;
+  if (n > bfly::kNormMaxN || !rows_fit(rows, n)) return BFLY_ERR_UNSUPPORTED;
+  return BFLY_OK;
+}
+
+bfly_status bfly_rmsnorm(const void* x, bfly_dtype x_dt, const void* residual, void* h,
+                         const void* weight, bfly_dtype w_dt, void* y, bfly_dtype y_dt,
+                         uint8_t* codes, uint16_t* scales, float* rstd, int64_t rows, int32_t n,
+                         float eps, bfly_q8 format, int32_t group, void* hip_stream) {
+  if (rows > 0) {
+    if (!x || (h && !residual) || (!codes != !scales)) return BFLY_ERR_NULL;
+    if (!h && !y && !codes && !rstd) return BFLY_ERR_NULL;
+  }
+  if (!dtype_ok(x_dt) || (weight && !dtype_ok(w_dt)) || (y && !dtype_ok(y_dt)))
+    return BFLY_ERR_DTYPE;
+  const bfly_status st = norm_sizes(rows, n);
+  if (st != BFLY_OK) return st;
+  if (!(eps > 0.f) || eps > 3.4e38f) return BFLY_ERR_SIZE;
+  if (codes) {
+    if (format != BFLY_Q8_INT8 && format != BFLY_Q8_E4M3) return BFLY_ERR_QUANT;
+    const int lg = log2_pow2(group);
+    if (group != n && (lg < 3 || lg > 9 || n % group != 0)) return BFLY_ERR_QUANT;
+  }
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(h, 16) || !aligned(weight, 16) ||
+      !aligned(y, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(rstd, 4))
+    return BFLY_ERR_ALIGN;
+  if (rows == 0) return BFLY_OK;
+  bfly::NormParams p;
+  p.x = x;
+  p.residual = residual;
+  p.h = h;
+  p.weight = weight;
+  p.y = y;
+  p.codes = codes;
+  p.scales = scales;
+  p.rstd = rstd;
+  p.rows = rows;
+  p.n = n;
+  p.group = codes ? group : n;
+  p.x_bf16 = x_dt == BFLY_BF16;
+  p.w_bf16 = weight && w_dt == BFLY_BF16;
+  p.y_bf16 = y && y_dt == BFLY_BF16;
+  p.e4m3 = codes && format == BFLY_Q8_E4M3;
+  p.eps = eps;
+  const hipError_t e = bfly::launch_rmsnorm(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? BFLY_OK : hip_fail(e);
+}
+
+size_t bfly_rmsnorm_backward_workspace_bytes(int64_t rows, int32_t n) {
+  if (norm_sizes(rows, n) != BFLY_OK) return 0;
+  return (size_t)bfly::rmsnorm_bwd_slots(rows, n) * (size_t)n * sizeof(float);
+}
+
+bfly_status bfly_rmsnorm_backward(const void* h, bfly_dtype h_dt, const void* weight,
+                                  bfly_dtype w_dt, const float* rstd, const void* dy,
+                                  const void* dh, void* dx, bfly_dtype g_dt, float* dweight,
+                                  int64_t rows, int32_t n, void* workspace,
+                                  size_t workspace_bytes, void* hip_stream) {
+  if (rows > 0 && (!h || !rstd || !dy || !dx || (dweight && !workspace))) return BFLY_ERR_NULL;
+  if (!dtype_ok(h_dt) || !dtype_ok(g_dt) || (weight && !dtype_ok(w_dt))) return BFLY_ERR_DTYPE;
+  const bfly_status st = norm_sizes(rows, n);
+  if (st != BFLY_OK) return st;
+  if (dweight && workspace_bytes < bfly_rmsnorm_backward_workspace_bytes(rows, n))
+    return BFLY_ERR_WORKSPACE;
+  if (!aligned(h, 16) || !aligned(weight, 16) || !aligned(rstd, 4) || !aligned(dy, 16) ||
+      !aligned(dh, 16) || !aligned(dx, 16) || !aligned(dweight, 4) ||
+      (dweight && !aligned(workspace, 16)))
+    return BFLY_ERR_ALIGN;
+  if (rows == 0 && !dweight) return BFLY_OK;
+  bfly::NormBwdParams p;
+  p.h = h;
+  p.weight = weight;
+  p.rstd = rstd;
+  p.dy = dy;
+  p.dh = dh;
+  p.dx = dx;
+  p.dweight = dweight;
+  p.partials = static_cast<float*>(workspace);
+  p.rows = rows;
+  p.n = n;
+  p.h_bf16 = h_dt == BFLY_BF16;
+  p.w_bf16 = weight && w_dt == BFLY_BF16;
+  p.g_bf16 = g_dt == BFLY_BF16;
+  const hipError_t e = bfly::launch_rmsnorm_backward(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? BFLY_OK : hip_fail(e);
+}
+
+static bfly_status lora_sizes(int64_t rows, int32_t n_out, int32_t k, int32_t rank) {
+  if (rows < 0 || n_out < 1 || k < 1 || rank < 1) return BFLY_ERR_SIZE;
+  if (n_out % 8 != 0 || k % 8 != 0 || rank % 8 != 0 || n_out > (1 << 20) || k > 65536 ||
+      rank > bfly::kLoraMaxRank || rows > (int64_t(1) << 23))
+    return BFLY_ERR_UNSUPPORTED;
+  return BFLY_OK;
+}
+
+size_t bfly_lora_matmul_workspace_bytes(int64_t rows, int32_t n_out, int32_t k, int32_t rank) {
+  if (lora_sizes(rows, n_out, k, rank) != BFLY_OK || rows == 0) return 0;
+  return bfly::lora_workspace_bytes(rows, k, rank);
+}
+
+bfly_status bfly_lora_matmul(const void* x, bfly_dtype x_dt, const int32_t* ids,
+                             const void* lora_a, const void* lora_b, const float* scaling,
+                             const void* base, bfly_dtype base_dt, void* y, bfly_dtype y_dt,
+                             int64_t rows, int32_t n_out, int32_t k, int32_t n_adapters,
+                             int32_t rank, void* workspace, size_t workspace_bytes,
+                             void* hip_stream) {
+  if (rows > 0 && (!x || !ids || !lora_a || !lora_b || !scaling || !y || !workspace))
+    return BFLY_ERR_NULL;
+  if (x_dt != BFLY_BF16 || !dtype_ok(y_dt) || (base && !dtype_ok(base_dt))) return BFLY_ERR_DTYPE;
+  if (base && base == y && base_dt != y_dt) return BFLY_ERR_DTYPE;
+  if (n_adapters < 1) return BFLY_ERR_SIZE;
+  const bfly_status st = lora_sizes(rows, n_out, k, rank);
+  if (st != BFLY_OK) return st;
+  if (workspace_bytes < bfly_lora_matmul_workspace_bytes(rows, n_out, k, rank))
+    return BFLY_ERR_WORKSPACE;
+  if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(lora_a, 16) || !aligned(lora_b, 16) ||
+      !aligned(scaling, 4) || !aligned(base, 16) || !aligned(y, 16) || !aligned(workspace, 16))
+    return BFLY_ERR_ALIGN;
+  if (rows == 0) return BFLY_OK;
+  bfly::LoraParams p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.ids = ids;
+  p.a = static_cast<const uint16_t*>(lora_a);
+  p.b = static_cast<const uint16_t*>(lora_b);
+  p.scaling = scaling;
+  p.base = base;
+  p.y = y;
+  p.t = static_cast<float*>(workspace);
+  p.rows = rows;
+  p.n_out = n_out;
+  p.k = k;
+  p.n_adapters = n_adapters;
+  p.rank = rank;
+  p.base_bf16 = base && base_dt == BFLY_BF16;
+  p.y_bf16 = y_dt == BFLY_BF16;
+  const hipError_t e = bfly::launch_lora(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? BFLY_OK : hip_fail(e);
+}
+
+constexpr int32_t kClipMaxTensors = 65536;
+
+size_t bfly_grad_clip_workspace_bytes(int32_t count) {
+  if (count < 0 || count > kClipMaxTensors) return 0;
+  return bfly::clip_workspace_bytes(count);
+}
+
+bfly_status bfly_grad_clip(int32_t count, const void* const* grads, void* const* outs,
+                           const int64_t* numels, const int32_t* dtypes, float max_norm,
+                           float* norm, void* workspace, size_t workspace_bytes,
+                           void* hip_stream) {
+  if (count < 0 || !(max_norm > 0.f)) return BFLY_ERR_SIZE;
+  if (!norm || !workspace || (count > 0 && (!grads || !numels || !dtypes))) return BFLY_ERR_NULL;
+  if (count > kClipMaxTensors) return BFLY_ERR_UNSUPPORTED;
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (numels[i] < 0) return BFLY_ERR_SIZE;
+    if (!dtype_ok(dtypes[i])) return BFLY_ERR_DTYPE;
+    if (numels[i] == 0) continue;
+    const void* out = outs ? outs[i] : grads[i];
+    if (!grads[i] || !out) return BFLY_ERR_NULL;
+    const uintptr_t es = dtypes[i] == BFLY_BF16 ? 2 : 4;
+    if (!aligned(grads[i], es) || !aligned(out, es)) return BFLY_ERR_ALIGN;
+    if (numels[i] >= (int64_t(1) << 42) || (total += numels[i]) >= (int64_t(1) << 42))
+      return BFLY_ERR_UNSUPPORTED;
+  }
+  if (workspace_bytes < bfly_grad_clip_workspace_bytes(count)) return BFLY_ERR_WORKSPACE;
+  if (!aligned(norm, 4) || !aligned(workspace, 16)) return BFLY_ERR_ALIGN;
+  bfly::ClipParams p;
+  p.count = count;
+  p.in = grads;
+  p.out = outs ? outs : (void* const*)grads;
+  p.numel = numels;
+  p.dtype = dtypes;
+  p.max_norm = max_norm;
+  p.norm = norm;
+  p.workspace = workspace;
+  const hipError_t e = bfly::launch_grad_clip(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? BFLY_OK : hip_fail(e);
 }
 
 const char* bfly_status_string(bfly_status s) {

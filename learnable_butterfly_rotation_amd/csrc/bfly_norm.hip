@@ -1,0 +1,412 @@
+// Root-mean-square norm of rows, with the residual's addition in front and
+// the round-to-nearest group quantizer at 8 bits behind, and its gradient.
+//
+//   h = x + residual (rounded to x's type)
+//   rstd = (mean_i h_i^2 + eps)^(-1/2),  y_i = (h_i rstd) w_i
+//   scale = fp16(max |y| / top) over a group, code_i = rnd(y_i / scale)
+//
+// One pass: a row stays in the registers of the threads that own it (64, 256
+// or 1024 of them, eight elements a chunk) from its load to its last store.
+#include "bfly_norm.h"
+#include "bfly_rows.h"
+
+#include <type_traits>
+
+namespace bfly {
+namespace {
+
+// rstd from the mean square, in fp64: the hardware's reciprocal square root
+// and two Newton steps (each squares the relative error), so that the fp32
+// value is the correctly rounded one but for ties and the codes next to a
+// rounding border do not depend on the order of the sum.
+__device__ __forceinline__ float inv_sqrt(double m) {
+  double r = __builtin_amdgcn_rsq(m);
+  r = r * fma(-0.5 * m * r, r, 1.5);
+  r = r * fma(-0.5 * m * r, r, 1.5);
+  return m == __builtin_inf() ? 0.f : (float)r;
+}
+
+// Sum (or maximum) over the T threads of a row from each wave's value.  One
+// barrier: the caller alternates between two buffers, so that a wave still
+// reading one is never overtaken by a wave that writes it again.
+template <int T, typename F>
+__device__ __forceinline__ F block_sum(F v, F* buf, int t) {
+  if constexpr (T == 64) return v;
+  if ((t & 63) == 0) buf[t >> 6] = v;
+  __syncthreads();
+  F s = buf[0];
+#pragma unroll
+  for (int i = 1; i < T / 64; ++i) s += buf[i];
+  return s;
+}
+template <int T>
+__device__ __forceinline__ float block_max(float v, float* buf, int t) {
+  if constexpr (T == 64) return v;
+  if ((t & 63) == 0) buf[t >> 6] = v;
+  __syncthreads();
+  float s = buf[0];
+#pragma unroll
+  for (int i = 1; i < T / 64; ++i) s = fmaxf(s, buf[i]);
+  return s;
+}
+
+// fp16(amax / top), saturated at the largest fp16 value.
+__device__ __forceinline__ _Float16 group_scale(float amax, float top) {
+  return (_Float16)fminf(amax / top, 65504.f);
+}
+
+// The codes of eight values, four to a word (d = the group's scale, 0: codes 0).
+template <bool E4M3>
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float d) {
+  constexpr float top = E4M3 ? 448.f : 127.f;
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = d > 0.f ? fminf(fmaxf(y[e] / d, -top), top) : 0.f;
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (E4M3) {
+      int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
+      w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], v, true);
+    } else {
+      w[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[i] |= ((uint32_t)(int)rintf(q[4 * i + e]) & 0xFFu) << (8 * e);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// T threads to a row, V chunks of eight elements to a thread; VEC: n is a
+// multiple of 8 (RowIo).  Q: 0 no codes, 1 int8, 2 e4m3.
+template <int T, int V, bool VEC, bool XB, int Q>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
+  constexpr int RPB = T < 256 ? 256 / T : 1;  // rows a workgroup works on at once
+  __shared__ double sums[2][T / 64];
+  __shared__ float tops[2][T / 64];
+  using X = RowIo<T, VEC, XB>;
+  const int t = threadIdx.x & (T - 1);
+  const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / T);
+  const int n = P.n;
+  const double inv_n = 1.0 / n;
+  constexpr int es = XB ? 2 : 4;
+
+  float w[V][8];
+  {
+    const __amdgpu_buffer_rsrc_t rw = row_range(P.weight, 0, n, P.w_bf16 ? 2 : 4);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!P.weight) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[v][e] = 1.f;
+      } else if (P.w_bf16) {
+        RowIo<T, VEC, true>::unpack(RowIo<T, VEC, true>::load(rw, t, v), w[v]);
+      } else {
+        RowIo<T, VEC, false>::unpack(RowIo<T, VEC, false>::load(rw, t, v), w[v]);
+      }
+    }
+  }
+
+  int turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < P.rows;
+       row0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const int64_t row = row0 + sub;
+    if (row >= P.rows) break;  // only rows of one wave (T = 64): no barrier is missed
+    const __amdgpu_buffer_rsrc_t rx = row_range(P.x, row, n, es);
+    const __amdgpu_buffer_rsrc_t rr = row_range(P.residual, row, n, es);
+    typename X::Raw qx[V], qr[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) qx[v] = X::load(rx, t, v);
+    if (P.residual) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) qr[v] = X::load(rr, t, v);
+    }
+    float h[V][8];
+    if (P.residual) {
+      const __amdgpu_buffer_rsrc_t rh = row_range(P.h, row, n, es);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float a[8], b[8];
+        X::unpack(qx[v], a);
+        X::unpack(qr[v], b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += b[e];
+        const typename X::Raw q = X::pack(a);
+        if (P.h) X::store(rh, t, v, q);
+        X::unpack(q, h[v]);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) X::unpack(qx[v], h[v]);
+    }
+    double ss = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fma((double)h[v][e], (double)h[v][e], ss);
+    ss = block_sum<T>(wave_sum(ss), sums[turn], t);
+    const float rstd = inv_sqrt(fma(ss, inv_n, (double)P.eps));
+    if (P.rstd && t == 0) P.rstd[row] = rstd;
+    float top = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[v][e] = (h[v][e] * rstd) * w[v][e];
+    if (P.y) {
+      if (P.y_bf16) {
+        const __amdgpu_buffer_rsrc_t ry = row_range(P.y, row, n, 2);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          RowIo<T, VEC, true>::store(ry, t, v, RowIo<T, VEC, true>::pack(h[v]));
+      } else {
+        const __amdgpu_buffer_rsrc_t ry = row_range(P.y, row, n, 4);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          RowIo<T, VEC, false>::store(ry, t, v, RowIo<T, VEC, false>::pack(h[v]));
+      }
+    }
+    if constexpr (Q != 0) {
+      constexpr float qtop = Q == 2 ? 448.f : 127.f;
+      const __amdgpu_buffer_rsrc_t rc = row_range(P.codes, row, n, 1);
+      const int per_row = n / P.group;
+      uint16_t* const sc = P.scales + row * per_row;
+      float d = 0.f;
+      if (P.group == n) {  // one scale for the row
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(h[v][e]));
+        top = block_max<T>(run_max(top, 64), tops[turn], t);
+        const _Float16 s = group_scale(top, qtop);
+        d = (float)s;
+        if (t == 0) sc[0] = __builtin_bit_cast(uint16_t, s);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (VEC && P.group != n) {  // a run of group / 8 lanes shares a scale
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[v][e]));
+          m = run_max(m, P.group >> 3);
+          const _Float16 s = group_scale(m, qtop);
+          d = (float)s;
+          const int i = X::index(t, v, 0);
+          if (i < n && (i & (P.group - 1)) == 0)
+            sc[i / P.group] = __builtin_bit_cast(uint16_t, s);
+        }
+        const uint2 c = codes8<Q == 2>(h[v], d);
+        if constexpr (VEC) {
+          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+          const u32x2 cw = {c.x, c.y};
+          __builtin_amdgcn_raw_buffer_store_b64(cw, rc, (v * T + t) * 8, 0, 0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            __builtin_amdgcn_raw_buffer_store_b8(
+                (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3))), rc, X::index(t, v, e), 0, 0);
+        }
+      }
+    }
+  }
+}
+
+// ---- gradient --------------------------------------------------------------
+//
+//   g = dy w,  dx = (g - xhat mean(g xhat)) rstd + dh,  xhat = h rstd
+//   dw = sum over rows of dy xhat
+// Workgroup b takes row groups b, b + slots, ...; each thread sums dw of its
+// columns over them in fp32 and writes one row of `partials`, which
+// norm_dw_kernel adds up in a fixed order.
+template <int T, int V, bool VEC, bool HB, bool GB>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdParams P) {
+  constexpr int RPB = T < 256 ? 256 / T : 1;
+  __shared__ float sums[2][T / 64];
+  using H = RowIo<T, VEC, HB>;
+  using G = RowIo<T, VEC, GB>;
+  const int t = threadIdx.x & (T - 1);
+  const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / T);
+  const int n = P.n;
+  const float inv_n = 1.f / (float)n;
+
+  float w[V][8], dw[V][8];
+  {
+    const __amdgpu_buffer_rsrc_t rw = row_range(P.weight, 0, n, P.w_bf16 ? 2 : 4);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (!P.weight) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[v][e] = 1.f;
+      } else if (P.w_bf16) {
+        RowIo<T, VEC, true>::unpack(RowIo<T, VEC, true>::load(rw, t, v), w[v]);
+      } else {
+        RowIo<T, VEC, false>::unpack(RowIo<T, VEC, false>::load(rw, t, v), w[v]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[v][e] = 0.f;
+    }
+  }
+
+  int turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < P.rows;
+       row0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
+    const int64_t row = row0 + sub;
+    if (row >= P.rows) break;  // only rows of one wave (T = 64): no barrier is missed
+    const __amdgpu_buffer_rsrc_t rh = row_range(P.h, row, n, HB ? 2 : 4);
+    const __amdgpu_buffer_rsrc_t rg = row_range(P.dy, row, n, GB ? 2 : 4);
+    const __amdgpu_buffer_rsrc_t rd = row_range(P.dh, row, n, GB ? 2 : 4);
+    typename H::Raw qh[V];
+    typename G::Raw qg[V], qd[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) qh[v] = H::load(rh, t, v);
+#pragma unroll
+    for (int v = 0; v < V; ++v) qg[v] = G::load(rg, t, v);
+    if (P.dh) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) qd[v] = G::load(rd, t, v);
+    }
+    const float rstd = P.rstd[row];
+    float c = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float h[8], g[8];
+      H::unpack(qh[v], h);
+      G::unpack(qg[v], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = g[e] * (h[e] * rstd);
+        dw[v][e] += a;
+        c = fmaf(a, w[v][e], c);
+      }
+    }
+    c = block_sum<T>(wave_sum(c), sums[turn], t) * inv_n;
+    const __amdgpu_buffer_rsrc_t ro = row_range(P.dx, row, n, GB ? 2 : 4);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float h[8], g[8], d[8];
+      H::unpack(qh[v], h);
+      G::unpack(qg[v], g);
+      if (P.dh) {
+        G::unpack(qd[v], d);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        d[e] = fmaf(fmaf(-c, h[e] * rstd, g[e] * w[v][e]), rstd, d[e]);
+      G::store(ro, t, v, G::pack(d));
+    }
+  }
+
+  if (!P.dweight) return;
+  const __amdgpu_buffer_rsrc_t rp = row_range(P.partials, blockIdx.x, n, 4);
+  if constexpr (RPB > 1) {  // the rows of a workgroup's waves, added in order
+    __shared__ float all[RPB][V * 8][64];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) all[sub][v * 8 + e][t] = dw[v][e];
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int s = 1; s < RPB; ++s) dw[v][e] += all[s][v * 8 + e][t];
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    RowIo<T, VEC, false>::store(rp, t, v, RowIo<T, VEC, false>::pack(dw[v]));
+}
+
+// dweight[i] = sum over slots of partials[slot][i]: 16 columns to a workgroup
+// of 256 threads, each adding every 16th slot, then the 16 sums in order.
+constexpr int kDwCols = 16, kDwWays = 16;
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* partials, float* dweight,
+                                                      int slots, int n) {
+  __shared__ float part[kDwWays][kDwCols];
+  const int c = threadIdx.x % kDwCols, k = threadIdx.x / kDwCols;
+  const int i = blockIdx.x * kDwCols + c;
+  float s = 0.f;
+  if (i < n)
+    for (int j = k; j < slots; j += kDwWays) s += partials[(int64_t)j * n + i];
+  part[k][c] = s;
+  __syncthreads();
+  if (k == 0 && i < n) {
+#pragma unroll
+    for (int j = 1; j < kDwWays; ++j) s += part[j][c];
+    dweight[i] = s;
+  }
+}
+
+// Threads and chunks to a row: the fewest threads that hold it.
+template <typename F>
+hipError_t by_width(int n, F f) {
+  if (n <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  if (n <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (n <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+  if (n <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  if (n <= 8192) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
+  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+}
+int rows_per_block(int n) { return n <= 1024 ? 4 : 1; }
+
+constexpr int64_t kNormBlocks = 2048;  // workgroups of a forward launch at most
+constexpr int64_t kNormBwdSlots = 1024;
+
+template <bool VEC, bool XB, int Q>
+hipError_t norm_run(const NormParams& p, hipStream_t s) {
+  return by_width(p.n, [&](auto T, auto V) {
+    const int64_t need = (p.rows + rows_per_block(p.n) - 1) / rows_per_block(p.n);
+    const int grid = (int)(need < kNormBlocks ? need : kNormBlocks);
+    hipLaunchKernelGGL((norm_kernel<T(), V(), VEC, XB, Q>), dim3(grid),
+                       dim3(T() < 256 ? 256 : T()), 0, s, p);
+    return hipGetLastError();
+  });
+}
+
+template <bool VEC, bool HB, bool GB>
+hipError_t norm_bwd_run(const NormBwdParams& p, hipStream_t s) {
+  return by_width(p.n, [&](auto T, auto V) {
+    hipLaunchKernelGGL((norm_bwd_kernel<T(), V(), VEC, HB, GB>),
+                       dim3(rmsnorm_bwd_slots(p.rows, p.n)), dim3(T() < 256 ? 256 : T()), 0, s, p);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+int rmsnorm_bwd_slots(int64_t rows, int n) {
+  const int64_t need = (rows + rows_per_block(n) - 1) / rows_per_block(n);
+  return (int)(need < kNormBwdSlots ? need : kNormBwdSlots);
+}
+
+hipError_t launch_rmsnorm(const NormParams& p, hipStream_t s) {
+  const int q = !p.codes ? 0 : p.e4m3 ? 2 : 1;
+  const bool vec = p.n % 8 == 0;
+#define BFLY_NORM(VEC, XB)                                    \
+  (q == 0   ? norm_run<VEC, XB, 0>(p, s)                      \
+   : q == 1 ? norm_run<VEC, XB, 1>(p, s)                      \
+            : norm_run<VEC, XB, 2>(p, s))
+  return vec ? (p.x_bf16 ? BFLY_NORM(true, true) : BFLY_NORM(true, false))
+             : (p.x_bf16 ? BFLY_NORM(false, true) : BFLY_NORM(false, false));
+#undef BFLY_NORM
+}
+
+hipError_t launch_rmsnorm_backward(const NormBwdParams& p, hipStream_t s) {
+  const bool vec = p.n % 8 == 0;
+  hipError_t e = hipSuccess;
+#define BFLY_NORM_BWD(HB, GB) (vec ? norm_bwd_run<true, HB, GB>(p, s) : norm_bwd_run<false, HB, GB>(p, s))
+  if (p.rows > 0)
+    e = p.h_bf16 ? (p.g_bf16 ? BFLY_NORM_BWD(true, true) : BFLY_NORM_BWD(true, false))
+                 : (p.g_bf16 ? BFLY_NORM_BWD(false, true) : BFLY_NORM_BWD(false, false));
+#undef BFLY_NORM_BWD
+  if (e != hipSuccess || !p.dweight) return e;
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((p.n + kDwCols - 1) / kDwCols), dim3(256), 0, s,
+                     p.partials, p.dweight, rmsnorm_bwd_slots(p.rows, p.n), p.n);
+  return hipGetLastError();
+}
+
+}  // namespace bfly

@@ -1,0 +1,130 @@
+"""bfly_grad_clip on the GPU.  The sum of squares is held in fp64 (2^-52 a
+rounding, at most a few thousand of them), so the norm and the factor are the
+fp64 values rounded to fp32: 2^-24 relative, and one part in 10^6 of that for
+the sum.  A scaled gradient is one fp32 product and one rounding to its type:
+with the kernel's factor numpy reproduces its bits."""
+import numpy as np
+import pytest
+
+import learnable_butterfly_rotation_amd as B
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+F32, BF16 = torch.float32, torch.bfloat16
+TOL = 2.0 ** -24 * (1 + 1e-6)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def workspace(count):
+    return torch.full((B.bfly_grad_clip_workspace_bytes(count),), 0x7F, dtype=torch.uint8,
+                      device="cuda")
+
+
+def tensors(seed, sizes, dtypes, scale=1e-2):
+    g = torch.Generator().manual_seed(seed)
+    return [(torch.randn(n, generator=g) * scale).to(dtypes[i % len(dtypes)])
+            for i, n in enumerate(sizes)]
+
+
+def check(grads, max_norm, in_place, on_gpu=None):
+    dev = on_gpu or [g.cuda() for g in grads]
+    before = [g.cpu() for g in dev]
+    outs = None if in_place else [torch.full_like(g, 7.0) for g in dev]
+    norm, ws = torch.full((2,), 7.0, device="cuda"), workspace(len(dev))
+    B.bfly_grad_clip(dev, max_norm, norm, ws, outs=outs)
+    torch.cuda.synchronize()
+    want = float(np.sqrt(sum(float((g.double() ** 2).sum()) for g in before)))
+    got, factor = (float(v) for v in norm.cpu())
+    assert abs(got - want) <= TOL * want
+    # the call takes max_norm as fp32: 0.01 is 0.00999999977..., 2.2e-8 below, and
+    # that value is what the formula divides
+    most = float(np.float32(max_norm))
+    f64 = most / want if want > most else 1.0
+    assert abs(factor - f64) <= TOL * f64
+    for g, o in zip(before, dev if in_place else outs):
+        assert torch.equal(o.cpu(), (g.float() * np.float32(factor)).to(g.dtype))
+    if not in_place:
+        for g, d in zip(before, dev):
+            assert torch.equal(g, d.cpu())
+
+
+SIZES = [[1], [4096], [4097], [1, 1, 1], [3, 4095, 4096, 4097, 8192, 1], [24576] * 40, [5] * 500,
+         [0, 7, 0, 0, 20000, 0], [5000000], [100003] * 70, [1 << 20, 3, 1 << 20]]
+
+
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: "%dx%d" % (len(s), max(s)))
+@pytest.mark.parametrize("dtypes", [(F32,), (BF16,), (F32, BF16)], ids=["f32", "bf16", "mixed"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_clip_sizes(sizes, dtypes, in_place):
+    check(tensors(len(sizes), sizes, dtypes), 0.01, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_clip_below_the_limit(in_place):
+    check(tensors(1, [4096, 100, 9999], (F32, BF16)), 1e4, in_place)
+
+
+@pytest.mark.parametrize("skip", [1, 2, 3, 5])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_clip_views_of_one_buffer(skip, dtype):
+    # tensors that start anywhere in a flat buffer; what lies between stays
+    flat = (torch.randn(60000, generator=torch.Generator().manual_seed(skip)) * 0.1).to(dtype).cuda()
+    cuts = [(skip, 4096), (5001 + skip, 9000), (15000 + skip, 1), (15001 + skip, 30001)]
+    views = [flat[a:a + n] for a, n in cuts]
+    keep = torch.ones(60000, dtype=torch.bool, device="cuda")
+    for a, n in cuts:
+        keep[a:a + n] = False
+    before = flat.clone()
+    check(None, 0.5, True, on_gpu=views)
+    assert torch.equal(before[keep], flat[keep])
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-20, 1e18, 1e30])
+def test_clip_magnitudes(scale):
+    # squares below and above fp32's range
+    check(tensors(2, [5000, 300], (F32,), scale), 1.0, False)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_clip_not_finite(bad):
+    grads = [g.cuda() for g in tensors(3, [5000, 300], (F32, BF16), 10.0)]
+    grads[1][7] = bad
+    before = [g.clone() for g in grads]
+    norm = torch.zeros(2, device="cuda")
+    B.bfly_grad_clip(grads, 1.0, norm, workspace(2))
+    assert not torch.isfinite(norm[0]) and norm[1] == 1.0
+    for a, b in zip(before, grads):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_clip_nothing_and_zeros():
+    norm = torch.full((2,), 7.0, device="cuda")
+    B.bfly_grad_clip([], 1.0, norm, workspace(0))
+    assert norm.tolist() == [0.0, 1.0]
+    g = torch.zeros(100, device="cuda")
+    B.bfly_grad_clip([g], 1.0, norm, workspace(1))
+    assert norm.tolist() == [0.0, 1.0] and (g == 0).all()
+    B.bfly_grad_clip([g + 3], float("inf"), norm, workspace(1))
+    assert norm.tolist() == [30.0, 1.0]
+
+
+def test_clip_same_bits_every_time():
+    grads = [g.cuda() for g in tensors(5, [100003] * 30, (F32,))]
+    norm, ws = torch.empty(2, device="cuda"), workspace(30)
+    outs = [torch.empty_like(g) for g in grads]
+    first = None
+    for _ in range(5):
+        B.bfly_grad_clip(grads, 0.1, norm, ws, outs=outs)
+        v = norm.tolist()
+        first = first or v
+        assert v == first

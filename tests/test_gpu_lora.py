@@ -1,0 +1,183 @@
+"""bfly_lora_matmul on the GPU against the formula in 64 bits.
+
+Tolerance (u = 2^-24): t = A x is a sum of k exact products in fp32, at most
+k + 64 roundings whatever the order; times scaling one more; what the bf16
+terms of s t leave out is at most 2^-16 of it (two terms, bf16 y) or 2^-24
+(three, fp32 y); the second product sums terms * rank exact products; the
+base's addition one rounding; y half a step of its type."""
+import numpy as np
+import pytest
+
+import learnable_butterfly_rotation_amd as B
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+class Case:
+    def __init__(self, rows, k, n_out, rank, num, ids="mixed", base=BF16, y=BF16, seed=0):
+        g = torch.Generator().manual_seed(seed + rows + 7 * k + rank)
+        self.x = torch.randn((rows, k), generator=g).to(BF16)
+        self.a = (torch.randn((num, rank, k), generator=g) / k ** 0.5).to(BF16)
+        self.b = torch.randn((num, n_out, rank), generator=g).to(BF16)
+        self.s = 0.5 + torch.rand(num, generator=g)
+        if isinstance(ids, str):
+            if ids == "mixed":
+                self.ids = torch.randint(-1, num, (rows,), generator=g, dtype=torch.int32)
+            elif ids == "runs":
+                self.ids = torch.sort(torch.randint(0, num, (rows,), generator=g,
+                                                    dtype=torch.int32))[0]
+            else:
+                self.ids = torch.full((rows,), int(ids), dtype=torch.int32)
+        else:
+            self.ids = torch.tensor(ids, dtype=torch.int32)
+        self.base = None if base is None else torch.randn((rows, n_out), generator=g).to(base)
+        self.y_dt, self.num, self.rank = y, num, rank
+
+    def run(self, in_place=False, stream=None):
+        rows, k = self.x.shape
+        n_out = self.b.shape[1]
+        dev = [t.cuda() for t in (self.x, self.ids, self.a, self.b, self.s)]
+        base = None if self.base is None else self.base.cuda()
+        y = base if in_place else torch.full((rows + 1, n_out), 7.0, dtype=self.y_dt,
+                                             device="cuda")
+        ws = torch.full((max(1, B.bfly_lora_matmul_workspace_bytes(rows, n_out, k, self.rank)),),
+                        0x7F, dtype=torch.uint8, device="cuda")
+        B.bfly_lora_matmul(*dev, y[:rows], ws, base=base)
+        torch.cuda.synchronize()
+        if not in_place:
+            assert (y[rows:] == 7.0).all()
+        return y[:rows]
+
+    def check(self, y):
+        rows, k = self.x.shape
+        x, base = np64(self.x), 0.0 if self.base is None else np64(self.base)
+        add = np.zeros((rows, self.b.shape[1]))
+        err = np.zeros_like(add)
+        for i in range(self.num):
+            at = np.nonzero(self.ids.numpy() == i)[0]
+            if not len(at):
+                continue
+            a, b, s = np64(self.a[i]), np64(self.b[i]), float(self.s[i])
+            t, tabs = x[at] @ a.T * s, np.abs(x[at]) @ np.abs(a).T * s
+            terms, cut = (2, 2.0 ** -16) if self.y_dt == BF16 else (3, 2.0 ** -24)
+            et = 1.01 * (k + 64) * U * tabs + (2 * U + cut) * np.abs(t)
+            add[at] = t @ b.T
+            err[at] = et @ np.abs(b).T + 1.01 * terms * self.rank * U * (np.abs(t) @ np.abs(b).T)
+        want = base + add
+        half = torch.finfo(self.y_dt).eps / 2
+        tol = err + U * (np.abs(want) + err) + half * (np.abs(want) + 2 * err)
+        got = np64(y)
+        assert np.isfinite(got).all()
+        assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
+        none = (self.ids.numpy() < 0) | (self.ids.numpy() >= self.num)
+        if none.any():
+            b0 = torch.zeros_like(y.cpu()) if self.base is None else self.base.to(self.y_dt)
+            assert torch.equal(y.cpu()[none], b0[none])
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 64, 72, 128, 136, 200, 256])
+@pytest.mark.parametrize("y", [F32, BF16])
+def test_ranks(rank, y):
+    c = Case(37, 520, 272, rank, 3, y=y)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 64, 65, 255, 256, 257, 300, 513, 1100])
+@pytest.mark.parametrize("ids", ["mixed", "runs", "0", "-1", "5"])
+def test_rows_and_orders(rows, ids):
+    c = Case(rows, 264, 136, 16, 4, ids=ids)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("k", [8, 16, 120, 128, 136, 504, 512, 520, 1000, 4096, 11008])
+def test_depths(k):
+    for rows in (3, 70):
+        c = Case(rows, k, 64, 8, 2, y=F32, base=F32)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("n_out", [8, 16, 24, 32, 40, 64, 248, 256, 264, 1000, 4096])
+def test_widths(n_out):
+    for rows in (3, 70):
+        c = Case(rows, 128, n_out, 16, 2)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("base", [None, F32, BF16])
+@pytest.mark.parametrize("y", [F32, BF16])
+def test_types(base, y):
+    for rows in (5, 260):
+        c = Case(rows, 264, 136, 32, 5, base=base, y=y)
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("y", [F32, BF16])
+def test_in_place(y):
+    for rows in (5, 260):
+        c = Case(rows, 264, 136, 32, 5, base=y, y=y)
+        c.check(c.run(in_place=True))
+
+
+def test_every_row_its_own_adapter():
+    rng = np.random.default_rng(0)
+    c = Case(256, 128, 64, 8, 300, ids=rng.permutation(300)[:256])
+    c.check(c.run())
+
+
+def test_ids_out_of_range():
+    c = Case(7, 128, 64, 8, 3, ids=[0, 3, 2, -2147483648, 2147483647, -1, 1])
+    c.check(c.run())
+
+
+def test_a_row_does_not_depend_on_the_others():
+    # the same rows alone, and among others in another order, in one block of
+    # rows and so with the same split of the k axis
+    c = Case(64, 1024, 128, 16, 6)
+    y = c.run()
+    perm = torch.randperm(64, generator=torch.Generator().manual_seed(1))
+    d = Case(64, 1024, 128, 16, 6)
+    d.x, d.ids, d.base = c.x[perm], c.ids[perm], c.base[perm]
+    assert torch.equal(d.run(), y[perm.cuda()])
+
+
+def test_unused_adapters_and_missing_ranks_are_not_read():
+    # adapters that no row has hold NaN; so do the rows of x without one
+    c = Case(40, 264, 136, 24, 6)
+    c.ids[c.ids == 2] = 4
+    c.a[2] = c.b[2] = c.s[2] = float("nan")
+    y = c.run()
+    c.x[c.ids < 0] = float("nan")
+    assert torch.equal(c.run(), y)
+    c.x[c.ids < 0] = 0.0
+    c.a[2], c.b[2], c.s[2] = 0, 0, 1
+    c.check(y)
+
+
+def test_no_rows():
+    c = Case(0, 128, 64, 8, 2)
+    c.run()
+
+
+def test_same_bits_every_time():
+    c = Case(300, 4096, 264, 64, 7, y=F32)
+    y = c.run()
+    for _ in range(3):
+        assert torch.equal(c.run(), y)
