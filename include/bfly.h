@@ -532,7 +532,7 @@ size_t bfly_rmsnorm_backward_workspace_bytes(int64_t rows, int32_t n);
  * enters the second product, times scaling, with 16 bits (bf16 y) or 24 (fp32
  * y); y is rounded once.  A row's result does not depend on the other rows'.
  * Sizes: k and n_out multiples of 8, k <= 65536, n_out <= 1048576, rank a
- * multiple of 8 up to 256, rows <= 8388608, n_adapters >= 1.  All pointers
+ * multiple of 8 up to 256, rows <= 8388608, n_adapters <= 4194304.  All pointers
  * 16-byte aligned but ids and scaling (4).  rows == 0 is a no-op.
  * Errors: BFLY_ERR_NULL, BFLY_ERR_DTYPE, BFLY_ERR_SIZE (rows < 0 or another
  * size below 1), BFLY_ERR_UNSUPPORTED, BFLY_ERR_WORKSPACE, BFLY_ERR_ALIGN,

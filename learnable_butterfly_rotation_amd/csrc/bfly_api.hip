@@ -1043,6 +1043,7 @@ bfly_status bfly_lora_matmul(const void* x, bfly_dtype x_dt, const int32_t* ids,
   if (n_adapters < 1) return BFLY_ERR_SIZE;
   const bfly_status st = lora_sizes(rows, n_out, k, rank);
   if (st != BFLY_OK) return st;
+  if (n_adapters > bfly::kLoraMaxAdapters) return BFLY_ERR_UNSUPPORTED;
   if (workspace_bytes < bfly_lora_matmul_workspace_bytes(rows, n_out, k, rank))
     return BFLY_ERR_WORKSPACE;
   if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(lora_a, 16) || !aligned(lora_b, 16) ||

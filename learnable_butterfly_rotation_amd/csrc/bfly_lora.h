@@ -7,6 +7,7 @@
 namespace bfly {
 
 constexpr int kLoraMaxRank = 256;
+constexpr int kLoraMaxAdapters = 1 << 22;
 
 struct LoraParams {
   const uint16_t* x;      // bf16 [rows][k]

@@ -25,68 +25,77 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kBlockRows = 256;  // rows whose order a workgroup works out
 constexpr int kTileRows = 64;    // rows of one adapter in a tile at most
-constexpr int kNoAdapter = 0x7FFFFFFF;
+constexpr int kNoAdapter = kLoraMaxAdapters;
 
 // The rows of a block in the order of their adapters, cut into tiles of at
 // most kTileRows rows of one adapter; rows without one come last.
 struct Tiles {
-  int key[kBlockRows];                 // by row; a missing row: kNoAdapter
-  uint8_t order[kBlockRows];           // row at every place
-  int id[kBlockRows];                  // by tile
-  uint16_t start[kBlockRows], len[kBlockRows];
+  uint32_t key[kBlockRows];    // by row, adapter * 256 + row; a missing row: the largest value
+  uint32_t sorted[kBlockRows];  // the keys in their order
+  uint64_t heads[kBlockRows / 64];  // places where a tile begins
+  uint64_t runs[kBlockRows / 64];   // places where an adapter's rows begin
+  uint16_t start[kBlockRows];  // by tile: its first place
   int count;
+  __device__ int row(int place) const { return (int)(sorted[place] & 255u); }
+  __device__ int id(int place) const { return (int)(sorted[place] >> 8); }
 };
 
-// Every thread ranks its own row against all the others (the ids are in LDS,
-// read as broadcasts): no sort, no atomics, any number of adapters.
+// Every thread ranks its own row against all the others (the keys are in LDS,
+// read four at a time as broadcasts): no sort, no atomics, and any ids.
 __device__ __forceinline__ void make_tiles(Tiles& s, const int32_t* ids, int nr, int n_adapters) {
-  __shared__ uint64_t starts[kBlockRows / 64];
-  __shared__ uint8_t head[kBlockRows];
-  const int i = threadIdx.x;
-  int id = kNoAdapter;
+  const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+  uint32_t key = ~0u;
   if (i < nr) {
-    id = ids[i];
-    if (id < 0 || id >= n_adapters) id = kNoAdapter;
+    const int id = ids[i];
+    key = (uint32_t)(id >= 0 && id < n_adapters ? id : kNoAdapter) << 8 | (uint32_t)i;
   }
-  s.key[i] = id;
+  s.key[i] = key;
   __syncthreads();
-  int less = 0, before = 0, same = 0;
-  for (int j = 0; j < nr; ++j) {
-    const int o = s.key[j];
-    less += o < id;
-    same += o == id;
-    before += o == id && j < i;
+  int place = 0;
+#pragma unroll 4
+  for (int j = 0; j < nr; j += 4) {  // past nr: the largest value, never below
+    const uint4 o = *reinterpret_cast<const uint4*>(s.key + j);
+    place += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
   }
-  const int place = less + before;
-  const bool first = i < nr && before % kTileRows == 0;
-  if (i < nr) {
-    s.order[place] = (uint8_t)i;
-    head[place] = first;
-  } else {
-    head[i] = 0;
-  }
+  if (i < nr) s.sorted[place] = key;
   __syncthreads();
-  const uint64_t m = __ballot(head[i] != 0);
-  if ((i & 63) == 0) starts[i >> 6] = m;
+  const uint32_t mine = i < nr ? s.sorted[i] >> 8 : ~0u;
+  const uint32_t left = i > 0 && i < nr ? s.sorted[i - 1] >> 8 : ~0u;
+  const uint64_t runs = __ballot(i < nr && mine != left);
+  if (lane == 0) s.runs[wave] = runs;
   __syncthreads();
-  if (first) {
-    int tile = 0;
-    for (int w = 0; w < kBlockRows / 64; ++w) {
-      const uint64_t b = starts[w];
-      if (w < place >> 6) tile += __popcll(b);
-      else if (w == place >> 6) tile += __popcll(b & ((1ull << (place & 63)) - 1));
-    }
-    const int left = same - before;
-    s.id[tile] = id;
-    s.start[tile] = (uint16_t)place;
-    s.len[tile] = (uint16_t)(left < kTileRows ? left : kTileRows);
+  // the first place of this place's adapter: the last run mark not beyond it
+  int first = 0;
+  for (int w = 0; w <= wave; ++w) {
+    const uint64_t m = w < wave ? s.runs[w] : runs & (~0ull >> (63 - lane));
+    if (m) first = w * 64 + 63 - __clzll((long long)m);
   }
-  if (i == 0) {
-    int c = 0;
-    for (int w = 0; w < kBlockRows / 64; ++w) c += __popcll(starts[w]);
-    s.count = c;
-  }
+  const bool head = i < nr && ((i - first) & (kTileRows - 1)) == 0;
+  const uint64_t heads = __ballot(head);
+  if (lane == 0) s.heads[wave] = heads;
   __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kBlockRows / 64; ++w) {
+    const int c = __popcll(s.heads[w]);
+    before += w < wave ? c : 0;
+    all += c;
+  }
+  if (head) s.start[before + __popcll(heads & ((1ull << lane) - 1))] = (uint16_t)i;
+  if (i == 0) s.count = all;
+  __syncthreads();
+}
+// First place, number of rows and adapter of a tile, uniform over the wave.
+struct Tile {
+  int start, len, id;
+};
+__device__ __forceinline__ Tile tile_at(const Tiles& s, int tile, int nr) {
+  Tile t;
+  t.start = __builtin_amdgcn_readfirstlane((int)s.start[tile]);
+  const int end = tile + 1 < s.count ? (int)s.start[tile + 1] : nr;
+  t.len = __builtin_amdgcn_readfirstlane(end) - t.start;
+  t.id = __builtin_amdgcn_readfirstlane(s.id(t.start));
+  return t;
 }
 
 __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
@@ -96,118 +105,230 @@ __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
 
 // t[split][row][j] = sum over the split's k of A_id[j][k] x[row][k].
 // Grid: (blocks of rows, tile lanes, splits * rank blocks).  RT tiles of 16
-// ranks, NT of 16 rows at a time; the four waves take every fourth run of 128 k and
-// add their sums through LDS.
+// ranks; the four waves take every fourth run of 128 k and add their sums
+// through LDS.
+template <int RT>
+struct ShrinkArgs {
+  __amdgpu_buffer_rsrc_t rx, ra;  // the block's rows of x, the adapter's rows of A
+  const Tiles* tiles;
+  float* t;      // the split's sums of the block's first row, at the rank block
+  f32x4* part;   // LDS [2][RT * NT][64]
+  int k, kbeg, kend, stride;
+};
+
+// NT * 16 rows of a tile (`len` of them, the others read as zeros).  The loop
+// has no branch around its loads: all of a run's loads are in flight together.
 template <int RT, int NT>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int splits, int slice,
-                                                          int stride) {
-  __shared__ Tiles tiles;
-  __shared__ f32x4 part[2][RT * NT][64];
+__device__ __forceinline__ void shrink_rows(const ShrinkArgs<RT>& P, int start, int len) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int64_t row0 = (int64_t)blockIdx.x * kBlockRows;
-  const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
-  const int split = blockIdx.z % splits, rank0 = blockIdx.z / splits * (RT * 16);
-  const int kbeg = split * slice, kend = P.k - kbeg < slice ? P.k : kbeg + slice;
-  make_tiles(tiles, P.ids + row0, nr, P.n_adapters);
-  const __amdgpu_buffer_rsrc_t rx = buffer_range(P.x + row0 * P.k, (int64_t)nr * P.k * 2);
-  const int count = tiles.count;
-  for (int tile = blockIdx.y; tile < count; tile += gridDim.y) {
-    const int id = __builtin_amdgcn_readfirstlane(tiles.id[tile]);
-    if (id == kNoAdapter) break;  // the rows without an adapter come last
-    const int start = __builtin_amdgcn_readfirstlane((int)tiles.start[tile]);
-    const int all = __builtin_amdgcn_readfirstlane((int)tiles.len[tile]);
-    const __amdgpu_buffer_rsrc_t ra =
-        buffer_range(P.a + ((int64_t)id * P.rank + rank0) * P.k, (int64_t)(P.rank - rank0) * P.k * 2);
-    uint32_t ao[RT];
+  uint32_t xo[NT], ao[RT];
+  int row[NT];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) ao[j] = (uint32_t)(j * 16 + n) * (uint32_t)P.k * 2u;
-    for (int first = 0; first < all; first += NT * 16) {
-      const int len = all - first;  // NT * 16 of them at most are taken here
-      uint32_t xo[NT];
-      int row[NT];
+  for (int q = 0; q < NT; ++q) {
+    const int at = q * 16 + n;
+    row[q] = at < len ? P.tiles->row(start + at) : -1;
+    xo[q] = row[q] >= 0 ? (uint32_t)row[q] * (uint32_t)P.k * 2u : kOutOfRange;
+  }
 #pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        const int at = q * 16 + n;
-        row[q] = at < len ? tiles.order[start + first + at] : -1;
-        xo[q] = (uint32_t)row[q] * (uint32_t)P.k * 2u;
-      }
-      f32x4 acc[RT][NT];
+  for (int j = 0; j < RT; ++j) ao[j] = (uint32_t)(j * 16 + n) * (uint32_t)P.k * 2u;
+  f32x4 acc[RT][NT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+#pragma unroll
+    for (int q = 0; q < NT; ++q) acc[j][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int kc = P.kbeg + wave * 128; kc < P.kend; kc += 512) {
+    uint4 fa[4][RT], fx[4][NT];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int kk = kc + u * 32 + g * 8;
+      const bool in = kk < P.kend;
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+        fx[u][q] = buf_ld16(P.rx, in && row[q] >= 0 ? xo[q] + 2u * kk : kOutOfRange);
+#pragma unroll
+      for (int j = 0; j < RT; ++j) fa[u][j] = buf_ld16(P.ra, in ? ao[j] + 2u * kk : kOutOfRange);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[j][q] = mfma(fa[u][j], fx[u][q], acc[j][q]);
+  }
+  // waves 2 and 3 to 0 and 1, then 1 to 0
+  constexpr int half = RT * NT * 64;
+  __syncthreads();  // the turn before has read `part`
+  if (wave >= 2) {
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) P.part[(wave - 2) * half + (j * NT + q) * 64 + lane] = acc[j][q];
+  }
+  __syncthreads();
+  if (wave < 2) {
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) acc[j][q] += P.part[wave * half + (j * NT + q) * 64 + lane];
+  }
+  if (wave == 1) {
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) P.part[half + (j * NT + q) * 64 + lane] = acc[j][q];
+  }
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      if (row[q] < 0) continue;
+      float* const to = P.t + (int64_t)row[q] * P.stride + 4 * g;
 #pragma unroll
       for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int q = 0; q < NT; ++q) acc[j][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int kc = kbeg + wave * 128; kc < kend; kc += 512) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int kk = kc + u * 32 + g * 8;
-          const bool in = kk < kend;
-          uint4 fa[RT];
-#pragma unroll
-          for (int j = 0; j < RT; ++j) fa[j] = buf_ld16(ra, in ? ao[j] + 2u * kk : kOutOfRange);
-#pragma unroll
-          for (int q = 0; q < NT; ++q) {
-            if (q * 16 < len) {
-              const uint4 fx = buf_ld16(rx, in && row[q] >= 0 ? xo[q] + 2u * kk : kOutOfRange);
-#pragma unroll
-              for (int j = 0; j < RT; ++j) acc[j][q] = mfma(fa[j], fx, acc[j][q]);
-            }
-          }
-        }
-      }
-      // waves 2 and 3 to 0 and 1, then 1 to 0
-      __syncthreads();  // the turn before has read `part`
-      if (wave >= 2) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-          for (int q = 0; q < NT; ++q) part[wave - 2][j * NT + q][lane] = acc[j][q];
-      }
-      __syncthreads();
-      if (wave < 2) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-          for (int q = 0; q < NT; ++q) acc[j][q] += part[wave][j * NT + q][lane];
-      }
-      if (wave == 1) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-          for (int q = 0; q < NT; ++q) part[1][j * NT + q][lane] = acc[j][q];
-      }
-      __syncthreads();
-      if (wave == 0) {
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          if (row[q] < 0) continue;
-          float* const to =
-              P.t + ((int64_t)split * P.rows + row0 + row[q]) * stride + rank0 + 4 * g;
-#pragma unroll
-          for (int j = 0; j < RT; ++j)
-            *reinterpret_cast<f32x4*>(to + 16 * j) = acc[j][q] + part[1][j * NT + q][lane];
-        }
-      }
+        *reinterpret_cast<f32x4*>(to + 16 * j) =
+            acc[j][q] + P.part[half + (j * NT + q) * 64 + lane];
     }
   }
 }
 
-// y = base + B_id (s_id t).  Grid: (column tiles, blocks of rows).  The
-// matrix cores' rows are columns of y, in an order that leaves eight
-// consecutive columns of one row of y to a lane: tile j of a pair takes column
-// 8 (m / 4) + 4 j + m % 4 of a run of 32 as its row m.
-constexpr int kCols = 256;  // columns of a workgroup, 64 to a wave
-template <int TERMS, bool BB, bool YB>
-__global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int splits, int stride,
-                                                          int depth, int tile_rows) {
+template <int RT>
+__global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int splits, int slice,
+                                                          int stride) {
+  constexpr int NT = RT == 8 ? 2 : 4;  // 16-row tiles at a time at most
   __shared__ Tiles tiles;
-  extern __shared__ __align__(16) uint16_t terms[];  // [TERMS][tile_rows][depth + 8]
+  __shared__ f32x4 part[2 * RT * NT * 64];
+  const int64_t row0 = (int64_t)blockIdx.x * kBlockRows;
+  const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
+  const int split = blockIdx.z % splits, rank0 = blockIdx.z / splits * (RT * 16);
+  make_tiles(tiles, P.ids + row0, nr, P.n_adapters);
+  ShrinkArgs<RT> a;
+  a.rx = buffer_range(P.x + row0 * P.k, (int64_t)nr * P.k * 2);
+  a.tiles = &tiles;
+  a.t = P.t + ((int64_t)split * P.rows + row0) * stride + rank0;
+  a.part = part;
+  a.k = P.k;
+  a.kbeg = split * slice;
+  a.kend = P.k - a.kbeg < slice ? P.k : a.kbeg + slice;
+  a.stride = stride;
+  const int count = tiles.count;
+  for (int tile = blockIdx.y; tile < count; tile += gridDim.y) {
+    const Tile t = tile_at(tiles, tile, nr);
+    if (t.id == kNoAdapter) break;  // the rows without an adapter come last
+    a.ra = buffer_range(P.a + ((int64_t)t.id * P.rank + rank0) * P.k,
+                        (int64_t)(P.rank - rank0) * P.k * 2);
+    for (int first = 0; first < t.len; first += NT * 16) {
+      const int len = t.len - first;
+      if (len <= 16) shrink_rows<RT, 1>(a, t.start + first, len);
+      else if (len <= 32 || NT == 2) shrink_rows<RT, 2>(a, t.start + first, len);
+      else shrink_rows<RT, NT>(a, t.start + first, len);
+    }
+  }
+}
+
+// y = base + B_id (s_id t).  Grid: (column tiles, blocks of rows, tile lanes).
+// The matrix cores' rows are columns of y, in an order that leaves eight
+// consecutive columns of one row of y to a lane: tile j of a pair takes column
+// 8 (m / 4) + 4 j + m % 4 of a run of 32 as its row m.  DK: runs of 32 ranks.
+// CG: runs of 32 columns to a wave, the next one's loads ahead of this one's
+// products.
+template <int TERMS, bool BB, bool YB, int DK, int CG>
+struct Expand {
+  static constexpr int QN = DK == 8 ? 2 : 4;  // 16-row tiles at a time
+  static constexpr int kRows = QN * 16;
+  static constexpr int kDepth = DK * 32;
+  static constexpr int kPitch = kDepth + 8;
+  static constexpr int kCols = 128 * CG;
+  struct Frag {
+    uint4 b[2][DK];
+    uint4 base[QN][BB ? 1 : 2];
+  };
+  static __device__ __forceinline__ void load(const LoraParams& P, __amdgpu_buffer_rsrc_t rb,
+                                              __amdgpu_buffer_rsrc_t rbase,
+                                              const uint32_t (&ro)[QN], int c0, bool none, Frag& f) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    if (!none) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = c0 + 8 * (n >> 2) + 4 * j + (n & 3);
+#pragma unroll
+        for (int d = 0; d < DK; ++d) {
+          const int r = d * 32 + 8 * g;
+          f.b[j][d] = buf_ld16(rb, r < P.rank && c < P.n_out
+                                       ? ((uint32_t)c * (uint32_t)P.rank + r) * 2u
+                                       : kOutOfRange);
+        }
+      }
+    }
+    if (P.base) {
+      const int c = c0 + 8 * g;
+#pragma unroll
+      for (int q = 0; q < QN; ++q) {
+        const bool in = ro[q] != kOutOfRange && c < P.n_out;
+        const uint32_t at = (ro[q] + (uint32_t)c) * (BB ? 2u : 4u);
+        f.base[q][0] = buf_ld16(rbase, in ? at : kOutOfRange);
+        if constexpr (!BB) f.base[q][1] = buf_ld16(rbase, in ? at + 16u : kOutOfRange);
+      }
+    }
+  }
+  static __device__ __forceinline__ void finish(const LoraParams& P, __amdgpu_buffer_rsrc_t ry,
+                                                const uint16_t* terms, const uint32_t (&ro)[QN],
+                                                int c0, int len, bool none, const Frag& f) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int c = c0 + 8 * g;
+#pragma unroll
+    for (int q = 0; q < QN; ++q) {
+      if (q * 16 >= len) break;
+      f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      if (!none) {
+        const int at = q * 16 + n < len ? q * 16 + n : len - 1;
+#pragma unroll
+        for (int d = 0; d < DK; ++d)
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) {
+            const uint4 ft =
+                *reinterpret_cast<const uint4*>(terms + (k * kRows + at) * kPitch + d * 32 + 8 * g);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[j] = mfma(f.b[j][d], ft, acc[j]);
+          }
+      }
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = acc[e >> 2][e & 3];
+      if (P.base) {
+        const uint4 w0 = f.base[q][0], w1 = f.base[q][BB ? 0 : 1];
+        const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] += !BB ? __uint_as_float(ww[e]) : (e & 1) ? bf16_hi(ww[e >> 1]) : bf16_lo(ww[e >> 1]);
+      }
+      const bool in = ro[q] != kOutOfRange && c < P.n_out;
+      const uint32_t to = (ro[q] + (uint32_t)c) * (YB ? 2u : 4u);
+      if constexpr (YB) {
+        buf_st16(ry, in ? to : kOutOfRange,
+                 make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                            pack_bf16(v[6], v[7])));
+      } else {
+        buf_st16(ry, in ? to : kOutOfRange,
+                 make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                            __float_as_uint(v[3])));
+        buf_st16(ry, in ? to + 16u : kOutOfRange,
+                 make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                            __float_as_uint(v[7])));
+      }
+    }
+  }
+};
+
+template <int TERMS, bool BB, bool YB, int DK, int CG>
+__global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int splits, int stride) {
+  using E = Expand<TERMS, BB, YB, DK, CG>;
+  __shared__ Tiles tiles;
+  __shared__ __align__(16) uint16_t terms[TERMS * E::kRows * E::kPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
   const int64_t row0 = (int64_t)blockIdx.y * kBlockRows;
   const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
-  const int col0 = blockIdx.x * kCols + wave * 64;
-  const int pitch = depth + 8;
+  const int col0 = blockIdx.x * E::kCols + wave * 32 * CG;
   make_tiles(tiles, P.ids + row0, nr, P.n_adapters);
   constexpr int bs = BB ? 2 : 4, ys = YB ? 2 : 4;
   const __amdgpu_buffer_rsrc_t rbase =
@@ -216,27 +337,34 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int spli
   const __amdgpu_buffer_rsrc_t ry =
       buffer_range(static_cast<char*>(P.y) + row0 * P.n_out * ys, (int64_t)nr * P.n_out * ys);
   const int count = tiles.count;
-  for (int tile = 0; tile < count; ++tile) {
-    const int id = __builtin_amdgcn_readfirstlane(tiles.id[tile]);
-    const bool none = id == kNoAdapter;
+  for (int tile = blockIdx.z; tile < count; tile += gridDim.z) {
+    const Tile t = tile_at(tiles, tile, nr);
+    const bool none = t.id == kNoAdapter;
     if (none && P.base == P.y) break;  // in place: those rows stay as they are
-    const int start = __builtin_amdgcn_readfirstlane((int)tiles.start[tile]);
-    const int all = __builtin_amdgcn_readfirstlane((int)tiles.len[tile]);
     const __amdgpu_buffer_rsrc_t rb = none
         ? buffer_range32(nullptr, 0)
-        : buffer_range(P.b + (int64_t)id * P.n_out * P.rank, (int64_t)P.n_out * P.rank * 2);
-    for (int part = 0; part < all; part += tile_rows) {
-      const int len = all - part < tile_rows ? all - part : tile_rows;
+        : buffer_range(P.b + (int64_t)t.id * P.n_out * P.rank, (int64_t)P.n_out * P.rank * 2);
+    for (int part = 0; part < t.len; part += E::kRows) {
+      const int len = t.len - part < E::kRows ? t.len - part : E::kRows;
+      uint32_t ro[E::QN];
+#pragma unroll
+      for (int q = 0; q < E::QN; ++q) {
+        const int at = q * 16 + (lane & 15);
+        ro[q] = at < len ? (uint32_t)tiles.row(t.start + part + at) * (uint32_t)P.n_out
+                         : kOutOfRange;
+      }
+      typename E::Frag f[CG];
+      E::load(P, rb, rbase, ro, col0, none, f[0]);
       if (!none) {
         // the terms of s t, four ranks to a thread at a time
-        const float s = P.scaling[id];
-        __syncthreads();
-        const int quads = depth / 4;
-        for (int i = threadIdx.x; i < len * quads; i += kThreads) {
-          const int r = i / quads, c = i % quads * 4;
+        const float s = P.scaling[t.id];
+        __syncthreads();  // the turn before has read them
+        for (int i = threadIdx.x; i < len * (E::kDepth / 4); i += kThreads) {
+          const int r = i / (E::kDepth / 4), c = i % (E::kDepth / 4) * 4;
           f32x4 v = {0.f, 0.f, 0.f, 0.f};
           if (c < stride) {
-            const float* from = P.t + (row0 + tiles.order[start + part + r]) * stride + c;
+            const float* from = P.t + (row0 + tiles.row(t.start + part + r)) * stride + c;
+#pragma unroll 4
             for (int k = 0; k < splits; ++k)
               v += *reinterpret_cast<const f32x4*>(from + k * P.rows * stride);
             v *= s;
@@ -244,74 +372,17 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int spli
 #pragma unroll
           for (int q = 0; q < TERMS; ++q) {
             const uint32_t lo = pack_bf16(v.x, v.y), hi = pack_bf16(v.z, v.w);
-            *reinterpret_cast<uint2*>(terms + (q * tile_rows + r) * pitch + c) = make_uint2(lo, hi);
+            *reinterpret_cast<uint2*>(terms + (q * E::kRows + r) * E::kPitch + c) =
+                make_uint2(lo, hi);
             v -= f32x4{bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
           }
         }
         __syncthreads();
       }
-      for (int c32 = 0; c32 < 64; c32 += 32) {
-        const int c0 = col0 + c32;
-        if (c0 >= P.n_out) break;
-        for (int q = 0; q < len; q += 16) {
-          f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-          if (!none) {
-            for (int d = 0; d < depth; d += 32) {
-              const int r = d + 8 * g;
-              uint4 fb[2];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int c = c0 + 8 * (n >> 2) + 4 * j + (n & 3);
-                fb[j] = buf_ld16(rb, r < P.rank && c < P.n_out
-                                         ? ((uint32_t)c * (uint32_t)P.rank + r) * 2u
-                                         : kOutOfRange);
-              }
-#pragma unroll
-              for (int k = 0; k < TERMS; ++k) {
-                const int at = q + n < len ? q + n : len - 1;
-                const uint4 ft = *reinterpret_cast<const uint4*>(
-                    terms + (k * tile_rows + at) * pitch + r);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[j] = mfma(fb[j], ft, acc[j]);
-              }
-            }
-          }
-          // lane: row q + n, columns c0 + 8 g .. + 7
-          const int c = c0 + 8 * g;
-          const bool in = q + n < len && c < P.n_out;
-          const uint32_t at = in ? (uint32_t)tiles.order[start + part + q + n] * (uint32_t)P.n_out +
-                                       (uint32_t)c
-                                 : 0u;
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = acc[e >> 2][e & 3];
-          if (P.base) {
-            if constexpr (BB) {
-              const uint4 w = buf_ld16(rbase, in ? at * 2u : kOutOfRange);
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] += (e & 1) ? bf16_hi(ww[e >> 1]) : bf16_lo(ww[e >> 1]);
-            } else {
-              const uint4 w0 = buf_ld16(rbase, in ? at * 4u : kOutOfRange);
-              const uint4 w1 = buf_ld16(rbase, in ? at * 4u + 16u : kOutOfRange);
-              const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] += __uint_as_float(ww[e]);
-            }
-          }
-          if constexpr (YB) {
-            buf_st16(ry, in ? at * 2u : kOutOfRange,
-                     make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
-          } else {
-            buf_st16(ry, in ? at * 4u : kOutOfRange,
-                     make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                __float_as_uint(v[2]), __float_as_uint(v[3])));
-            buf_st16(ry, in ? at * 4u + 16u : kOutOfRange,
-                     make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                __float_as_uint(v[6]), __float_as_uint(v[7])));
-          }
-        }
+      for (int cg = 0; cg < CG; ++cg) {
+        if (cg + 1 < CG) E::load(P, rb, rbase, ro, col0 + 32 * (cg + 1), none, f[cg + 1]);
+        E::finish(P, ry, terms, ro, col0 + 32 * cg, len, none, f[cg]);
       }
     }
   }
@@ -323,40 +394,60 @@ struct Cut {
   int ranks;     // rank blocks of 16 rt
   int stride;    // floats of a row of t
   int64_t blocks;  // blocks of rows
-  int lanes;     // shrink workgroups that share a block's tiles
   int splits, slice;  // of the k axis
 };
+// Workgroups that share a block's tiles: as many as it can have tiles, up to
+// a number that leaves few of them idle when there are many blocks.
+int tile_lanes(int64_t rows, int64_t blocks, int n_adapters) {
+  const int64_t r = rows < kBlockRows ? rows : kBlockRows;
+  const int64_t most = (r < n_adapters ? r : n_adapters) + r / kTileRows + 1;
+  const int64_t cap = blocks <= 2 ? 32 : blocks <= 8 ? 16 : 4;
+  return (int)(most < cap ? most : cap);
+}
 Cut cut(int64_t rows, int k, int rank) {
   Cut c;
   c.rt = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
   c.ranks = (rank + 16 * c.rt - 1) / (16 * c.rt);
   c.stride = c.ranks * c.rt * 16;
   c.blocks = (rows + kBlockRows - 1) / kBlockRows;
-  c.lanes = c.blocks > 1 ? 4 : (int)(rows < 16 ? rows : 16);
-  const int64_t groups = c.blocks * c.lanes * c.ranks;
+  // tiles there are at least: one to 64 rows
+  const int64_t groups = (rows + kTileRows - 1) / kTileRows * c.ranks;
   const int most = (k + 511) / 512;
-  const int64_t want = (768 + groups - 1) / groups;
+  const int64_t want = (512 + groups - 1) / groups;
   c.splits = (int)(want < most ? want : most);
   c.slice = ((k + c.splits - 1) / c.splits + 127) / 128 * 128;
   c.splits = (k + c.slice - 1) / c.slice;
   return c;
 }
 
-template <int RT, int NT>
+template <int RT>
 void shrink(const LoraParams& p, const Cut& c, hipStream_t s) {
-  hipLaunchKernelGGL((shrink_kernel<RT, NT>),
-                     dim3((unsigned)c.blocks, c.lanes, c.splits * c.ranks), dim3(kThreads), 0, s, p,
-                     c.splits, c.slice, c.stride);
+  hipLaunchKernelGGL((shrink_kernel<RT>),
+                     dim3((unsigned)c.blocks, tile_lanes(p.rows, c.blocks, p.n_adapters),
+                          c.splits * c.ranks),
+                     dim3(kThreads), 0, s, p, c.splits, c.slice, c.stride);
 }
 
-template <int TERMS, bool BB, bool YB>
+template <int TERMS, bool BB, bool YB, int DK, int CG>
 void expand(const LoraParams& p, const Cut& c, hipStream_t s) {
-  const int depth = (c.stride + 31) / 32 * 32;
-  const int tile_rows = depth > 128 ? 32 : 64;
-  hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB>),
-                     dim3((p.n_out + kCols - 1) / kCols, (unsigned)c.blocks), dim3(kThreads),
-                     TERMS * tile_rows * (depth + 8) * sizeof(uint16_t), s, p, c.splits, c.stride,
-                     depth, tile_rows);
+  using E = Expand<TERMS, BB, YB, DK, CG>;
+  // few rows: a workgroup to a tile; many: a workgroup to a block
+  const int lanes = c.blocks <= 8 ? tile_lanes(p.rows, c.blocks, p.n_adapters) : 1;
+  hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB, DK, CG>),
+                     dim3((p.n_out + E::kCols - 1) / E::kCols, (unsigned)c.blocks, lanes),
+                     dim3(kThreads), 0, s, p, c.splits, c.stride);
+}
+template <int TERMS, bool BB, bool YB, int DK>
+void expand_cg(const LoraParams& p, const Cut& c, hipStream_t s) {
+  if (c.blocks <= 8) expand<TERMS, BB, YB, DK, 1>(p, c, s);
+  else expand<TERMS, BB, YB, DK, 2>(p, c, s);
+}
+template <int TERMS, bool BB, bool YB>
+void expand_dk(const LoraParams& p, const Cut& c, hipStream_t s) {
+  if (c.stride <= 32) expand_cg<TERMS, BB, YB, 1>(p, c, s);
+  else if (c.stride <= 64) expand_cg<TERMS, BB, YB, 2>(p, c, s);
+  else if (c.stride <= 128) expand_cg<TERMS, BB, YB, 4>(p, c, s);
+  else expand_cg<TERMS, BB, YB, 8>(p, c, s);
 }
 
 }  // namespace
@@ -369,19 +460,19 @@ size_t lora_workspace_bytes(int64_t rows, int k, int rank) {
 hipError_t launch_lora(const LoraParams& p, hipStream_t s) {
   const Cut c = cut(p.rows, p.k, p.rank);
   switch (c.rt) {
-    case 1: shrink<1, 4>(p, c, s); break;
-    case 2: shrink<2, 4>(p, c, s); break;
-    case 4: shrink<4, 4>(p, c, s); break;
-    default: shrink<8, 2>(p, c, s); break;
+    case 1: shrink<1>(p, c, s); break;
+    case 2: shrink<2>(p, c, s); break;
+    case 4: shrink<4>(p, c, s); break;
+    default: shrink<8>(p, c, s); break;
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.y_bf16) {
-    if (p.base_bf16) expand<2, true, true>(p, c, s);
-    else expand<2, false, true>(p, c, s);
+    if (p.base_bf16) expand_dk<2, true, true>(p, c, s);
+    else expand_dk<2, false, true>(p, c, s);
   } else {
-    if (p.base_bf16) expand<3, true, false>(p, c, s);
-    else expand<3, false, false>(p, c, s);
+    if (p.base_bf16) expand_dk<3, true, false>(p, c, s);
+    else expand_dk<3, false, false>(p, c, s);
   }
   return hipGetLastError();
 }

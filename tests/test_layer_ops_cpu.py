@@ -96,7 +96,7 @@ def test_lora_refusals(L):
         assert lora(L, **{name: 0}) == SIZE, name
     assert lora(L, rows=-1) == SIZE
     for name, v in (("n_out", 12), ("k", 4), ("rank", 12), ("n_out", (1 << 20) + 8), ("k", 65544),
-                    ("rank", 264), ("rows", (1 << 23) + 1)):
+                    ("rank", 264), ("rows", (1 << 23) + 1), ("num", (1 << 22) + 1)):
         assert lora(L, **{name: v}) == UNSUPPORTED, (name, v)
     need = B.bfly_lora_matmul_workspace_bytes(4, 256, 512, 16)
     assert need > 0 and lora(L, wsb=need - 1) == WORKSPACE
