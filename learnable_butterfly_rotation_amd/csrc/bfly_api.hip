@@ -1058,7 +1058,7 @@ bfly_status bfly_lora_matmul(const void* x, bfly_dtype x_dt, const int32_t* ids,
   p.scaling = scaling;
   p.base = base;
   p.y = y;
-  p.t = static_cast<float*>(workspace);
+  p.workspace = workspace;
   p.rows = rows;
   p.n_out = n_out;
   p.k = k;

@@ -17,7 +17,7 @@ struct LoraParams {
   const float* scaling;   // [n_adapters]
   const void* base;       // [rows][n_out] of base_bf16 or fp32, or nullptr (zeros)
   void* y;                // [rows][n_out] of y_bf16 or fp32; may be base (same type)
-  float* t;               // workspace: [splits][rows][lora_t_stride(rank)]
+  void* workspace;        // lora_workspace_bytes
   int64_t rows;
   int32_t n_out, k, n_adapters, rank;
   int32_t base_bf16, y_bf16;

@@ -21,6 +21,7 @@ namespace {
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int kBlockRows = 256;  // rows whose order a workgroup works out
@@ -51,11 +52,15 @@ __device__ __forceinline__ void make_tiles(Tiles& s, const int32_t* ids, int nr,
   }
   s.key[i] = key;
   __syncthreads();
-  int place = 0;
+  int place = i;
+  // packed prompts mostly come in order: nothing to rank then
+  if (!__syncthreads_and(i == 0 || s.key[i - 1] <= key)) {
+    place = 0;
 #pragma unroll 4
-  for (int j = 0; j < nr; j += 4) {  // past nr: the largest value, never below
-    const uint4 o = *reinterpret_cast<const uint4*>(s.key + j);
-    place += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
+    for (int j = 0; j < nr; j += 4) {  // past nr: the largest value, never below
+      const uint4 o = *reinterpret_cast<const uint4*>(s.key + j);
+      place += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
+    }
   }
   if (i < nr) s.sorted[place] = key;
   __syncthreads();
@@ -85,6 +90,26 @@ __device__ __forceinline__ void make_tiles(Tiles& s, const int32_t* ids, int nr,
   if (i == 0) s.count = all;
   __syncthreads();
 }
+
+// The order that shrink works out, as it leaves it for expand in the workspace.
+struct Order {
+  uint32_t sorted[kBlockRows];
+  uint16_t start[kBlockRows];
+  int32_t count, pad[3];
+};
+__device__ __forceinline__ void put_order(Order* o, const Tiles& s) {
+  const int i = threadIdx.x;
+  o->sorted[i] = s.sorted[i];
+  o->start[i] = s.start[i];
+  if (i == 0) o->count = s.count;
+}
+__device__ __forceinline__ void get_order(Tiles& s, const Order* o) {
+  const int i = threadIdx.x;
+  s.sorted[i] = o->sorted[i];
+  s.start[i] = o->start[i];
+  if (i == 0) s.count = o->count;
+  __syncthreads();
+}
 // First place, number of rows and adapter of a tile, uniform over the wave.
 struct Tile {
   int start, len, id;
@@ -98,115 +123,178 @@ __device__ __forceinline__ Tile tile_at(const Tiles& s, int tile, int nr) {
   return t;
 }
 
+// The workspace: the orders of the blocks, then t.
+__device__ __forceinline__ Order* order_at(const LoraParams& P) {
+  return static_cast<Order*>(P.workspace);
+}
+__device__ __forceinline__ float* t_at(const LoraParams& P) {
+  return reinterpret_cast<float*>(order_at(P) + (P.rows + kBlockRows - 1) / kBlockRows);
+}
+
 __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// A row of 64 k in LDS: 128 bytes and 16 of padding, so that eight lanes
+// reading one 16-byte column of eight rows touch every bank once.
+constexpr int kRun = 64;
+constexpr int kRunPitch = 2 * kRun + 16;
+
 // t[split][row][j] = sum over the split's k of A_id[j][k] x[row][k].
 // Grid: (blocks of rows, tile lanes, splits * rank blocks).  RT tiles of 16
-// ranks; the four waves take every fourth run of 128 k and add their sums
-// through LDS.
+// ranks; the four waves take every fourth run of 64 k, each by itself, and
+// add their sums through LDS at the end.
+//
+// A matrix-core operand wants row l % 16 in lane l, so loading it straight
+// from memory makes four neighbouring lanes touch four lines and a load of
+// the wave take 64 cycles of the address unit instead of 16: for few rows
+// that, not the memory, was the bound (2.2 us for 512 k of 64 ranks, 0.6 now).
+// So eight neighbouring lanes load a row's 128 bytes and the operands are
+// read back from LDS.
 template <int RT>
 struct ShrinkArgs {
+  static constexpr int kMaxTiles = 4;                // 16-row tiles at a time at most
+  static constexpr int kStaged = RT == 4 ? 2 : 4;    // of them in LDS at once
+  static constexpr int kWaveBytes = (RT + kStaged) * 16 * kRunPitch;
   __amdgpu_buffer_rsrc_t rx, ra;  // the block's rows of x, the adapter's rows of A
   const Tiles* tiles;
   float* t;      // the split's sums of the block's first row, at the rank block
-  f32x4* part;   // LDS [2][RT * NT][64]
+  uint8_t* lds;  // [4][kWaveBytes]; then the sums of two waves
   int k, kbeg, kend, stride;
 };
 
-// NT * 16 rows of a tile (`len` of them, the others read as zeros).  The loop
-// has no branch around its loads: all of a run's loads are in flight together.
+// NT * 16 rows of a tile (`len` of them, the others read as zeros).
 template <int RT, int NT>
 __device__ __forceinline__ void shrink_rows(const ShrinkArgs<RT>& P, int start, int len) {
+  using S = ShrinkArgs<RT>;
+  constexpr int XS = NT < S::kStaged ? NT : S::kStaged;
+  static_assert(2 * RT * S::kMaxTiles * 64 * 16 <= 4 * S::kWaveBytes, "the sums fit");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  uint32_t xo[NT], ao[RT];
-  int row[NT];
+  uint8_t* const mine = P.lds + wave * S::kWaveBytes;
+  // loading: row 8 i + lane / 8, its 16-byte piece lane % 8
+  const int piece = lane & 7;
+  uint32_t xo[2 * NT];
 #pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    const int at = q * 16 + n;
-    row[q] = at < len ? P.tiles->row(start + at) : -1;
-    xo[q] = row[q] >= 0 ? (uint32_t)row[q] * (uint32_t)P.k * 2u : kOutOfRange;
+  for (int i = 0; i < 2 * NT; ++i) {
+    const int at = i * 8 + (lane >> 3);
+    xo[i] = at < len ? (uint32_t)P.tiles->row(start + at) * (uint32_t)P.k * 2u : kOutOfRange;
   }
+  const uint32_t ao = (uint32_t)(lane >> 3) * (uint32_t)P.k * 2u;
+  uint4 qa[2 * RT], qx[2 * NT];
+  const auto load_a = [&](int kc) {
+    const int kk = kc + piece * 8;
 #pragma unroll
-  for (int j = 0; j < RT; ++j) ao[j] = (uint32_t)(j * 16 + n) * (uint32_t)P.k * 2u;
+    for (int i = 0; i < 2 * RT; ++i)
+      qa[i] = buf_ld16(P.ra, kk < P.kend ? ao + (uint32_t)(i * 8 * P.k + kk) * 2u : kOutOfRange);
+  };
+  const auto load_x = [&](int kc, int first) {
+    const int kk = kc + piece * 8;
+#pragma unroll
+    for (int i = 0; i < 2 * XS; ++i)
+      qx[2 * first + i] = buf_ld16(P.rx, kk < P.kend && xo[2 * first + i] != kOutOfRange
+                                             ? xo[2 * first + i] + 2u * kk
+                                             : kOutOfRange);
+  };
+  uint8_t* const put = mine + (lane >> 3) * kRunPitch + piece * 16;
+  const uint8_t* const get = mine + n * kRunPitch + g * 16;
   f32x4 acc[RT][NT];
 #pragma unroll
   for (int j = 0; j < RT; ++j)
 #pragma unroll
     for (int q = 0; q < NT; ++q) acc[j][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kc = P.kbeg + wave * 128; kc < P.kend; kc += 512) {
-    uint4 fa[4][RT], fx[4][NT];
+
+  int kc = P.kbeg + wave * kRun;
+  load_a(kc);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int kk = kc + u * 32 + g * 8;
-      const bool in = kk < P.kend;
+  for (int f = 0; f < NT; f += XS) load_x(kc, f);
+  for (; kc < P.kend; kc += 4 * kRun) {
+    wave_lds_sync();
 #pragma unroll
-      for (int q = 0; q < NT; ++q)
-        fx[u][q] = buf_ld16(P.rx, in && row[q] >= 0 ? xo[q] + 2u * kk : kOutOfRange);
+    for (int i = 0; i < 2 * RT; ++i) *reinterpret_cast<uint4*>(put + i * 8 * kRunPitch) = qa[i];
+    load_a(kc + 4 * kRun);
 #pragma unroll
-      for (int j = 0; j < RT; ++j) fa[u][j] = buf_ld16(P.ra, in ? ao[j] + 2u * kk : kOutOfRange);
+    for (int f = 0; f < NT; f += XS) {
+      if (f > 0) wave_lds_sync();
+#pragma unroll
+      for (int i = 0; i < 2 * XS; ++i)
+        *reinterpret_cast<uint4*>(put + (RT * 16 + i * 8) * kRunPitch) = qx[2 * f + i];
+      load_x(kc + 4 * kRun, f);
+      wave_lds_sync();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4 fa[RT], fx[XS];
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+          fa[j] = *reinterpret_cast<const uint4*>(get + j * 16 * kRunPitch + u * 64);
+#pragma unroll
+        for (int q = 0; q < XS; ++q)
+          fx[q] = *reinterpret_cast<const uint4*>(get + (RT + q) * 16 * kRunPitch + u * 64);
+#pragma unroll
+        for (int q = 0; q < XS; ++q)
+#pragma unroll
+          for (int j = 0; j < RT; ++j) acc[j][f + q] = mfma(fa[j], fx[q], acc[j][f + q]);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int j = 0; j < RT; ++j) acc[j][q] = mfma(fa[u][j], fx[u][q], acc[j][q]);
   }
+
   // waves 2 and 3 to 0 and 1, then 1 to 0
+  f32x4* const part = reinterpret_cast<f32x4*>(P.lds);
   constexpr int half = RT * NT * 64;
-  __syncthreads();  // the turn before has read `part`
+  __syncthreads();
   if (wave >= 2) {
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int q = 0; q < NT; ++q) P.part[(wave - 2) * half + (j * NT + q) * 64 + lane] = acc[j][q];
+      for (int q = 0; q < NT; ++q) part[(wave - 2) * half + (j * NT + q) * 64 + lane] = acc[j][q];
   }
   __syncthreads();
   if (wave < 2) {
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int q = 0; q < NT; ++q) acc[j][q] += P.part[wave * half + (j * NT + q) * 64 + lane];
+      for (int q = 0; q < NT; ++q) acc[j][q] += part[wave * half + (j * NT + q) * 64 + lane];
   }
   if (wave == 1) {
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int q = 0; q < NT; ++q) P.part[half + (j * NT + q) * 64 + lane] = acc[j][q];
+      for (int q = 0; q < NT; ++q) part[half + (j * NT + q) * 64 + lane] = acc[j][q];
   }
   __syncthreads();
   if (wave == 0) {
 #pragma unroll
     for (int q = 0; q < NT; ++q) {
-      if (row[q] < 0) continue;
-      float* const to = P.t + (int64_t)row[q] * P.stride + 4 * g;
+      if (q * 16 + n < len) {
+        float* const to =
+            P.t + (int64_t)P.tiles->row(start + q * 16 + n) * P.stride + 4 * g;
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
-        *reinterpret_cast<f32x4*>(to + 16 * j) =
-            acc[j][q] + P.part[half + (j * NT + q) * 64 + lane];
+        for (int j = 0; j < RT; ++j)
+          *reinterpret_cast<f32x4*>(to + 16 * j) =
+              acc[j][q] + part[half + (j * NT + q) * 64 + lane];
+      }
     }
   }
+  __syncthreads();  // the next turn writes over the sums
 }
 
 template <int RT>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int splits, int slice,
                                                           int stride) {
-  constexpr int NT = RT == 8 ? 2 : 4;  // 16-row tiles at a time at most
+  using S = ShrinkArgs<RT>;
   __shared__ Tiles tiles;
-  __shared__ f32x4 part[2 * RT * NT * 64];
+  __shared__ __align__(16) uint8_t lds[4 * S::kWaveBytes];
   const int64_t row0 = (int64_t)blockIdx.x * kBlockRows;
   const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
   const int split = blockIdx.z % splits, rank0 = blockIdx.z / splits * (RT * 16);
   make_tiles(tiles, P.ids + row0, nr, P.n_adapters);
-  ShrinkArgs<RT> a;
+  if (blockIdx.y == 0 && blockIdx.z == 0) put_order(order_at(P) + blockIdx.x, tiles);
+  S a;
   a.rx = buffer_range(P.x + row0 * P.k, (int64_t)nr * P.k * 2);
   a.tiles = &tiles;
-  a.t = P.t + ((int64_t)split * P.rows + row0) * stride + rank0;
-  a.part = part;
+  a.t = t_at(P) + ((int64_t)split * P.rows + row0) * stride + rank0;
+  a.lds = lds;
   a.k = P.k;
   a.kbeg = split * slice;
   a.kend = P.k - a.kbeg < slice ? P.k : a.kbeg + slice;
@@ -217,144 +305,129 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int spli
     if (t.id == kNoAdapter) break;  // the rows without an adapter come last
     a.ra = buffer_range(P.a + ((int64_t)t.id * P.rank + rank0) * P.k,
                         (int64_t)(P.rank - rank0) * P.k * 2);
-    for (int first = 0; first < t.len; first += NT * 16) {
-      const int len = t.len - first;
-      if (len <= 16) shrink_rows<RT, 1>(a, t.start + first, len);
-      else if (len <= 32 || NT == 2) shrink_rows<RT, 2>(a, t.start + first, len);
-      else shrink_rows<RT, NT>(a, t.start + first, len);
-    }
+    if (t.len <= 16) shrink_rows<RT, 1>(a, t.start, t.len);
+    else if (t.len <= 32) shrink_rows<RT, 2>(a, t.start, t.len);
+    else shrink_rows<RT, 4>(a, t.start, t.len);
   }
 }
 
 // y = base + B_id (s_id t).  Grid: (column tiles, blocks of rows, tile lanes).
-// The matrix cores' rows are columns of y, in an order that leaves eight
-// consecutive columns of one row of y to a lane: tile j of a pair takes column
-// 8 (m / 4) + 4 j + m % 4 of a run of 32 as its row m.  DK: runs of 32 ranks.
-// CG: runs of 32 columns to a wave, the next one's loads ahead of this one's
-// products.
-template <int TERMS, bool BB, bool YB, int DK, int CG>
+// The matrix cores' columns are columns of y: tile j of JT takes columns
+// JT n + j as its columns n, so that a lane is left with JT consecutive
+// columns of a row and 16 lanes with a run of 16 JT (memory in whole lines).
+// DK: runs of 32 ranks.
+template <int TERMS, bool BB, bool YB, int DK>
 struct Expand {
+  static constexpr int JT = 4;                 // 8: 138 us for 135 of a prompt's call
   static constexpr int QN = DK == 8 ? 2 : 4;  // 16-row tiles at a time
   static constexpr int kRows = QN * 16;
   static constexpr int kDepth = DK * 32;
   static constexpr int kPitch = kDepth + 8;
-  static constexpr int kCols = 128 * CG;
-  struct Frag {
-    uint4 b[2][DK];
-    uint4 base[QN][BB ? 1 : 2];
+  static constexpr int kCols = 64 * JT;  // columns of a workgroup
+  static constexpr int kBaseWords = JT * (BB ? 2 : 4) / 4, kYWords = JT * (YB ? 2 : 4) / 4;
+  struct Base {
+    uint32_t w[4][kBaseWords];
   };
-  static __device__ __forceinline__ void load(const LoraParams& P, __amdgpu_buffer_rsrc_t rb,
-                                              __amdgpu_buffer_rsrc_t rbase,
-                                              const uint32_t (&ro)[QN], int c0, bool none, Frag& f) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    if (!none) {
+  static __device__ __forceinline__ void load_base(__amdgpu_buffer_rsrc_t r,
+                                                   const uint32_t (&ro)[4], int c, int n_out,
+                                                   Base& f) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = c0 + 8 * (n >> 2) + 4 * j + (n & 3);
+    for (int i = 0; i < 4; ++i) {
+      const bool in = ro[i] != kOutOfRange && c < n_out;
+      const uint32_t at = in ? (ro[i] + (uint32_t)c) * (BB ? 2u : 4u) : kOutOfRange;
+      if constexpr (kBaseWords == 2) {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, 0);
+        f.w[i][0] = v.x;
+        f.w[i][1] = v.y;
+      } else {
 #pragma unroll
-        for (int d = 0; d < DK; ++d) {
-          const int r = d * 32 + 8 * g;
-          f.b[j][d] = buf_ld16(rb, r < P.rank && c < P.n_out
-                                       ? ((uint32_t)c * (uint32_t)P.rank + r) * 2u
-                                       : kOutOfRange);
+        for (int k = 0; k < kBaseWords; k += 4) {
+          const uint4 v = buf_ld16(r, in ? at + 4u * k : kOutOfRange);
+          f.w[i][k] = v.x;
+          f.w[i][k + 1] = v.y;
+          f.w[i][k + 2] = v.z;
+          f.w[i][k + 3] = v.w;
         }
       }
     }
-    if (P.base) {
-      const int c = c0 + 8 * g;
-#pragma unroll
-      for (int q = 0; q < QN; ++q) {
-        const bool in = ro[q] != kOutOfRange && c < P.n_out;
-        const uint32_t at = (ro[q] + (uint32_t)c) * (BB ? 2u : 4u);
-        f.base[q][0] = buf_ld16(rbase, in ? at : kOutOfRange);
-        if constexpr (!BB) f.base[q][1] = buf_ld16(rbase, in ? at + 16u : kOutOfRange);
-      }
-    }
   }
-  static __device__ __forceinline__ void finish(const LoraParams& P, __amdgpu_buffer_rsrc_t ry,
-                                                const uint16_t* terms, const uint32_t (&ro)[QN],
-                                                int c0, int len, bool none, const Frag& f) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    const int c = c0 + 8 * g;
+  static __device__ __forceinline__ float base_at(const Base& f, int i, int j) {
+    if constexpr (!BB) return __uint_as_float(f.w[i][j]);
+    else return (j & 1) ? bf16_hi(f.w[i][j >> 1]) : bf16_lo(f.w[i][j >> 1]);
+  }
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t ro, int c,
+                                               int n_out, const float (&v)[JT]) {
+    const bool in = ro != kOutOfRange && c < n_out;
+    const uint32_t at = in ? (ro + (uint32_t)c) * (YB ? 2u : 4u) : kOutOfRange;
+    uint32_t w[kYWords];
 #pragma unroll
-    for (int q = 0; q < QN; ++q) {
-      if (q * 16 >= len) break;
-      f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      if (!none) {
-        const int at = q * 16 + n < len ? q * 16 + n : len - 1;
+    for (int k = 0; k < kYWords; ++k)
+      w[k] = YB ? pack_bf16(v[(2 * k) % JT], v[(2 * k + 1) % JT]) : __float_as_uint(v[k % JT]);
+    if constexpr (kYWords == 2) {
+      const u32x2 q = {w[0], w[1]};
+      __builtin_amdgcn_raw_buffer_store_b64(q, r, (int)at, 0, 0);
+    } else {
 #pragma unroll
-        for (int d = 0; d < DK; ++d)
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) {
-            const uint4 ft =
-                *reinterpret_cast<const uint4*>(terms + (k * kRows + at) * kPitch + d * 32 + 8 * g);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc[j] = mfma(f.b[j][d], ft, acc[j]);
-          }
-      }
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = acc[e >> 2][e & 3];
-      if (P.base) {
-        const uint4 w0 = f.base[q][0], w1 = f.base[q][BB ? 0 : 1];
-        const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[e] += !BB ? __uint_as_float(ww[e]) : (e & 1) ? bf16_hi(ww[e >> 1]) : bf16_lo(ww[e >> 1]);
-      }
-      const bool in = ro[q] != kOutOfRange && c < P.n_out;
-      const uint32_t to = (ro[q] + (uint32_t)c) * (YB ? 2u : 4u);
-      if constexpr (YB) {
-        buf_st16(ry, in ? to : kOutOfRange,
-                 make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                            pack_bf16(v[6], v[7])));
-      } else {
-        buf_st16(ry, in ? to : kOutOfRange,
-                 make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                            __float_as_uint(v[3])));
-        buf_st16(ry, in ? to + 16u : kOutOfRange,
-                 make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                            __float_as_uint(v[7])));
-      }
+      for (int k = 0; k < kYWords; k += 4)
+        buf_st16(r, in ? at + 4u * k : kOutOfRange,
+                 make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]));
     }
   }
 };
 
-template <int TERMS, bool BB, bool YB, int DK, int CG>
+template <int TERMS, bool BB, bool YB, int DK>
 __global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int splits, int stride) {
-  using E = Expand<TERMS, BB, YB, DK, CG>;
+  using E = Expand<TERMS, BB, YB, DK>;
+  constexpr int JT = E::JT;
   __shared__ Tiles tiles;
   __shared__ __align__(16) uint16_t terms[TERMS * E::kRows * E::kPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
   const int64_t row0 = (int64_t)blockIdx.y * kBlockRows;
   const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
-  const int col0 = blockIdx.x * E::kCols + wave * 32 * CG;
-  make_tiles(tiles, P.ids + row0, nr, P.n_adapters);
+  const int col = blockIdx.x * E::kCols + wave * 16 * JT + JT * n;  // the lane's first column
+  get_order(tiles, order_at(P) + blockIdx.y);
   constexpr int bs = BB ? 2 : 4, ys = YB ? 2 : 4;
   const __amdgpu_buffer_rsrc_t rbase =
       buffer_range(static_cast<const char*>(P.base) + row0 * P.n_out * bs,
                    P.base ? (int64_t)nr * P.n_out * bs : 0);
   const __amdgpu_buffer_rsrc_t ry =
       buffer_range(static_cast<char*>(P.y) + row0 * P.n_out * ys, (int64_t)nr * P.n_out * ys);
+  const float* const t_all = t_at(P);
   const int count = tiles.count;
   for (int tile = blockIdx.z; tile < count; tile += gridDim.z) {
     const Tile t = tile_at(tiles, tile, nr);
     const bool none = t.id == kNoAdapter;
     if (none && P.base == P.y) break;  // in place: those rows stay as they are
-    const __amdgpu_buffer_rsrc_t rb = none
-        ? buffer_range32(nullptr, 0)
-        : buffer_range(P.b + (int64_t)t.id * P.n_out * P.rank, (int64_t)P.n_out * P.rank * 2);
+    uint4 fb[JT][DK];
+    if (!none) {
+      const __amdgpu_buffer_rsrc_t rb = buffer_range(
+          P.b + (int64_t)t.id * P.n_out * P.rank, (int64_t)P.n_out * P.rank * 2);
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int d = 0; d < DK; ++d) {
+          const int r = d * 32 + 8 * g;
+          fb[j][d] = buf_ld16(rb, r < P.rank && col + j < P.n_out
+                                      ? ((uint32_t)(col + j) * (uint32_t)P.rank + r) * 2u
+                                      : kOutOfRange);
+        }
+    }
     for (int part = 0; part < t.len; part += E::kRows) {
       const int len = t.len - part < E::kRows ? t.len - part : E::kRows;
-      uint32_t ro[E::QN];
+      const int first = t.start + part;
+      // offsets of the lane's rows 16 q + 4 g + i, and their base one tile ahead
+      const auto rows_of = [&](int q, uint32_t (&ro)[4]) {
 #pragma unroll
-      for (int q = 0; q < E::QN; ++q) {
-        const int at = q * 16 + (lane & 15);
-        ro[q] = at < len ? (uint32_t)tiles.row(t.start + part + at) * (uint32_t)P.n_out
-                         : kOutOfRange;
-      }
-      typename E::Frag f[CG];
-      E::load(P, rb, rbase, ro, col0, none, f[0]);
+        for (int i = 0; i < 4; ++i) {
+          const int at = 16 * q + 4 * g + i;
+          ro[i] = at < len ? (uint32_t)tiles.row(first + at) * (uint32_t)P.n_out : kOutOfRange;
+        }
+      };
+      uint32_t ro[2][4];
+      typename E::Base base[2];
+      rows_of(0, ro[0]);
+      if (P.base) E::load_base(rbase, ro[0], col, P.n_out, base[0]);
       if (!none) {
         // the terms of s t, four ranks to a thread at a time
         const float s = P.scaling[t.id];
@@ -363,7 +436,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int spli
           const int r = i / (E::kDepth / 4), c = i % (E::kDepth / 4) * 4;
           f32x4 v = {0.f, 0.f, 0.f, 0.f};
           if (c < stride) {
-            const float* from = P.t + (row0 + tiles.row(t.start + part + r)) * stride + c;
+            const float* from = t_all + (row0 + tiles.row(first + r)) * stride + c;
 #pragma unroll 4
             for (int k = 0; k < splits; ++k)
               v += *reinterpret_cast<const f32x4*>(from + k * P.rows * stride);
@@ -380,9 +453,35 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int spli
         __syncthreads();
       }
 #pragma unroll
-      for (int cg = 0; cg < CG; ++cg) {
-        if (cg + 1 < CG) E::load(P, rb, rbase, ro, col0 + 32 * (cg + 1), none, f[cg + 1]);
-        E::finish(P, ry, terms, ro, col0 + 32 * cg, len, none, f[cg]);
+      for (int q = 0; q < E::QN; ++q) {
+        if (q * 16 >= len) break;
+        if (q + 1 < E::QN) {
+          rows_of(q + 1, ro[(q + 1) & 1]);
+          if (P.base) E::load_base(rbase, ro[(q + 1) & 1], col, P.n_out, base[(q + 1) & 1]);
+        }
+        f32x4 acc[JT];
+#pragma unroll
+        for (int j = 0; j < JT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (!none) {
+          const int at = q * 16 + n < len ? q * 16 + n : len - 1;
+#pragma unroll
+          for (int d = 0; d < DK; ++d)
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k) {
+              const uint4 ft = *reinterpret_cast<const uint4*>(
+                  terms + (k * E::kRows + at) * E::kPitch + d * 32 + 8 * g);
+#pragma unroll
+              for (int j = 0; j < JT; ++j) acc[j] = mfma(ft, fb[j][d], acc[j]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v[JT];
+#pragma unroll
+          for (int j = 0; j < JT; ++j)
+            v[j] = P.base ? acc[j][i] + E::base_at(base[q & 1], i, j) : acc[j][i];
+          E::store(ry, ro[q & 1][i], col, P.n_out, v);
+        }
       }
     }
   }
@@ -396,24 +495,32 @@ struct Cut {
   int64_t blocks;  // blocks of rows
   int splits, slice;  // of the k axis
 };
-// Workgroups that share a block's tiles: as many as it can have tiles, up to
-// a number that leaves few of them idle when there are many blocks.
+// Workgroups that share a block's tiles: as many as it can have tiles, and
+// where there are many blocks as many as packed prompts have (four, and one
+// more for every change of adapter within 256 rows): the others would start
+// only to find nothing, 257 rows of 32 adapters 36.3 us with 16 lanes and 31.0
+// with 33, 8192 rows of 6 adapters 137 us with 8 and no less with more.
 int tile_lanes(int64_t rows, int64_t blocks, int n_adapters) {
   const int64_t r = rows < kBlockRows ? rows : kBlockRows;
   const int64_t most = (r < n_adapters ? r : n_adapters) + r / kTileRows + 1;
-  const int64_t cap = blocks <= 2 ? 32 : blocks <= 8 ? 16 : 4;
+  const int64_t cap = blocks <= 2 ? 64 : blocks <= 8 ? 16 : 8;
   return (int)(most < cap ? most : cap);
 }
 Cut cut(int64_t rows, int k, int rank) {
   Cut c;
-  c.rt = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
+  c.rt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
   c.ranks = (rank + 16 * c.rt - 1) / (16 * c.rt);
   c.stride = c.ranks * c.rt * 16;
   c.blocks = (rows + kBlockRows - 1) / kBlockRows;
-  // tiles there are at least: one to 64 rows
+  // The k axis is split until there is a workgroup for every CU, counting one
+  // tile to 64 rows.  A workgroup takes 2048 k at least (257 rows, 32
+  // adapters, k = 11008, rank 64: 42 us with 512, 33 with 1024, 31 with 2048
+  // and 4096, 34 with 8192) and with a tile of rows 512, which the smallest
+  // calls wait for one after the other.
   const int64_t groups = (rows + kTileRows - 1) / kTileRows * c.ranks;
-  const int most = (k + 511) / 512;
-  const int64_t want = (512 + groups - 1) / groups;
+  const int run = rows <= kTileRows ? 512 : 2048;
+  const int most = (k + run - 1) / run;
+  const int64_t want = groups < 256 ? 256 / groups : 1;
   c.splits = (int)(want < most ? want : most);
   c.slice = ((k + c.splits - 1) / c.splits + 127) / 128 * 128;
   c.splits = (k + c.slice - 1) / c.slice;
@@ -428,33 +535,28 @@ void shrink(const LoraParams& p, const Cut& c, hipStream_t s) {
                      dim3(kThreads), 0, s, p, c.splits, c.slice, c.stride);
 }
 
-template <int TERMS, bool BB, bool YB, int DK, int CG>
+template <int TERMS, bool BB, bool YB, int DK>
 void expand(const LoraParams& p, const Cut& c, hipStream_t s) {
-  using E = Expand<TERMS, BB, YB, DK, CG>;
-  // few rows: a workgroup to a tile; many: a workgroup to a block
-  const int lanes = c.blocks <= 8 ? tile_lanes(p.rows, c.blocks, p.n_adapters) : 1;
-  hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB, DK, CG>),
-                     dim3((p.n_out + E::kCols - 1) / E::kCols, (unsigned)c.blocks, lanes),
+  using E = Expand<TERMS, BB, YB, DK>;
+  hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB, DK>),
+                     dim3((p.n_out + E::kCols - 1) / E::kCols, (unsigned)c.blocks,
+                          tile_lanes(p.rows, c.blocks, p.n_adapters)),
                      dim3(kThreads), 0, s, p, c.splits, c.stride);
 }
-template <int TERMS, bool BB, bool YB, int DK>
-void expand_cg(const LoraParams& p, const Cut& c, hipStream_t s) {
-  if (c.blocks <= 8) expand<TERMS, BB, YB, DK, 1>(p, c, s);
-  else expand<TERMS, BB, YB, DK, 2>(p, c, s);
-}
 template <int TERMS, bool BB, bool YB>
-void expand_dk(const LoraParams& p, const Cut& c, hipStream_t s) {
-  if (c.stride <= 32) expand_cg<TERMS, BB, YB, 1>(p, c, s);
-  else if (c.stride <= 64) expand_cg<TERMS, BB, YB, 2>(p, c, s);
-  else if (c.stride <= 128) expand_cg<TERMS, BB, YB, 4>(p, c, s);
-  else expand_cg<TERMS, BB, YB, 8>(p, c, s);
+void expand_by_rank(const LoraParams& p, const Cut& c, hipStream_t s) {
+  if (c.stride <= 32) expand<TERMS, BB, YB, 1>(p, c, s);
+  else if (c.stride <= 64) expand<TERMS, BB, YB, 2>(p, c, s);
+  else if (c.stride <= 128) expand<TERMS, BB, YB, 4>(p, c, s);
+  else expand<TERMS, BB, YB, 8>(p, c, s);
 }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t rows, int k, int rank) {
   const Cut c = cut(rows, k, rank);
-  return (size_t)c.splits * (size_t)rows * (size_t)c.stride * sizeof(float);
+  return (size_t)c.blocks * sizeof(Order) +
+         (size_t)c.splits * (size_t)rows * (size_t)c.stride * sizeof(float);
 }
 
 hipError_t launch_lora(const LoraParams& p, hipStream_t s) {
@@ -462,17 +564,16 @@ hipError_t launch_lora(const LoraParams& p, hipStream_t s) {
   switch (c.rt) {
     case 1: shrink<1>(p, c, s); break;
     case 2: shrink<2>(p, c, s); break;
-    case 4: shrink<4>(p, c, s); break;
-    default: shrink<8>(p, c, s); break;
+    default: shrink<4>(p, c, s); break;
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.y_bf16) {
-    if (p.base_bf16) expand_dk<2, true, true>(p, c, s);
-    else expand_dk<2, false, true>(p, c, s);
+    if (p.base_bf16) expand_by_rank<2, true, true>(p, c, s);
+    else expand_by_rank<2, false, true>(p, c, s);
   } else {
-    if (p.base_bf16) expand_dk<3, true, false>(p, c, s);
-    else expand_dk<3, false, false>(p, c, s);
+    if (p.base_bf16) expand_by_rank<3, true, false>(p, c, s);
+    else expand_by_rank<3, false, false>(p, c, s);
   }
   return hipGetLastError();
 }

@@ -107,6 +107,14 @@ def test_rows_and_orders(rows, ids):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("rank", [8, 40, 104, 176])
+@pytest.mark.parametrize("base,y", [(None, BF16), (F32, BF16), (BF16, F32), (F32, F32)])
+def test_many_rows(rank, base, y):
+    for ids in ("mixed", "runs"):
+        c = Case(2300, 136, 328, rank, 5, ids=ids, base=base, y=y)
+        c.check(c.run())
+
+
 @pytest.mark.parametrize("k", [8, 16, 120, 128, 136, 504, 512, 520, 1000, 4096, 11008])
 def test_depths(k):
     for rows in (3, 70):
