@@ -181,38 +181,48 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _scratch(device, workspace):
-    """A workspace (None: not given) is contiguous and lies on `device`."""
-    if workspace is not None and (workspace.get_device() != device or
-                                  not workspace.is_contiguous()):
+def _at(name, t, shape, dtypes, device):
+    """The address of a tensor (None: NULL) that has to be contiguous, of this
+    shape, of one of these types and on the GPU `device`."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError("%s is %s" % (name, t.dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s has to be contiguous of shape %s, got %s with strides %s"
+                         % (name, tuple(shape), tuple(t.shape), t.stride()))
+    if t.get_device() != device:
+        raise ValueError("%s is on another device than the first argument" % name)
+    return t.data_ptr()
+
+
+def _scratch(workspace, device):
+    """A workspace's address and bytes (None: NULL, 0)."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("the workspace has to be contiguous and on the first argument's device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _on(device, stream, call):
-    """call(stream handle) with `device` current: the caller's stream, or
-    torch's current one of that device."""
+def _call(name, device, stream, *args):
+    """The library's `name` with `args` and a stream: the caller's, or torch's
+    current one of the arguments' device, which is made current for the call."""
     import torch
+    if device < 0:
+        raise ValueError("%s: the tensors have to be on a GPU" % name)
+    f = getattr(lib(), name)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
     if torch.cuda.current_device() != device:
         with torch.cuda.device(device):
-            return call(_stream(stream))
-    return call(_stream(stream))
-
-
-def _expect(device, **tensors):
-    """Every tensor (None: not given) has its shape, is contiguous and lies on
-    the GPU `device`.  tensors: name=(tensor, shape, dtypes)."""
-    if device < 0:
-        raise ValueError("the tensors have to be on a GPU")
-    for name, (t, shape, dtypes) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype not in dtypes:
-            raise TypeError("%s is %s" % (name, t.dtype))
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError("%s has to be contiguous of shape %s, got %s with strides %s"
-                             % (name, tuple(shape), tuple(t.shape), t.stride()))
-        if t.get_device() != device:
-            raise ValueError("%s is on another device than the first argument" % name)
+            status = f(*args, stream)
+    else:
+        status = f(*args, stream)
+    if status != 0:
+        raise BflyError(status, name)
 
 
 def _table_ws(n, theta, coeffs, workspace, like):
@@ -406,14 +416,19 @@ def bfly_calib_step_weight(x, w, theta, adam_m, adam_v, step: int, cfg: bfly_cal
 # the norm in front of a layer, adapters beside its product, clipping
 # ---------------------------------------------------------------------------
 
-def _row_types():
-    import torch
-    return torch.float32, torch.bfloat16
+_types = None
 
 
-def _one_byte():
-    import torch
-    return torch.int8, torch.uint8, torch.float8_e4m3fn
+def _dtypes():
+    """(rows, bfloat16, float32, float16, one byte, int32): the torch types
+    that the calls below take, and the bfly_dtype of the rows'."""
+    global _types
+    if _types is None:
+        import torch
+        _types = ({torch.float32: BFLY_F32, torch.bfloat16: BFLY_BF16}, (torch.bfloat16,),
+                  (torch.float32,), (torch.float16,),
+                  (torch.int8, torch.uint8, torch.float8_e4m3fn), (torch.int32,))
+    return _types
 
 
 def bfly_rmsnorm(x, weight, eps, y=None, codes=None, scales=None, residual=None, h=None, rstd=None,
@@ -423,21 +438,19 @@ def bfly_rmsnorm(x, weight, eps, y=None, codes=None, scales=None, residual=None,
     bfloat16; codes: [rows, n] of one byte an element with scales [rows,
     n/group] float16 (group None: one scale per row); rstd: [rows] float32;
     weight: [n] or None (ones).  Outputs that are None are not computed."""
-    import torch
-    rows, n = x.shape
+    row, _, f32, f16, byte, _ = _dtypes()
+    shape = rows, n = x.shape
     if group is None or codes is None:
         group = n
-    f = _row_types()
     dev = x.get_device()
-    _expect(dev, x=(x, (rows, n), f), residual=(residual, (rows, n), (x.dtype,)),
-            h=(h, (rows, n), (x.dtype,)), weight=(weight, (n,), f), y=(y, (rows, n), f),
-            codes=(codes, (rows, n), _one_byte()),
-            scales=(scales, (rows, n // group if group > 0 else 0), (torch.float16,)),
-            rstd=(rstd, (rows,), (torch.float32,)))
-    _check(_on(dev, stream, lambda s: lib().bfly_rmsnorm(
-        _ptr(x), _dt(x), _ptr(residual), _ptr(h), _ptr(weight),
-        0 if weight is None else _dt(weight), _ptr(y), 0 if y is None else _dt(y), _ptr(codes),
-        _ptr(scales), _ptr(rstd), rows, n, eps, format, group, s)), "bfly_rmsnorm")
+    same = (x.dtype,)
+    _call("bfly_rmsnorm", dev, stream, _at("x", x, shape, row, dev), row[x.dtype],
+          _at("residual", residual, shape, same, dev), _at("h", h, shape, same, dev),
+          _at("weight", weight, (n,), row, dev), 0 if weight is None else row[weight.dtype],
+          _at("y", y, shape, row, dev), 0 if y is None else row[y.dtype],
+          _at("codes", codes, shape, byte, dev),
+          _at("scales", scales, (rows, n // group if group > 0 else 0), f16, dev),
+          _at("rstd", rstd, (rows,), f32, dev), rows, n, eps, format, group)
 
 
 def bfly_rmsnorm_backward_workspace_bytes(rows: int, n: int) -> int:
@@ -450,19 +463,16 @@ def bfly_rmsnorm_backward(h, weight, rstd, dy, dx, dweight=None, dh=None, worksp
     gradient.  h: [rows, n]; dy, dh, dx: [rows, n] of one type; rstd: [rows]
     and dweight: [n] float32; workspace: a uint8 tensor of
     bfly_rmsnorm_backward_workspace_bytes (needed with dweight)."""
-    import torch
-    rows, n = h.shape
-    f = _row_types()
+    row, _, f32, _, _, _ = _dtypes()
+    shape = rows, n = h.shape
     dev = h.get_device()
-    _expect(dev, h=(h, (rows, n), f), weight=(weight, (n,), f),
-            rstd=(rstd, (rows,), (torch.float32,)), dy=(dy, (rows, n), f),
-            dx=(dx, (rows, n), (dy.dtype,)), dh=(dh, (rows, n), (dy.dtype,)),
-            dweight=(dweight, (n,), (torch.float32,)))
-    _scratch(dev, workspace)
-    _check(_on(dev, stream, lambda s: lib().bfly_rmsnorm_backward(
-        _ptr(h), _dt(h), _ptr(weight), 0 if weight is None else _dt(weight), _ptr(rstd), _ptr(dy),
-        _ptr(dh), _ptr(dx), _dt(dy), _ptr(dweight), rows, n, _ptr(workspace), _nbytes(workspace),
-        s)), "bfly_rmsnorm_backward")
+    same = (dy.dtype,)
+    ws, ws_bytes = _scratch(workspace, dev)
+    _call("bfly_rmsnorm_backward", dev, stream, _at("h", h, shape, row, dev), row[h.dtype],
+          _at("weight", weight, (n,), row, dev), 0 if weight is None else row[weight.dtype],
+          _at("rstd", rstd, (rows,), f32, dev), _at("dy", dy, shape, row, dev),
+          _at("dh", dh, shape, same, dev), _at("dx", dx, shape, same, dev), row[dy.dtype],
+          _at("dweight", dweight, (n,), f32, dev), rows, n, ws, ws_bytes)
 
 
 def bfly_lora_matmul_workspace_bytes(rows: int, n_out: int, k: int, rank: int) -> int:
@@ -477,21 +487,19 @@ def bfly_lora_matmul(x, ids, lora_a, lora_b, scaling, y, workspace, base=None,
     bfloat16; scaling: [adapters] float32; base, y: [rows, n_out] float32 or
     bfloat16 (base None: zeros; y may be base); workspace: a uint8 tensor of
     bfly_lora_matmul_workspace_bytes."""
-    import torch
+    row, bf, f32, _, _, i32 = _dtypes()
     rows, k = x.shape
-    num, rank = lora_a.shape[:2]
-    n_out = y.shape[1]
-    f, bf = _row_types(), (torch.bfloat16,)
+    num, rank, _ = lora_a.shape
+    shape = _, n_out = y.shape
     dev = x.get_device()
-    _expect(dev, x=(x, (rows, k), bf), ids=(ids, (rows,), (torch.int32,)),
-            lora_a=(lora_a, (num, rank, k), bf), lora_b=(lora_b, (num, n_out, rank), bf),
-            scaling=(scaling, (num,), (torch.float32,)), base=(base, (rows, n_out), f),
-            y=(y, (rows, n_out), f))
-    _scratch(dev, workspace)
-    _check(_on(dev, stream, lambda s: lib().bfly_lora_matmul(
-        _ptr(x), BFLY_BF16, _ptr(ids), _ptr(lora_a), _ptr(lora_b), _ptr(scaling), _ptr(base),
-        0 if base is None else _dt(base), _ptr(y), _dt(y), rows, n_out, k, num, rank,
-        _ptr(workspace), _nbytes(workspace), s)), "bfly_lora_matmul")
+    ws, ws_bytes = _scratch(workspace, dev)
+    _call("bfly_lora_matmul", dev, stream, _at("x", x, (rows, k), bf, dev), BFLY_BF16,
+          _at("ids", ids, (rows,), i32, dev), _at("lora_a", lora_a, (num, rank, k), bf, dev),
+          _at("lora_b", lora_b, (num, n_out, rank), bf, dev),
+          _at("scaling", scaling, (num,), f32, dev),
+          _at("base", base, shape, row, dev), 0 if base is None else row[base.dtype],
+          _at("y", y, (rows, n_out), row, dev), row[y.dtype], rows, n_out, k, num, rank, ws,
+          ws_bytes)
 
 
 def bfly_grad_clip_workspace_bytes(count: int) -> int:
@@ -504,24 +512,28 @@ def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> 
     and every gradient times norm[1], in place or into `outs`.  norm: [2]
     float32; workspace: a uint8 tensor of bfly_grad_clip_workspace_bytes."""
     import torch
+    from array import array
+    row, _, f32, _, _, _ = _dtypes()
+    T = torch.Tensor
+    dtype = T.dtype.__get__
     dev = norm.get_device()
-    _expect(dev, norm=(norm, (2,), (torch.float32,)))
-    _scratch(dev, workspace)
+    ws, ws_bytes = _scratch(workspace, dev)
     num = len(grads)
-    if outs is not None and len(outs) != num:
-        raise ValueError("%d gradients and %d outputs" % (num, len(outs)))
-    for i, t in enumerate(grads):
-        if not t.is_contiguous() or t.get_device() != dev:
-            raise ValueError("gradient %d has to be contiguous and on norm's device" % i)
-        if outs is not None:
-            o = outs[i]
-            if o.dtype != t.dtype or o.numel() != t.numel() or not o.is_contiguous() or \
-                    o.get_device() != dev:
-                raise ValueError("output %d has to be like its gradient" % i)
-    ptrs = ctypes.c_void_p * num
-    _check(_on(dev, stream, lambda s: lib().bfly_grad_clip(
-        num, ptrs(*[t.data_ptr() for t in grads]),
-        None if outs is None else ptrs(*[t.data_ptr() for t in outs]),
-        (ctypes.c_int64 * num)(*[t.numel() for t in grads]),
-        (ctypes.c_int32 * num)(*[_dt(t) for t in grads]), max_norm, _ptr(norm), _ptr(workspace),
-        _nbytes(workspace), s)), "bfly_grad_clip")
+    numels, types = array("q", map(T.numel, grads)), list(map(dtype, grads))
+    if not set(types) <= row.keys():
+        raise TypeError("libbfly takes float32 or bfloat16 gradients")
+    given = [grads]
+    if outs is not None:
+        if array("q", map(T.numel, outs)) != numels or list(map(dtype, outs)) != types:
+            raise ValueError("the outputs have to be like their gradients")
+        given.append(outs)
+    for tensors in given:
+        if not all(map(T.is_contiguous, tensors)):
+            raise ValueError("the gradients and outputs have to be contiguous")
+        if not set(map(T.get_device, tensors)) <= {dev}:
+            raise ValueError("the gradients and outputs have to be on norm's device")
+    kinds = array("i", [row[t] for t in types])
+    ptrs = [array("Q", map(T.data_ptr, tensors)) for tensors in given]
+    at = [a.buffer_info()[0] if num else None for a in (*ptrs, numels, kinds)]
+    _call("bfly_grad_clip", dev, stream, num, at[0], at[1] if outs is not None else None, at[-2],
+          at[-1], max_norm, _at("norm", norm, (2,), f32, dev), ws, ws_bytes)

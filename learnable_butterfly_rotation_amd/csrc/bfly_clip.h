@@ -6,22 +6,24 @@
 
 namespace bfly {
 
-// The tensors are cut into granules of kClipGranule elements (a tensor's last
-// one may be shorter), numbered through all tensors; a slot is a run of
-// consecutive granules, summed by one workgroup.
+// The tensors are cut into granules of kClipGranule elements, numbered through
+// all tensors; a slot is a run of consecutive granules, summed by one
+// workgroup.  A tensor's granules start at the 16-byte boundary at or below
+// its first element, so that every whole vector in them is aligned.
 constexpr int kClipGranule = 4096;
 constexpr int kClipSlots = 1024;
 
-inline int64_t clip_granules(int64_t numel) { return (numel + kClipGranule - 1) / kClipGranule; }
-
-// One tensor in the workspace's table.
+// One tensor of the table.
 struct ClipTensor {
-  const void* in;
-  void* out;
-  int64_t numel;
-  int32_t first;  // its first granule
-  int32_t bf16;   // 1: bf16, 0: fp32
+  const char* in;  // that boundary
+  char* out;       // the output's address of it
+  int64_t end;     // elements from there to the tensor's end
+  int32_t first;   // the tensor's first granule
+  int32_t kind;    // 1: bf16, 0: fp32; + 2 * the elements before the tensor's first
 };
+// Tensors whose table goes into a launch's arguments; for more of them it is
+// written to the workspace first, this many to a launch.
+constexpr int kClipBatch = 112;
 
 // Workspace: the slots' sums of squares, then the table.
 constexpr size_t kClipTableOffset = kClipSlots * sizeof(double);

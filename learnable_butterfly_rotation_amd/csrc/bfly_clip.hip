@@ -6,19 +6,22 @@
 // Squares are summed in fp64 (an fp32 square overflows above 1.8e19 and loses
 // everything below 1e-23, and a sum over 10^9 elements loses half its digits).
 // Two passes over the data: the slots' sums, then the scaling, whose every
-// workgroup first adds the (at most 1024) slot sums in a fixed order.
+// workgroup first adds the (at most 1024) slot sums in a fixed order.  Both
+// are bound by memory.
 #include "bfly_clip.h"
 #include "bfly_rows.h"
+
+#include <string.h>
 
 namespace bfly {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;  // vectors of a thread in flight
 
-// The table's entries of up to kBatch tensors, as kernel arguments.
-constexpr int kBatch = 120;
+// The table's entries of up to kClipBatch tensors, as kernel arguments.
 struct Batch {
-  ClipTensor t[kBatch];
+  ClipTensor t[kClipBatch];
 };
 __global__ void __launch_bounds__(128) table_kernel(Batch b, int count, ClipTensor* to) {
   const int i = threadIdx.x;
@@ -31,70 +34,104 @@ __device__ __forceinline__ int find_tensor(const ClipTensor* tab, int count, int
   for (int i = threadIdx.x; i < count; i += kThreads)
     if (tab[i].first <= g && (i + 1 == count || tab[i + 1].first > g)) *found = i;
   __syncthreads();
-  return *found;
+  return __builtin_amdgcn_readfirstlane(*found);
 }
 
-// One granule's elements of thread t, four at a time: 16-byte loads of fp32
-// or 8-byte loads of bf16 where the tensor is aligned to them, else single
-// elements.  f(values, offset of the first, how many are valid).
-template <typename F>
-__device__ __forceinline__ void each_four(const ClipTensor& c, int64_t at, int len, F f) {
-  const int t = threadIdx.x;
-  if (c.bf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(c.in) + at;
-    const bool wide = ((uintptr_t)p & 7) == 0;
+// A 16-byte vector of a tensor's elements, as fp32.
+template <bool BF>
+struct Vec {
+  static constexpr int W = BF ? 8 : 4;
+  float v[W];
+  __device__ __forceinline__ void load(const char* p) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int k = 0; k < kClipGranule / (4 * kThreads); ++k) {
-      const int i = (k * kThreads + t) * 4, m = len - i < 4 ? len - i : 4;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (wide && m == 4) {
-        const uint2 q = *reinterpret_cast<const uint2*>(p + i);
-        v[0] = bf16_lo(q.x);
-        v[1] = bf16_hi(q.x);
-        v[2] = bf16_lo(q.y);
-        v[3] = bf16_hi(q.y);
-      } else {
+    for (int e = 0; e < W; ++e)
+      v[e] = !BF ? __uint_as_float(w[e]) : (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+  }
+  // elements [lo, hi) of the vector, the others 0
+  __device__ __forceinline__ void load_some(const char* p, int lo, int hi) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < m) v[e] = bf16_lo(p[i + e]);
-      }
-      f(v, i, m);
+    for (int e = 0; e < W; ++e) {
+      v[e] = 0.f;
+      if (e >= lo && e < hi)
+        v[e] = BF ? bf16_lo(reinterpret_cast<const uint16_t*>(p)[e])
+                  : reinterpret_cast<const float*>(p)[e];
     }
-  } else {
-    const float* p = static_cast<const float*>(c.in) + at;
-    const bool wide = ((uintptr_t)p & 15) == 0;
+  }
+  __device__ __forceinline__ void words(uint32_t (&w)[4]) const {
 #pragma unroll
-    for (int k = 0; k < kClipGranule / (4 * kThreads); ++k) {
-      const int i = (k * kThreads + t) * 4, m = len - i < 4 ? len - i : 4;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (wide && m == 4) {
-        const float4 q = *reinterpret_cast<const float4*>(p + i);
-        v[0] = q.x;
-        v[1] = q.y;
-        v[2] = q.z;
-        v[3] = q.w;
-      } else {
+    for (int i = 0; i < 4; ++i)
+      w[i] = BF ? pack_bf16(v[(2 * i) % W], v[(2 * i + 1) % W]) : __float_as_uint(v[i]);
+  }
+  __device__ __forceinline__ void store(char* p) const {
+    uint32_t w[4];
+    words(w);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store_some(char* p, int lo, int hi) const {
+    uint32_t w[4];
+    words(w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < m) v[e] = p[i + e];
+    for (int e = 0; e < W; ++e)
+      if (e >= lo && e < hi) {
+        if constexpr (BF) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        else reinterpret_cast<uint32_t*>(p)[e] = w[e];
       }
-      f(v, i, m);
+  }
+};
+
+// The elements [from, to) of a tensor, counted from its boundary, vector by
+// vector over the workgroup: f(vector, offset of it, first and last + 1 of
+// its elements that are the tensor's).  Vectors in pairs of four whole ones
+// where there are, whose loads are in flight together.
+template <bool BF, typename F>
+__device__ __forceinline__ void each_vector(const char* in, int64_t from, int64_t to, F f) {
+  using V = Vec<BF>;
+  constexpr int es = BF ? 2 : 4, W = V::W, step = kThreads * W;
+  const int64_t first = from / W * W;  // of a vector; from is inside it
+  int64_t at = first + threadIdx.x * W;
+  V v[kAhead];
+  if (from > first) {  // the tensor starts inside its first vector
+    if (threadIdx.x == 0) {
+      const int hi = to - at < W ? (int)(to - at) : W;
+      v[0].load_some(in + at * es, (int)(from - first), hi);
+      f(v[0], at, (int)(from - first), hi);
+    }
+    if (threadIdx.x == 0) at += step;
+  }
+  for (; at + (kAhead - 1) * step + W <= to; at += kAhead * step) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) v[k].load(in + (at + k * step) * es);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) f(v[k], at + k * step, 0, W);
+  }
+  for (; at < to; at += step) {
+    if (at + W <= to) {
+      v[0].load(in + at * es);
+      f(v[0], at, 0, W);
+    } else {
+      v[0].load_some(in + at * es, 0, (int)(to - at));
+      f(v[0], at, 0, (int)(to - at));
     }
   }
 }
 
-// Calls f(tensor, offset of the granule in it, its length) for a slot's granules.
+// Calls f(tensor, from, to) for a slot's granules, one range to a tensor.
 template <typename F>
-__device__ __forceinline__ void each_granule(const ClipTensor* tab, int count, int g0, int g1,
-                                             int* found, F f) {
+__device__ __forceinline__ void each_range(const ClipTensor* tab, int count, int g0, int g1,
+                                           int* found, F f) {
   if (g0 >= g1) return;
   int i = find_tensor(tab, count, g0, found);
-  for (int g = g0; g < g1; ++g) {
-    while (i + 1 < count && tab[i + 1].first <= g) ++i;
+  for (int g = g0; g < g1; ++i) {
     const ClipTensor c = tab[i];
-    const int64_t at = (int64_t)(g - c.first) * kClipGranule;
-    const int64_t left = c.numel - at;
-    f(c, at, (int)(left < kClipGranule ? left : kClipGranule));
+    const int next = i + 1 < count ? tab[i + 1].first : g1;
+    const int stop = next < g1 ? next : g1;
+    const int64_t skip = c.kind >> 1;
+    const int64_t from = (int64_t)(g - c.first) * kClipGranule;
+    const int64_t to = (int64_t)(stop - c.first) * kClipGranule;
+    f(c, from > skip ? from : skip, to < c.end ? to : c.end);
+    g = stop;
   }
 }
 
@@ -105,35 +142,40 @@ __device__ __forceinline__ double block_total(double v, double* buf) {
   return (buf[0] + buf[1]) + (buf[2] + buf[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) square_kernel(const ClipTensor* tab, int count,
-                                                          int granules, int per_slot,
-                                                          double* sums) {
+// How the granules are dealt out, and the table: `in_args` of it in the
+// launch's arguments, or all of it in memory.
+struct Slots {
+  const ClipTensor* table;  // nullptr: the batch
+  int count, granules, per_slot, slots;
+};
+
+__device__ __forceinline__ void square_slot(const ClipTensor* tab, const Slots& S, double* sums) {
   __shared__ int found;
   __shared__ double buf[kThreads / 64];
-  const int g0 = blockIdx.x * per_slot;
-  const int g1 = g0 + per_slot < granules ? g0 + per_slot : granules;
+  const int g0 = blockIdx.x * S.per_slot;
+  const int g1 = g0 + S.per_slot < S.granules ? g0 + S.per_slot : S.granules;
   double s = 0.0;
-  each_granule(tab, count, g0, g1, &found, [&](const ClipTensor& c, int64_t at, int len) {
-    each_four(c, at, len, [&](const float (&v)[4], int, int) {
+  each_range(tab, S.count, g0, g1, &found, [&](const ClipTensor& c, int64_t from, int64_t to) {
+    const auto add = [&](const auto& v, int64_t, int, int) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s = fma((double)v[e], (double)v[e], s);
-    });
+      for (float e : v.v) s = fma((double)e, (double)e, s);
+    };
+    if (c.kind & 1) each_vector<true>(c.in, from, to, add);
+    else each_vector<false>(c.in, from, to, add);
   });
   s = block_total(s, buf);
   if (threadIdx.x == 0) sums[blockIdx.x] = s;
 }
 
-__global__ void __launch_bounds__(kThreads) scale_kernel(const ClipTensor* tab, int count,
-                                                         int granules, int per_slot, int slots,
-                                                         const double* sums, float max_norm,
-                                                         float* norm) {
+__device__ __forceinline__ void scale_slot(const ClipTensor* tab, const Slots& S,
+                                           const double* sums, float max_norm, float* norm) {
   __shared__ int found;
   __shared__ double buf[kThreads / 64];
   double s = 0.0;
 #pragma unroll
   for (int k = 0; k < kClipSlots / kThreads; ++k) {
     const int i = k * kThreads + threadIdx.x;
-    s += i < slots ? sums[i] : 0.0;
+    s += i < S.slots ? sums[i] : 0.0;
   }
   const double all = sqrt(block_total(s, buf));
   // a norm that is not finite scales nothing: it is reported, and the caller drops the step
@@ -142,34 +184,37 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const ClipTensor* tab, 
     norm[0] = (float)all;
     norm[1] = c;
   }
-  const int g0 = blockIdx.x * per_slot;
-  const int g1 = g0 + per_slot < granules ? g0 + per_slot : granules;
-  each_granule(tab, count, g0, g1, &found, [&](const ClipTensor& t, int64_t at, int len) {
+  const int g0 = blockIdx.x * S.per_slot;
+  const int g1 = g0 + S.per_slot < S.granules ? g0 + S.per_slot : S.granules;
+  each_range(tab, S.count, g0, g1, &found, [&](const ClipTensor& t, int64_t from, int64_t to) {
     if (c == 1.f && t.in == t.out) return;  // in place and not scaled: nothing to write
-    each_four(t, at, len, [&](const float (&v)[4], int i, int m) {
-      if (m <= 0) return;
-      if (t.bf16) {
-        uint16_t* o = static_cast<uint16_t*>(t.out) + at + i;
-        const uint2 q = make_uint2(pack_bf16(v[0] * c, v[1] * c), pack_bf16(v[2] * c, v[3] * c));
-        if (m == 4 && ((uintptr_t)o & 7) == 0) {
-          *reinterpret_cast<uint2*>(o) = q;
-        } else {
+    const bool wide = ((uintptr_t)t.out & 15) == 0;  // the output is aligned as the input is
+    const auto put = [&](auto v, int64_t at, int lo, int hi) {
+      constexpr int W = decltype(v)::W;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < m) o[e] = (uint16_t)((e < 2 ? q.x : q.y) >> (16 * (e & 1)));
-        }
-      } else {
-        float* o = static_cast<float*>(t.out) + at + i;
-        if (m == 4 && ((uintptr_t)o & 15) == 0) {
-          *reinterpret_cast<float4*>(o) = make_float4(v[0] * c, v[1] * c, v[2] * c, v[3] * c);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < m) o[e] = v[e] * c;
-        }
-      }
-    });
+      for (float& e : v.v) e *= c;
+      char* const o = t.out + at * (16 / W);
+      if (wide && hi - lo == W) v.store(o);
+      else v.store_some(o, lo, hi);
+    };
+    if (t.kind & 1) each_vector<true>(t.in, from, to, put);
+    else each_vector<false>(t.in, from, to, put);
   });
+}
+
+__global__ void __launch_bounds__(kThreads) square_kernel(Slots S, double* sums) {
+  square_slot(S.table, S, sums);
+}
+__global__ void __launch_bounds__(kThreads) square_few_kernel(Batch b, Slots S, double* sums) {
+  square_slot(b.t, S, sums);
+}
+__global__ void __launch_bounds__(kThreads) scale_kernel(Slots S, const double* sums,
+                                                         float max_norm, float* norm) {
+  scale_slot(S.table, S, sums, max_norm, norm);
+}
+__global__ void __launch_bounds__(kThreads) scale_few_kernel(Batch b, Slots S, const double* sums,
+                                                             float max_norm, float* norm) {
+  scale_slot(b.t, S, sums, max_norm, norm);
 }
 
 }  // namespace
@@ -178,36 +223,47 @@ hipError_t launch_grad_clip(const ClipParams& p, hipStream_t s) {
   double* sums = static_cast<double*>(p.workspace);
   ClipTensor* tab = reinterpret_cast<ClipTensor*>(static_cast<char*>(p.workspace) + kClipTableOffset);
   int64_t granules = 0;
-  int count = 0;
+  int count = 0, held = 0;  // tensors that are not empty; those of them in the batch
+  for (int i = 0; i < p.count; ++i) count += p.numel[i] > 0;
+  const bool few = count <= kClipBatch;
   Batch b;
-  int filled = 0;
-  for (int i = 0; i <= p.count; ++i) {
-    if (filled == kBatch || (i == p.count && filled > 0)) {
-      hipLaunchKernelGGL(table_kernel, dim3(1), dim3(128), 0, s, b, filled, tab + count - filled);
+  memset(&b, 0, sizeof(b));
+  for (int i = 0, at = 0; i < p.count; ++i) {
+    if (p.numel[i] == 0) continue;
+    ClipTensor& t = b.t[held++];
+    const int es = p.dtype[i] ? 2 : 4;
+    const int skip = (int)((uintptr_t)p.in[i] & 15) / es;
+    t.in = static_cast<const char*>(p.in[i]) - skip * es;
+    t.out = static_cast<char*>(p.out[i]) - skip * es;
+    t.end = p.numel[i] + skip;
+    t.first = (int32_t)granules;
+    t.kind = p.dtype[i] + 2 * skip;
+    granules += (t.end + kClipGranule - 1) / kClipGranule;
+    ++at;
+    if (!few && (held == kClipBatch || at == count)) {
+      hipLaunchKernelGGL(table_kernel, dim3(1), dim3(128), 0, s, b, held, tab + at - held);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      filled = 0;
+      held = 0;
     }
-    if (i == p.count || p.numel[i] == 0) continue;
-    ClipTensor& t = b.t[filled++];
-    t.in = p.in[i];
-    t.out = p.out[i];
-    t.numel = p.numel[i];
-    t.first = (int32_t)granules;
-    t.bf16 = p.dtype[i];
-    granules += clip_granules(p.numel[i]);
-    ++count;
   }
-  const int64_t per_slot = granules > kClipSlots ? (granules + kClipSlots - 1) / kClipSlots : 1;
-  const int slots = (int)((granules + per_slot - 1) / per_slot);
-  if (slots > 0) {
-    hipLaunchKernelGGL(square_kernel, dim3(slots), dim3(kThreads), 0, s, tab, count, (int)granules,
-                       (int)per_slot, sums);
+  Slots S;
+  S.table = tab;
+  S.count = count;
+  S.granules = (int)granules;
+  S.per_slot = (int)(granules > kClipSlots ? (granules + kClipSlots - 1) / kClipSlots : 1);
+  S.slots = (int)((granules + S.per_slot - 1) / S.per_slot);
+  if (S.slots > 0) {
+    if (few) hipLaunchKernelGGL(square_few_kernel, dim3(S.slots), dim3(kThreads), 0, s, b, S, sums);
+    else hipLaunchKernelGGL(square_kernel, dim3(S.slots), dim3(kThreads), 0, s, S, sums);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(scale_kernel, dim3(slots > 0 ? slots : 1), dim3(kThreads), 0, s, tab, count,
-                     (int)granules, (int)per_slot, slots, sums, p.max_norm, p.norm);
+  const dim3 grid(S.slots > 0 ? S.slots : 1);
+  if (few)
+    hipLaunchKernelGGL(scale_few_kernel, grid, dim3(kThreads), 0, s, b, S, sums, p.max_norm, p.norm);
+  else
+    hipLaunchKernelGGL(scale_kernel, grid, dim3(kThreads), 0, s, S, sums, p.max_norm, p.norm);
   return hipGetLastError();
 }
 

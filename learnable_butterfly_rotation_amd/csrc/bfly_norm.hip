@@ -55,13 +55,19 @@ __device__ __forceinline__ _Float16 group_scale(float amax, float top) {
   return (_Float16)fminf(amax / top, 65504.f);
 }
 
-// The codes of eight values, four to a word (d = the group's scale, 0: codes 0).
+// The codes of eight values, four to a word; d the group's scale, r = 1 / d
+// (0 for a zero scale: codes 0).  y / d is the IEEE quotient, as a division
+// gives it: r is the rounded reciprocal and d has 11 bits, so one correction
+// of y r by its exact remainder rounds the quotient correctly (Markstein).
 template <bool E4M3>
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float d) {
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float d, float r) {
   constexpr float top = E4M3 ? 448.f : 127.f;
   float q[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = d > 0.f ? fminf(fmaxf(y[e] / d, -top), top) : 0.f;
+  for (int e = 0; e < 8; ++e) {
+    const float q0 = y[e] * r;
+    q[e] = __builtin_amdgcn_fmed3f(fmaf(fmaf(-q0, d, y[e]), r, q0), -top, top);
+  }
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -69,14 +75,18 @@ __device__ __forceinline__ uint2 codes8(const float (&y)[8], float d) {
       int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
       w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], v, true);
     } else {
-      w[i] = 0;
+      // 1.5 * 2^23 + q is rounded to nearest even at the unit: its low byte is the code
+      uint32_t u[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[i] |= ((uint32_t)(int)rintf(q[4 * i + e]) & 0xFFu) << (8 * e);
+      for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(q[4 * i + e] + 12582912.f);
+      w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[3], u[2], 0x0C0C0400u),
+                                   __builtin_amdgcn_perm(u[1], u[0], 0x0C0C0400u), 0x05040100u);
     }
   }
-  return make_uint2(w[0], w[1]);
+  const uint32_t any = d > 0.f ? ~0u : 0u;  // a zero scale: no negative zero either
+  return make_uint2(w[0] & any, w[1] & any);
 }
+__device__ __forceinline__ float reciprocal(float d) { return d > 0.f ? 1.f / d : 0.f; }
 
 // T threads to a row, V chunks of eight elements to a thread; VEC: n is a
 // multiple of 8 (RowIo).  Q: 0 no codes, 1 int8, 2 e4m3.
@@ -108,20 +118,23 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
     }
   }
 
-  int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < P.rows;
-       row0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
-    const int64_t row = row0 + sub;
-    if (row >= P.rows) break;  // only rows of one wave (T = 64): no barrier is missed
-    const __amdgpu_buffer_rsrc_t rx = row_range(P.x, row, n, es);
-    const __amdgpu_buffer_rsrc_t rr = row_range(P.residual, row, n, es);
-    typename X::Raw qx[V], qr[V];
+  typename X::Raw qx[V], qr[V];
+  const auto load = [&](int64_t row) {  // past the last row: nothing is read
+    const int len = row < P.rows ? n : 0;
+    const __amdgpu_buffer_rsrc_t rx = row_range(P.x, row < P.rows ? row : 0, len, es);
 #pragma unroll
     for (int v = 0; v < V; ++v) qx[v] = X::load(rx, t, v);
     if (P.residual) {
+      const __amdgpu_buffer_rsrc_t rr = row_range(P.residual, row < P.rows ? row : 0, len, es);
 #pragma unroll
       for (int v = 0; v < V; ++v) qr[v] = X::load(rr, t, v);
     }
+  };
+  int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + sub;
+  load(row);
+  for (; row < P.rows; row += step, turn ^= 1) {  // uniform over the rows' threads
     float h[V][8];
     if (P.residual) {
       const __amdgpu_buffer_rsrc_t rh = row_range(P.h, row, n, es);
@@ -140,6 +153,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
 #pragma unroll
       for (int v = 0; v < V; ++v) X::unpack(qx[v], h[v]);
     }
+    load(row + step);  // the next row's, in flight during this one's work
     double ss = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -171,7 +185,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
       const __amdgpu_buffer_rsrc_t rc = row_range(P.codes, row, n, 1);
       const int per_row = n / P.group;
       uint16_t* const sc = P.scales + row * per_row;
-      float d = 0.f;
+      float d = 0.f, r = 0.f;
       if (P.group == n) {  // one scale for the row
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -180,6 +194,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
         top = block_max<T>(run_max(top, 64), tops[turn], t);
         const _Float16 s = group_scale(top, qtop);
         d = (float)s;
+        r = reciprocal(d);
         if (t == 0) sc[0] = __builtin_bit_cast(uint16_t, s);
       }
 #pragma unroll
@@ -191,11 +206,12 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
           m = run_max(m, P.group >> 3);
           const _Float16 s = group_scale(m, qtop);
           d = (float)s;
+          r = reciprocal(d);
           const int i = X::index(t, v, 0);
           if (i < n && (i & (P.group - 1)) == 0)
             sc[i / P.group] = __builtin_bit_cast(uint16_t, s);
         }
-        const uint2 c = codes8<Q == 2>(h[v], d);
+        const uint2 c = codes8<Q == 2>(h[v], d, r);
         if constexpr (VEC) {
           typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
           const u32x2 cw = {c.x, c.y};
@@ -221,6 +237,8 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
 template <int T, int V, bool VEC, bool HB, bool GB>
 __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdParams P) {
   constexpr int RPB = T < 256 ? 256 / T : 1;
+  // a second row's loads, where the registers of a thread hold them
+  constexpr bool AHEAD = T < 1024;
   __shared__ float sums[2][T / 64];
   using H = RowIo<T, VEC, HB>;
   using G = RowIo<T, VEC, GB>;
@@ -247,25 +265,36 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
     }
   }
 
-  int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < P.rows;
-       row0 += (int64_t)gridDim.x * RPB, turn ^= 1) {
-    const int64_t row = row0 + sub;
-    if (row >= P.rows) break;  // only rows of one wave (T = 64): no barrier is missed
-    const __amdgpu_buffer_rsrc_t rh = row_range(P.h, row, n, HB ? 2 : 4);
-    const __amdgpu_buffer_rsrc_t rg = row_range(P.dy, row, n, GB ? 2 : 4);
-    const __amdgpu_buffer_rsrc_t rd = row_range(P.dh, row, n, GB ? 2 : 4);
-    typename H::Raw qh[V];
-    typename G::Raw qg[V], qd[V];
+  typename H::Raw qh[V];
+  typename G::Raw qg[V], qd[V];
+  float rstd;
+  const auto load = [&](int64_t row, typename H::Raw (&h)[V], typename G::Raw (&g)[V],
+                        typename G::Raw (&d)[V], float& r) {
+    const bool in = row < P.rows;  // past the last row: nothing is read
+    const int len = in ? n : 0;
+    const int64_t at = in ? row : 0;
+    const __amdgpu_buffer_rsrc_t rh = row_range(P.h, at, len, HB ? 2 : 4);
+    const __amdgpu_buffer_rsrc_t rg = row_range(P.dy, at, len, GB ? 2 : 4);
 #pragma unroll
-    for (int v = 0; v < V; ++v) qh[v] = H::load(rh, t, v);
+    for (int v = 0; v < V; ++v) h[v] = H::load(rh, t, v);
 #pragma unroll
-    for (int v = 0; v < V; ++v) qg[v] = G::load(rg, t, v);
+    for (int v = 0; v < V; ++v) g[v] = G::load(rg, t, v);
     if (P.dh) {
+      const __amdgpu_buffer_rsrc_t rd = row_range(P.dh, at, len, GB ? 2 : 4);
 #pragma unroll
-      for (int v = 0; v < V; ++v) qd[v] = G::load(rd, t, v);
+      for (int v = 0; v < V; ++v) d[v] = G::load(rd, t, v);
     }
-    const float rstd = P.rstd[row];
+    r = P.rstd[at];
+  };
+  int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + sub;
+  load(row, qh, qg, qd, rstd);
+  for (; row < P.rows; row += step, turn ^= 1) {  // uniform over the rows' threads
+    typename H::Raw nh[V];
+    typename G::Raw ng[V], nd[V];
+    float next;
+    if constexpr (AHEAD) load(row + step, nh, ng, nd, next);  // in flight during this row's work
     float c = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -297,6 +326,17 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
         d[e] = fmaf(fmaf(-c, h[e] * rstd, g[e] * w[v][e]), rstd, d[e]);
       G::store(ro, t, v, G::pack(d));
     }
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        qh[v] = nh[v];
+        qg[v] = ng[v];
+        if (P.dh) qd[v] = nd[v];
+      }
+      rstd = next;
+    } else {
+      load(row + step, qh, qg, qd, rstd);
+    }
   }
 
   if (!P.dweight) return;
@@ -321,17 +361,19 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
     RowIo<T, VEC, false>::store(rp, t, v, RowIo<T, VEC, false>::pack(dw[v]));
 }
 
-// dweight[i] = sum over slots of partials[slot][i]: 16 columns to a workgroup
-// of 256 threads, each adding every 16th slot, then the 16 sums in order.
-constexpr int kDwCols = 16, kDwWays = 16;
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* partials, float* dweight,
-                                                      int slots, int n) {
-  __shared__ float part[kDwWays][kDwCols];
-  const int c = threadIdx.x % kDwCols, k = threadIdx.x / kDwCols;
-  const int i = blockIdx.x * kDwCols + c;
+// dweight[i] = sum over slots of partials[slot][i]: 64 columns to a workgroup,
+// wave k of 16 adding slots k, k + 16, ..., then the 16 sums in order.
+constexpr int kDwWays = 16;
+__global__ void __launch_bounds__(64 * kDwWays) norm_dw_kernel(const float* partials,
+                                                               float* dweight, int slots, int n) {
+  __shared__ float part[kDwWays][64];
+  const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
+  const int i = blockIdx.x * 64 + c;
   float s = 0.f;
-  if (i < n)
+  if (i < n) {
+#pragma unroll 8
     for (int j = k; j < slots; j += kDwWays) s += partials[(int64_t)j * n + i];
+  }
   part[k][c] = s;
   __syncthreads();
   if (k == 0 && i < n) {
@@ -341,20 +383,39 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* partials, flo
   }
 }
 
-// Threads and chunks to a row: the fewest threads that hold it.
+// Threads and chunks to a row: the fewest threads that hold it (777 x 5120
+// bf16 to e4m3: 17.6 us with 1024 threads and one chunk, of which 384 threads
+// had nothing, 9.9 with 256 and three).
+#define BFLY_WIDTH(T, V) \
+  if (n <= T * V * 8) return f(std::integral_constant<int, T>{}, std::integral_constant<int, V>{})
 template <typename F>
 hipError_t by_width(int n, F f) {
-  if (n <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  if (n <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  if (n <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  if (n <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (n <= 8192) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
-  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  BFLY_WIDTH(64, 1);
+  BFLY_WIDTH(64, 2);
+  BFLY_WIDTH(256, 1);
+  BFLY_WIDTH(256, 2);
+  BFLY_WIDTH(256, 3);
+  BFLY_WIDTH(256, 4);
+  BFLY_WIDTH(1024, 2);
+  return hipErrorInvalidValue;
 }
+template <typename F>
+hipError_t by_width_bwd(int n, F f) {  // dw and the next row's loads need registers too
+  BFLY_WIDTH(64, 1);
+  BFLY_WIDTH(64, 2);
+  BFLY_WIDTH(256, 1);
+  BFLY_WIDTH(256, 2);
+  BFLY_WIDTH(512, 2);
+  BFLY_WIDTH(1024, 2);
+  return hipErrorInvalidValue;
+}
+#undef BFLY_WIDTH
 int rows_per_block(int n) { return n <= 1024 ? 4 : 1; }
 
-constexpr int64_t kNormBlocks = 2048;  // workgroups of a forward launch at most
-constexpr int64_t kNormBwdSlots = 1024;
+// Workgroups of a forward launch at most: enough to give each of 8192 rows its
+// own (8192 x 4096: 44.0 us; 1024 workgroups that load their next row ahead
+// 45.2, 512 of them 50.4).
+constexpr int64_t kNormBlocks = 8192;
 
 template <bool VEC, bool XB, int Q>
 hipError_t norm_run(const NormParams& p, hipStream_t s) {
@@ -369,7 +430,7 @@ hipError_t norm_run(const NormParams& p, hipStream_t s) {
 
 template <bool VEC, bool HB, bool GB>
 hipError_t norm_bwd_run(const NormBwdParams& p, hipStream_t s) {
-  return by_width(p.n, [&](auto T, auto V) {
+  return by_width_bwd(p.n, [&](auto T, auto V) {
     hipLaunchKernelGGL((norm_bwd_kernel<T(), V(), VEC, HB, GB>),
                        dim3(rmsnorm_bwd_slots(p.rows, p.n)), dim3(T() < 256 ? 256 : T()), 0, s, p);
     return hipGetLastError();
@@ -378,9 +439,14 @@ hipError_t norm_bwd_run(const NormBwdParams& p, hipStream_t s) {
 
 }  // namespace
 
+// 256 to 1024 slots, 4 MiB of partial sums where that allows it: writing and
+// adding them costs 16384 x 5120 fp32 6 us at 256 slots and 18 at 1024
+// (182 and 194 us in all), while narrow rows need the workgroups to have
+// enough loads in flight.
 int rmsnorm_bwd_slots(int64_t rows, int n) {
   const int64_t need = (rows + rows_per_block(n) - 1) / rows_per_block(n);
-  return (int)(need < kNormBwdSlots ? need : kNormBwdSlots);
+  const int64_t most = n <= 1024 ? 1024 : n >= 4096 ? 256 : (1 << 20) / n;
+  return (int)(need < most ? need : most);
 }
 
 hipError_t launch_rmsnorm(const NormParams& p, hipStream_t s) {
@@ -404,7 +470,7 @@ hipError_t launch_rmsnorm_backward(const NormBwdParams& p, hipStream_t s) {
                  : (p.g_bf16 ? BFLY_NORM_BWD(false, true) : BFLY_NORM_BWD(false, false));
 #undef BFLY_NORM_BWD
   if (e != hipSuccess || !p.dweight) return e;
-  hipLaunchKernelGGL(norm_dw_kernel, dim3((p.n + kDwCols - 1) / kDwCols), dim3(256), 0, s,
+  hipLaunchKernelGGL(norm_dw_kernel, dim3((p.n + 63) / 64), dim3(64 * kDwWays), 0, s,
                      p.partials, p.dweight, rmsnorm_bwd_slots(p.rows, p.n), p.n);
   return hipGetLastError();
 }

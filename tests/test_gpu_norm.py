@@ -227,7 +227,7 @@ def check_backward(h, w, dy, dh, in_place=False):
     tol = 1.01 * tol + (U if dy.dtype == F32 else half(BF16)) * (np.abs(want) + tol) + U * np.abs(want)
     assert (np.abs(np64(dx[:rows]) - want) <= tol).all()
     slots = -(-rows // (4 if n <= 1024 else 1))
-    slots = min(slots, 1024)
+    slots = min(slots, 1024 if n <= 1024 else 256 if n >= 4096 else (1 << 20) // n)
     depth = -(-rows // slots) + 3 + -(-slots // 16) + 15 + 2
     term = dy64 * xhat
     tol = 1.01 * depth * U * np.abs(term).sum(0)
