@@ -417,6 +417,7 @@ def bfly_calib_step_weight(x, w, theta, adam_m, adam_v, step: int, cfg: bfly_cal
 # ---------------------------------------------------------------------------
 
 _types = None
+_describer = None
 
 
 def _dtypes():
@@ -502,6 +503,21 @@ def bfly_lora_matmul(x, ids, lora_a, lora_b, scaling, y, workspace, base=None,
           ws_bytes)
 
 
+def _describe(tensors, device):
+    """Addresses, element counts and bfly_dtype values of a list of contiguous
+    float32 or bfloat16 tensors on the GPU `device`, each as bytes."""
+    global _describer
+    if _describer is None:
+        import torch  # noqa: F401  (the extension needs its libraries loaded)
+        try:
+            from ._tensors import describe
+        except ImportError as e:
+            raise RuntimeError("the _tensors extension is not built: run "
+                               "`python -m learnable_butterfly_rotation_amd.build`") from e
+        _describer = describe
+    return _describer(tensors, device)
+
+
 def bfly_grad_clip_workspace_bytes(count: int) -> int:
     return lib().bfly_grad_clip_workspace_bytes(count)
 
@@ -511,29 +527,13 @@ def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> 
     float32 or bfloat16 of any shape), norm[1] = min(1, max_norm / norm[0]),
     and every gradient times norm[1], in place or into `outs`.  norm: [2]
     float32; workspace: a uint8 tensor of bfly_grad_clip_workspace_bytes."""
-    import torch
-    from array import array
-    row, _, f32, _, _, _ = _dtypes()
-    T = torch.Tensor
-    dtype = T.dtype.__get__
     dev = norm.get_device()
     ws, ws_bytes = _scratch(workspace, dev)
-    num = len(grads)
-    numels, types = array("q", map(T.numel, grads)), list(map(dtype, grads))
-    if not set(types) <= row.keys():
-        raise TypeError("libbfly takes float32 or bfloat16 gradients")
-    given = [grads]
+    at, numels, types = _describe(grads, dev)
+    to = None
     if outs is not None:
-        if array("q", map(T.numel, outs)) != numels or list(map(dtype, outs)) != types:
+        to, *like = _describe(outs, dev)
+        if like != [numels, types]:
             raise ValueError("the outputs have to be like their gradients")
-        given.append(outs)
-    for tensors in given:
-        if not all(map(T.is_contiguous, tensors)):
-            raise ValueError("the gradients and outputs have to be contiguous")
-        if not set(map(T.get_device, tensors)) <= {dev}:
-            raise ValueError("the gradients and outputs have to be on norm's device")
-    kinds = array("i", [row[t] for t in types])
-    ptrs = [array("Q", map(T.data_ptr, tensors)) for tensors in given]
-    at = [a.buffer_info()[0] if num else None for a in (*ptrs, numels, kinds)]
-    _call("bfly_grad_clip", dev, stream, num, at[0], at[1] if outs is not None else None, at[-2],
-          at[-1], max_norm, _at("norm", norm, (2,), f32, dev), ws, ws_bytes)
+    _call("bfly_grad_clip", dev, stream, len(types) // 4, at, to, numels, types, max_norm,
+          _at("norm", norm, (2,), _dtypes()[2], dev), ws, ws_bytes)

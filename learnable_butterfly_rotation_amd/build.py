@@ -2,7 +2,8 @@
 
 Usage: python -m learnable_butterfly_rotation_amd.build
 Each translation unit is compiled in parallel, then linked into a shared
-library next to this file.
+library next to this file; the Python extension _tensors.so (host code only,
+against torch's headers) is built beside it.
 """
 from __future__ import annotations
 
@@ -43,6 +44,23 @@ FLAGS = [
 ]
 
 
+EXT_SRC = os.path.join(CSRC, "tensors_py.cpp")
+EXT = os.path.join(HERE, "_tensors.so")
+
+
+def extension_command(out: str):
+    """The host compiler's call that builds the Python extension."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+            *["-isystem" + d for d in dirs], EXT_SRC, "-L" + libs, "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10", "-o", out]
+
+
 def build(verbose: bool = False, extra=None) -> str:
     os.makedirs(OBJ, exist_ok=True)
     t0 = time.time()
@@ -52,6 +70,9 @@ def build(verbose: bool = False, extra=None) -> str:
         cmd = [HIPCC, *FLAGS, *defs, *(extra or []), "-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT, text=True)))
+    ext_tmp = EXT + ".tmp%d" % os.getpid()
+    ext = subprocess.Popen(extension_command(ext_tmp), stdout=subprocess.PIPE,
+                           stderr=subprocess.STDOUT, text=True)
     objs, failed = [], []
     for src, obj, p in procs:
         out, _ = p.communicate()
@@ -60,14 +81,18 @@ def build(verbose: bool = False, extra=None) -> str:
         if p.returncode != 0:
             failed.append((src, out))
         objs.append(obj)
+    out, _ = ext.communicate()
+    if ext.returncode != 0:
+        failed.append(("tensors_py.cpp", out))
     if failed:
         for src, out in failed:
             print("---- %s ----\n%s" % (src, out), file=sys.stderr)
-        raise RuntimeError("hipcc failed for: " + ", ".join(s for s, _ in failed))
+        raise RuntimeError("the compiler failed for: " + ", ".join(s for s, _ in failed))
     tmp = LIB + ".tmp%d" % os.getpid()
     subprocess.run([HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *objs, "-o", tmp],
                    check=True)
     os.replace(tmp, LIB)
+    os.replace(ext_tmp, EXT)
     if verbose:
         print("built %s in %.1f s" % (LIB, time.time() - t0), file=sys.stderr)
     return LIB

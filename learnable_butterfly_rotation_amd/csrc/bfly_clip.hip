@@ -5,9 +5,9 @@
 //
 // Squares are summed in fp64 (an fp32 square overflows above 1.8e19 and loses
 // everything below 1e-23, and a sum over 10^9 elements loses half its digits).
-// Two passes over the data: the slots' sums, then the scaling, whose every
-// workgroup first adds the (at most 1024) slot sums in a fixed order.  Both
-// are bound by memory.
+// Two passes over the data, both bound by memory: the slots' sums, then the
+// scaling.  With few granules its every workgroup first adds the (at most
+// 2048) slot sums itself, in a fixed order; with many a launch between does.
 #include "bfly_clip.h"
 #include "bfly_rows.h"
 
@@ -38,13 +38,15 @@ __device__ __forceinline__ int find_tensor(const ClipTensor* tab, int count, int
 }
 
 // A 16-byte vector of a tensor's elements, as fp32.
-template <bool BF>
+// NT: loads and whole stores marked as used once.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool BF, bool NT>
 struct Vec {
   static constexpr int W = BF ? 8 : 4;
   float v[W];
   __device__ __forceinline__ void load(const char* p) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const u32x4* const from = reinterpret_cast<const u32x4*>(p);
+    const u32x4 w = NT ? __builtin_nontemporal_load(from) : *from;
 #pragma unroll
     for (int e = 0; e < W; ++e)
       v[e] = !BF ? __uint_as_float(w[e]) : (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
@@ -67,7 +69,9 @@ struct Vec {
   __device__ __forceinline__ void store(char* p) const {
     uint32_t w[4];
     words(w);
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    const u32x4 q = {w[0], w[1], w[2], w[3]};
+    if (NT) __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(p));
+    else *reinterpret_cast<u32x4*>(p) = q;
   }
   __device__ __forceinline__ void store_some(char* p, int lo, int hi) const {
     uint32_t w[4];
@@ -83,11 +87,11 @@ struct Vec {
 
 // The elements [from, to) of a tensor, counted from its boundary, vector by
 // vector over the workgroup: f(vector, offset of it, first and last + 1 of
-// its elements that are the tensor's).  Vectors in pairs of four whole ones
-// where there are, whose loads are in flight together.
-template <bool BF, typename F>
+// its elements that are the tensor's).  Where there are kAhead whole vectors,
+// their loads are in flight together.
+template <bool BF, bool NT, typename F>
 __device__ __forceinline__ void each_vector(const char* in, int64_t from, int64_t to, F f) {
-  using V = Vec<BF>;
+  using V = Vec<BF, NT>;
   constexpr int es = BF ? 2 : 4, W = V::W, step = kThreads * W;
   const int64_t first = from / W * W;  // of a vector; from is inside it
   int64_t at = first + threadIdx.x * W;
@@ -142,10 +146,9 @@ __device__ __forceinline__ double block_total(double v, double* buf) {
   return (buf[0] + buf[1]) + (buf[2] + buf[3]);
 }
 
-// How the granules are dealt out, and the table: `in_args` of it in the
-// launch's arguments, or all of it in memory.
+// How the granules are dealt out, and the table in memory.
 struct Slots {
-  const ClipTensor* table;  // nullptr: the batch
+  const ClipTensor* table;
   int count, granules, per_slot, slots;
 };
 
@@ -160,11 +163,40 @@ __device__ __forceinline__ void square_slot(const ClipTensor* tab, const Slots& 
 #pragma unroll
       for (float e : v.v) s = fma((double)e, (double)e, s);
     };
-    if (c.kind & 1) each_vector<true>(c.in, from, to, add);
-    else each_vector<false>(c.in, from, to, add);
+    if (c.kind & 1) each_vector<true, false>(c.in, from, to, add);
+    else each_vector<false, false>(c.in, from, to, add);
   });
   s = block_total(s, buf);
   if (threadIdx.x == 0) sums[blockIdx.x] = s;
+}
+
+// The norm and the factor from the sum of squares.  A norm that is not finite
+// scales nothing: it is reported, and the caller drops the step.
+__device__ __forceinline__ float factor_of(double squares, float max_norm, float* norm) {
+  const double all = sqrt(squares);
+  const float c = all > (double)max_norm && all < __builtin_inf() ? (float)(max_norm / all) : 1.f;
+  if (norm) {
+    norm[0] = (float)all;
+    norm[1] = c;
+  }
+  return c;
+}
+
+template <bool NT>
+__device__ __forceinline__ void scale_range(const ClipTensor& t, int64_t from, int64_t to,
+                                            float c) {
+  if (c == 1.f && t.in == t.out) return;  // in place and not scaled: nothing to write
+  const bool wide = ((uintptr_t)t.out & 15) == 0;  // the output is aligned as the input is
+  const auto put = [&](auto v, int64_t at, int lo, int hi) {
+    constexpr int W = decltype(v)::W;
+#pragma unroll
+    for (float& e : v.v) e *= c;
+    char* const o = t.out + at * (16 / W);
+    if (wide && hi - lo == W) v.store(o);
+    else v.store_some(o, lo, hi);
+  };
+  if (t.kind & 1) each_vector<true, NT>(t.in, from, to, put);
+  else each_vector<false, NT>(t.in, from, to, put);
 }
 
 __device__ __forceinline__ void scale_slot(const ClipTensor* tab, const Slots& S,
@@ -177,29 +209,37 @@ __device__ __forceinline__ void scale_slot(const ClipTensor* tab, const Slots& S
     const int i = k * kThreads + threadIdx.x;
     s += i < S.slots ? sums[i] : 0.0;
   }
-  const double all = sqrt(block_total(s, buf));
-  // a norm that is not finite scales nothing: it is reported, and the caller drops the step
-  const float c = all > (double)max_norm && all < __builtin_inf() ? (float)(max_norm / all) : 1.f;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    norm[0] = (float)all;
-    norm[1] = c;
-  }
+  const float c = factor_of(block_total(s, buf), max_norm,
+                            blockIdx.x == 0 && threadIdx.x == 0 ? norm : nullptr);
   const int g0 = blockIdx.x * S.per_slot;
   const int g1 = g0 + S.per_slot < S.granules ? g0 + S.per_slot : S.granules;
   each_range(tab, S.count, g0, g1, &found, [&](const ClipTensor& t, int64_t from, int64_t to) {
-    if (c == 1.f && t.in == t.out) return;  // in place and not scaled: nothing to write
-    const bool wide = ((uintptr_t)t.out & 15) == 0;  // the output is aligned as the input is
-    const auto put = [&](auto v, int64_t at, int lo, int hi) {
-      constexpr int W = decltype(v)::W;
-#pragma unroll
-      for (float& e : v.v) e *= c;
-      char* const o = t.out + at * (16 / W);
-      if (wide && hi - lo == W) v.store(o);
-      else v.store_some(o, lo, hi);
-    };
-    if (t.kind & 1) each_vector<true>(t.in, from, to, put);
-    else each_vector<false>(t.in, from, to, put);
+    scale_range<false>(t, from, to, c);
   });
+}
+
+// Many granules: the norm by one workgroup, then a granule to a workgroup at
+// a time, neighbours together, past the caches (721M fp32 elements: 1429 us
+// as 1024 ranges through the caches).
+__global__ void __launch_bounds__(kThreads) factor_kernel(Slots S, const double* sums,
+                                                          float max_norm, float* norm) {
+  __shared__ double buf[kThreads / 64];
+  double s = 0.0;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < S.slots; i += kThreads) s += sums[i];
+  s = block_total(s, buf);
+  if (threadIdx.x == 0) factor_of(s, max_norm, norm);
+}
+__device__ __forceinline__ void scale_granules(const ClipTensor* tab, const Slots& S,
+                                               const float* norm) {
+  __shared__ int found[2];
+  const float c = norm[1];
+  int turn = 0;
+  for (int g = blockIdx.x; g < S.granules; g += gridDim.x, turn ^= 1)
+    each_range(tab, S.count, g, g + 1, &found[turn],
+               [&](const ClipTensor& t, int64_t from, int64_t to) {
+                 scale_range<true>(t, from, to, c);
+               });
 }
 
 __global__ void __launch_bounds__(kThreads) square_kernel(Slots S, double* sums) {
@@ -215,6 +255,14 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(Slots S, const double* 
 __global__ void __launch_bounds__(kThreads) scale_few_kernel(Batch b, Slots S, const double* sums,
                                                              float max_norm, float* norm) {
   scale_slot(b.t, S, sums, max_norm, norm);
+}
+
+__global__ void __launch_bounds__(kThreads) scale_many_kernel(Slots S, const float* norm) {
+  scale_granules(S.table, S, norm);
+}
+__global__ void __launch_bounds__(kThreads) scale_many_few_kernel(Batch b, Slots S,
+                                                                  const float* norm) {
+  scale_granules(b.t, S, norm);
 }
 
 }  // namespace
@@ -251,13 +299,23 @@ hipError_t launch_grad_clip(const ClipParams& p, hipStream_t s) {
   S.table = tab;
   S.count = count;
   S.granules = (int)granules;
-  S.per_slot = (int)(granules > kClipSlots ? (granules + kClipSlots - 1) / kClipSlots : 1);
+  const bool many = granules > kClipFew;
+  const int most = many ? kClipManySlots : kClipSlots;
+  S.per_slot = (int)(granules > most ? (granules + most - 1) / most : 1);
   S.slots = (int)((granules + S.per_slot - 1) / S.per_slot);
+  hipError_t e = hipSuccess;
   if (S.slots > 0) {
     if (few) hipLaunchKernelGGL(square_few_kernel, dim3(S.slots), dim3(kThreads), 0, s, b, S, sums);
     else hipLaunchKernelGGL(square_kernel, dim3(S.slots), dim3(kThreads), 0, s, S, sums);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (many) {
+    hipLaunchKernelGGL(factor_kernel, dim3(1), dim3(kThreads), 0, s, S, sums, p.max_norm, p.norm);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const dim3 grid(S.granules < 65536 ? S.granules : 65536);
+    if (few) hipLaunchKernelGGL(scale_many_few_kernel, grid, dim3(kThreads), 0, s, b, S, p.norm);
+    else hipLaunchKernelGGL(scale_many_kernel, grid, dim3(kThreads), 0, s, S, p.norm);
+    return hipGetLastError();
   }
   const dim3 grid(S.slots > 0 ? S.slots : 1);
   if (few)

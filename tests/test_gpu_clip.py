@@ -70,6 +70,20 @@ def test_clip_sizes(sizes, dtypes, in_place):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("count", [3, 300])
+def test_clip_many_elements(count, in_place):
+    # beyond 2^26 elements the norm has a launch of its own; the sizes are odd
+    # and the tensors views that start anywhere
+    g = torch.Generator().manual_seed(count)
+    each = (70 << 20) // count
+    sizes = [each - 7 * i for i in range(count)]
+    flat = torch.randn(sum(sizes), generator=g).cuda()
+    for dtype, grads in ((F32, flat), (BF16, flat.to(BF16))):
+        check(None, 0.5, in_place, on_gpu=list(grads.split(sizes)))
+        check(None, 1e9, in_place, on_gpu=list(grads.split(sizes)))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_clip_below_the_limit(in_place):
     check(tensors(1, [4096, 100, 9999], (F32, BF16)), 1e4, in_place)
 

@@ -151,3 +151,16 @@ def test_the_binding_refuses_tensors_of_the_host():
                            torch.zeros((2, 8)), ws)
     with pytest.raises(ValueError):
         B.bfly_grad_clip([w], 1.0, v, ws)
+
+
+def test_the_list_of_gradients_is_checked():
+    if not os.path.exists(os.path.join(os.path.dirname(B.library_path), "_tensors.so")):
+        pytest.skip("the extension is not built")
+    ok = torch.zeros(3)
+    assert B._describe([], 0) == (b"", b"", b"")
+    for bad, error in ((3, TypeError), ([3], TypeError), ([ok.double()], TypeError),
+                       ([torch.zeros(2, dtype=torch.int8), ok], TypeError), ([ok], ValueError),
+                       ([None], TypeError)):
+        for _ in range(3):
+            with pytest.raises(error):
+                B._describe(bad, 0)
