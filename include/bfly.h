@@ -554,7 +554,8 @@ size_t bfly_lora_matmul_workspace_bytes(int64_t rows, int32_t n_out, int32_t k, 
  *   outs[i] = grads[i] * factor
  *   grads  : host array of device pointers, read before the call returns
  *   outs   : host array of device pointers, or NULL (in place); outs[i] may
- *            be grads[i], no other aliasing
+ *            be grads[i], no other aliasing: no two tensors that are written
+ *            may overlap (a tensor listed twice in place would be scaled twice)
  *   numels : host array of element counts (0: a tensor without elements,
  *            whose pointers are not looked at)
  *   dtypes : host array of bfly_dtype values

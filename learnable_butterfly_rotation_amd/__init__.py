@@ -181,19 +181,28 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _at(name, t, shape, dtypes, device):
-    """The address of a tensor (None: NULL) that has to be contiguous, of this
-    shape, of one of these types and on the GPU `device`."""
-    if t is None:
-        return None
-    if t.dtype not in dtypes:
-        raise TypeError("%s is %s" % (name, t.dtype))
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s has to be contiguous of shape %s, got %s with strides %s"
-                         % (name, tuple(shape), tuple(t.shape), t.stride()))
-    if t.get_device() != device:
-        raise ValueError("%s is on another device than the first argument" % name)
-    return t.data_ptr()
+_extension = None
+
+
+def _ext():
+    """The extension that checks tensors: at(name, tensor, shape, kinds,
+    device) gives the address of a contiguous tensor of that shape, of one of
+    these types and on that GPU (None for None), or raises."""
+    global _extension
+    if _extension is None:
+        import importlib
+        import torch  # noqa: F401  (the extension needs its libraries loaded)
+        try:
+            _extension = importlib.import_module("._tensors", __name__)
+        except ImportError as e:
+            raise RuntimeError("the _tensors extension is not built: run "
+                               "`python -m learnable_butterfly_rotation_amd.build`") from e
+    return _extension
+
+
+# the types of at(), as bits
+_F32, _BF16, _F16, _BYTES, _I32 = 1, 2, 4, 8 | 16 | 32, 64
+_ROWS = _F32 | _BF16
 
 
 def _scratch(workspace, device):
@@ -416,22 +425,6 @@ def bfly_calib_step_weight(x, w, theta, adam_m, adam_v, step: int, cfg: bfly_cal
 # the norm in front of a layer, adapters beside its product, clipping
 # ---------------------------------------------------------------------------
 
-_types = None
-_describer = None
-
-
-def _dtypes():
-    """(rows, bfloat16, float32, float16, one byte, int32): the torch types
-    that the calls below take, and the bfly_dtype of the rows'."""
-    global _types
-    if _types is None:
-        import torch
-        _types = ({torch.float32: BFLY_F32, torch.bfloat16: BFLY_BF16}, (torch.bfloat16,),
-                  (torch.float32,), (torch.float16,),
-                  (torch.int8, torch.uint8, torch.float8_e4m3fn), (torch.int32,))
-    return _types
-
-
 def bfly_rmsnorm(x, weight, eps, y=None, codes=None, scales=None, residual=None, h=None, rstd=None,
                  format=BFLY_Q8_INT8, group=None, stream=None) -> None:
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight per row, and y
@@ -439,19 +432,20 @@ def bfly_rmsnorm(x, weight, eps, y=None, codes=None, scales=None, residual=None,
     bfloat16; codes: [rows, n] of one byte an element with scales [rows,
     n/group] float16 (group None: one scale per row); rstd: [rows] float32;
     weight: [n] or None (ones).  Outputs that are None are not computed."""
-    row, _, f32, f16, byte, _ = _dtypes()
+    at = _ext().at
     shape = rows, n = x.shape
     if group is None or codes is None:
         group = n
     dev = x.get_device()
-    same = (x.dtype,)
-    _call("bfly_rmsnorm", dev, stream, _at("x", x, shape, row, dev), row[x.dtype],
-          _at("residual", residual, shape, same, dev), _at("h", h, shape, same, dev),
-          _at("weight", weight, (n,), row, dev), 0 if weight is None else row[weight.dtype],
-          _at("y", y, shape, row, dev), 0 if y is None else row[y.dtype],
-          _at("codes", codes, shape, byte, dev),
-          _at("scales", scales, (rows, n // group if group > 0 else 0), f16, dev),
-          _at("rstd", rstd, (rows,), f32, dev), rows, n, eps, format, group)
+    px = at("x", x, shape, _ROWS, dev)
+    x_dt = _dt(x)
+    same = _BF16 if x_dt else _F32
+    _call("bfly_rmsnorm", dev, stream, px, x_dt, at("residual", residual, shape, same, dev),
+          at("h", h, shape, same, dev), at("weight", weight, (n,), _ROWS, dev),
+          0 if weight is None else _dt(weight), at("y", y, shape, _ROWS, dev),
+          0 if y is None else _dt(y), at("codes", codes, shape, _BYTES, dev),
+          at("scales", scales, (rows, n // group if group > 0 else 0), _F16, dev),
+          at("rstd", rstd, (rows,), _F32, dev), rows, n, eps, format, group)
 
 
 def bfly_rmsnorm_backward_workspace_bytes(rows: int, n: int) -> int:
@@ -464,16 +458,18 @@ def bfly_rmsnorm_backward(h, weight, rstd, dy, dx, dweight=None, dh=None, worksp
     gradient.  h: [rows, n]; dy, dh, dx: [rows, n] of one type; rstd: [rows]
     and dweight: [n] float32; workspace: a uint8 tensor of
     bfly_rmsnorm_backward_workspace_bytes (needed with dweight)."""
-    row, _, f32, _, _, _ = _dtypes()
+    at = _ext().at
     shape = rows, n = h.shape
     dev = h.get_device()
-    same = (dy.dtype,)
+    pdy = at("dy", dy, shape, _ROWS, dev)
+    g_dt = _dt(dy)
+    same = _BF16 if g_dt else _F32
     ws, ws_bytes = _scratch(workspace, dev)
-    _call("bfly_rmsnorm_backward", dev, stream, _at("h", h, shape, row, dev), row[h.dtype],
-          _at("weight", weight, (n,), row, dev), 0 if weight is None else row[weight.dtype],
-          _at("rstd", rstd, (rows,), f32, dev), _at("dy", dy, shape, row, dev),
-          _at("dh", dh, shape, same, dev), _at("dx", dx, shape, same, dev), row[dy.dtype],
-          _at("dweight", dweight, (n,), f32, dev), rows, n, ws, ws_bytes)
+    _call("bfly_rmsnorm_backward", dev, stream, at("h", h, shape, _ROWS, dev), _dt(h),
+          at("weight", weight, (n,), _ROWS, dev), 0 if weight is None else _dt(weight),
+          at("rstd", rstd, (rows,), _F32, dev), pdy, at("dh", dh, shape, same, dev),
+          at("dx", dx, shape, same, dev), g_dt, at("dweight", dweight, (n,), _F32, dev), rows, n,
+          ws, ws_bytes)
 
 
 def bfly_lora_matmul_workspace_bytes(rows: int, n_out: int, k: int, rank: int) -> int:
@@ -488,34 +484,18 @@ def bfly_lora_matmul(x, ids, lora_a, lora_b, scaling, y, workspace, base=None,
     bfloat16; scaling: [adapters] float32; base, y: [rows, n_out] float32 or
     bfloat16 (base None: zeros; y may be base); workspace: a uint8 tensor of
     bfly_lora_matmul_workspace_bytes."""
-    row, bf, f32, _, _, i32 = _dtypes()
+    at = _ext().at
     rows, k = x.shape
     num, rank, _ = lora_a.shape
-    shape = _, n_out = y.shape
+    _, n_out = y.shape
     dev = x.get_device()
     ws, ws_bytes = _scratch(workspace, dev)
-    _call("bfly_lora_matmul", dev, stream, _at("x", x, (rows, k), bf, dev), BFLY_BF16,
-          _at("ids", ids, (rows,), i32, dev), _at("lora_a", lora_a, (num, rank, k), bf, dev),
-          _at("lora_b", lora_b, (num, n_out, rank), bf, dev),
-          _at("scaling", scaling, (num,), f32, dev),
-          _at("base", base, shape, row, dev), 0 if base is None else row[base.dtype],
-          _at("y", y, (rows, n_out), row, dev), row[y.dtype], rows, n_out, k, num, rank, ws,
-          ws_bytes)
-
-
-def _describe(tensors, device):
-    """Addresses, element counts and bfly_dtype values of a list of contiguous
-    float32 or bfloat16 tensors on the GPU `device`, each as bytes."""
-    global _describer
-    if _describer is None:
-        import torch  # noqa: F401  (the extension needs its libraries loaded)
-        try:
-            from ._tensors import describe
-        except ImportError as e:
-            raise RuntimeError("the _tensors extension is not built: run "
-                               "`python -m learnable_butterfly_rotation_amd.build`") from e
-        _describer = describe
-    return _describer(tensors, device)
+    _call("bfly_lora_matmul", dev, stream, at("x", x, (rows, k), _BF16, dev), BFLY_BF16,
+          at("ids", ids, (rows,), _I32, dev), at("lora_a", lora_a, (num, rank, k), _BF16, dev),
+          at("lora_b", lora_b, (num, n_out, rank), _BF16, dev),
+          at("scaling", scaling, (num,), _F32, dev),
+          at("base", base, (rows, n_out), _ROWS, dev), 0 if base is None else _dt(base),
+          at("y", y, (rows, n_out), _ROWS, dev), _dt(y), rows, n_out, k, num, rank, ws, ws_bytes)
 
 
 def bfly_grad_clip_workspace_bytes(count: int) -> int:
@@ -526,14 +506,16 @@ def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> 
     """norm[0] = the 2-norm over all tensors of `grads` (a list; contiguous
     float32 or bfloat16 of any shape), norm[1] = min(1, max_norm / norm[0]),
     and every gradient times norm[1], in place or into `outs`.  norm: [2]
-    float32; workspace: a uint8 tensor of bfly_grad_clip_workspace_bytes."""
+    float32; workspace: a uint8 tensor of bfly_grad_clip_workspace_bytes.  No
+    two of the tensors that are written may overlap."""
+    ext = _ext()
     dev = norm.get_device()
     ws, ws_bytes = _scratch(workspace, dev)
-    at, numels, types = _describe(grads, dev)
+    at, numels, types = ext.describe(grads, dev, outs is None)
     to = None
     if outs is not None:
-        to, *like = _describe(outs, dev)
+        to, *like = ext.describe(outs, dev, True)
         if like != [numels, types]:
             raise ValueError("the outputs have to be like their gradients")
     _call("bfly_grad_clip", dev, stream, len(types) // 4, at, to, numels, types, max_norm,
-          _at("norm", norm, (2,), _dtypes()[2], dev), ws, ws_bytes)
+          ext.at("norm", norm, (2,), _F32, dev), ws, ws_bytes)

@@ -149,7 +149,7 @@ constexpr int kRunPitch = 2 * kRun + 16;
 // A matrix-core operand wants row l % 16 in lane l, so loading it straight
 // from memory makes four neighbouring lanes touch four lines and a load of
 // the wave take 64 cycles of the address unit instead of 16: for few rows
-// that, not the memory, was the bound (2.2 us for 512 k of 64 ranks, 0.6 now).
+// that, not the memory, was the bound (2.2 us for 512 k of 64 ranks, 1.2 so).
 // So eight neighbouring lanes load a row's 128 bytes and the operands are
 // read back from LDS.
 template <int RT>
@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int spli
   __shared__ __align__(16) uint8_t lds[4 * S::kWaveBytes];
   const int64_t row0 = (int64_t)blockIdx.x * kBlockRows;
   const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
+  if ((int)blockIdx.y >= nr) return;  // no more tiles than rows: a last block's may be few
   const int split = blockIdx.z % splits, rank0 = blockIdx.z / splits * (RT * 16);
   make_tiles(tiles, P.ids + row0, nr, P.n_adapters);
   if (blockIdx.y == 0 && blockIdx.z == 0) put_order(order_at(P) + blockIdx.x, tiles);
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int spli
   const int n = lane & 15, g = lane >> 4;
   const int64_t row0 = (int64_t)blockIdx.y * kBlockRows;
   const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
+  if ((int)blockIdx.z >= nr) return;
   const int col = blockIdx.x * E::kCols + wave * 16 * JT + JT * n;  // the lane's first column
   get_order(tiles, order_at(P) + blockIdx.y);
   constexpr int bs = BB ? 2 : 4, ys = YB ? 2 : 4;
@@ -498,30 +500,33 @@ struct Cut {
 // Workgroups that share a block's tiles: as many as it can have tiles, and
 // where there are many blocks as many as packed prompts have (four, and one
 // more for every change of adapter within 256 rows): the others would start
-// only to find nothing, 257 rows of 32 adapters 36.3 us with 16 lanes and 31.0
-// with 33, 8192 rows of 6 adapters 137 us with 8 and no less with more.
+// only to find nothing (257 rows of 32 adapters: 36.3 us with 16, 31.0 with 33;
+// 8192 rows of 6 adapters: 137 us with 8 and no less with more).
 int tile_lanes(int64_t rows, int64_t blocks, int n_adapters) {
   const int64_t r = rows < kBlockRows ? rows : kBlockRows;
   const int64_t most = (r < n_adapters ? r : n_adapters) + r / kTileRows + 1;
   const int64_t cap = blocks <= 2 ? 64 : blocks <= 8 ? 16 : 8;
   return (int)(most < cap ? most : cap);
 }
-Cut cut(int64_t rows, int k, int rank) {
+Cut cut(int64_t rows, int k, int n_adapters, int rank) {
   Cut c;
   c.rt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
   c.ranks = (rank + 16 * c.rt - 1) / (16 * c.rt);
   c.stride = c.ranks * c.rt * 16;
   c.blocks = (rows + kBlockRows - 1) / kBlockRows;
-  // The k axis is split until there is a workgroup for every CU, counting one
-  // tile to 64 rows.  A workgroup takes 2048 k at least (257 rows, 32
-  // adapters, k = 11008, rank 64: 42 us with 512, 33 with 1024, 31 with 2048
-  // and 4096, 34 with 8192) and with a tile of rows 512, which the smallest
-  // calls wait for one after the other.
-  const int64_t groups = (rows + kTileRows - 1) / kTileRows * c.ranks;
-  const int run = rows <= kTileRows ? 512 : 2048;
-  const int most = (k + run - 1) / run;
-  const int64_t want = groups < 256 ? 256 / groups : 1;
-  c.splits = (int)(want < most ? want : most);
+  // The k axis is split until there is a workgroup for every CU, counting the
+  // tiles there can be: one to 64 rows, and one more for every adapter of a
+  // block.  More of them cost more to start than they save (257 rows of 32
+  // adapters, k = 11008, rank 64: 31 us with 256 workgroups wanted, 38 with
+  // 384; 2048 rows of 4, k = 4096: 30 us with 192, 27 with 256, 29 with 384).
+  // A workgroup takes 512 k at least, which its waves wait for twice.
+  const int64_t tail = rows - (c.blocks - 1) * kBlockRows;
+  const int64_t tiles = (rows + kTileRows - 1) / kTileRows +
+                        (c.blocks - 1) * (n_adapters < kBlockRows ? n_adapters : kBlockRows) +
+                        (n_adapters < tail ? n_adapters : tail);
+  const int most = (k + 511) / 512;
+  const int64_t want = 256 / (tiles * c.ranks);
+  c.splits = (int)(want < 1 ? 1 : want < most ? want : most);
   c.slice = ((k + c.splits - 1) / c.splits + 127) / 128 * 128;
   c.splits = (k + c.slice - 1) / c.slice;
   return c;
@@ -554,13 +559,13 @@ void expand_by_rank(const LoraParams& p, const Cut& c, hipStream_t s) {
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t rows, int k, int rank) {
-  const Cut c = cut(rows, k, rank);
+  const Cut c = cut(rows, k, 1, rank);  // most splits
   return (size_t)c.blocks * sizeof(Order) +
          (size_t)c.splits * (size_t)rows * (size_t)c.stride * sizeof(float);
 }
 
 hipError_t launch_lora(const LoraParams& p, hipStream_t s) {
-  const Cut c = cut(p.rows, p.k, p.rank);
+  const Cut c = cut(p.rows, p.k, p.n_adapters, p.rank);
   switch (c.rt) {
     case 1: shrink<1>(p, c, s); break;
     case 2: shrink<2>(p, c, s); break;

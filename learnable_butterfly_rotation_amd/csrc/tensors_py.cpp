@@ -1,21 +1,46 @@
-// Python extension `_tensors`: what a list of torch tensors is made of, for the
-// calls of libbfly that take many of them.  Reading address, size, type,
-// device and contiguity of 96 gradients and their outputs through Python
-// costs 50 us, four times what the GPU needs to clip them.
+// Python extension `_tensors`: the checks of torch tensors before their
+// addresses go into a call of libbfly.  Reading type, shape, device and
+// contiguity of 96 gradients and their outputs through Python costs 50 us, four
+// times what the GPU needs to clip them, and of the eight tensors of a norm 4 us,
+// as long as its kernel takes for a token.
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <exception>
+#include <utility>
+#include <vector>
 
 namespace {
 
-// describe(tensors, device) -> (addresses, element counts, bfly_dtype values)
-// as bytes of uint64, int64 and int32.  Every item has to be a contiguous
-// float32 or bfloat16 tensor on GPU `device`.
+// Whether two of n ranges of bytes share any (empty ranges share none).
+bool overlap(const uint64_t* at, const int64_t* numel, const int32_t* type, Py_ssize_t n) {
+  const auto bytes = [&](Py_ssize_t i) { return (uint64_t)numel[i] * (type[i] ? 2 : 4); };
+  bool ordered = true;  // as views of one buffer mostly are
+  uint64_t end = 0;
+  for (Py_ssize_t i = 0; i < n && ordered; ++i) {
+    if (!numel[i]) continue;
+    ordered = at[i] >= end;
+    end = at[i] + bytes(i);
+  }
+  if (ordered) return false;
+  std::vector<std::pair<uint64_t, uint64_t>> r;
+  for (Py_ssize_t i = 0; i < n; ++i)
+    if (numel[i]) r.emplace_back(at[i], at[i] + bytes(i));
+  std::sort(r.begin(), r.end());
+  for (size_t i = 1; i < r.size(); ++i)
+    if (r[i].first < r[i - 1].second) return true;
+  return false;
+}
+
+// describe(tensors, device, distinct) -> (addresses, element counts, bfly_dtype
+// values) as bytes of uint64, int64 and int32.  Every item has to be a
+// contiguous float32 or bfloat16 tensor on GPU `device`; with `distinct`, no
+// two of them may overlap.
 PyObject* describe(PyObject*, PyObject* args) {
   PyObject* given = nullptr;
-  int device = -1;
-  if (!PyArg_ParseTuple(args, "Oi", &given, &device)) return nullptr;
+  int device = -1, distinct = 0;
+  if (!PyArg_ParseTuple(args, "Oip", &given, &device, &distinct)) return nullptr;
   PyObject* items = PySequence_Fast(given, "a list or tuple of tensors is needed");
   if (!items) return nullptr;
   const Py_ssize_t n = PySequence_Fast_GET_SIZE(items);
@@ -53,6 +78,8 @@ PyObject* describe(PyObject*, PyObject* args) {
         c[i] = x.numel();
         t[i] = s == at::kBFloat16 ? 1 : 0;
       }
+      if (i == n && distinct && overlap(a, c, t, n))
+        PyErr_SetString(PyExc_ValueError, "two of the tensors to write overlap");
     } catch (const std::exception& e) {
       PyErr_Format(PyExc_RuntimeError, "tensor %zd: %s", i, e.what());
     }
@@ -65,7 +92,55 @@ PyObject* describe(PyObject*, PyObject* args) {
   return result;
 }
 
+// The types that `at` is told to take, as bits.
+int kind_of(at::ScalarType s) {
+  switch (s) {
+    case at::kFloat: return 1;
+    case at::kBFloat16: return 2;
+    case at::kHalf: return 4;
+    case at::kChar: return 8;
+    case at::kByte: return 16;
+    case at::kFloat8_e4m3fn: return 32;
+    case at::kInt: return 64;
+    default: return 0;
+  }
+}
+
+// at(name, tensor, shape, kinds, device) -> the address of a tensor that is
+// contiguous, of this shape, of one of these types and on GPU `device`; None
+// for None.
+PyObject* address(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 5) return PyErr_Format(PyExc_TypeError, "at() takes five arguments");
+  PyObject *const name = args[0], *const item = args[1], *const shape = args[2];
+  if (item == Py_None) Py_RETURN_NONE;
+  if (!THPVariable_Check(item)) return PyErr_Format(PyExc_TypeError, "%S is not a tensor", name);
+  if (!PyTuple_Check(shape))
+    return PyErr_Format(PyExc_TypeError, "the shape of %S has to be a tuple", name);
+  const long kinds = PyLong_AsLong(args[3]), device = PyLong_AsLong(args[4]);
+  if (PyErr_Occurred()) return nullptr;
+  try {
+    const at::Tensor& x = THPVariable_Unpack(item);
+    if (!(kind_of(x.scalar_type()) & kinds))
+      return PyErr_Format(PyExc_TypeError, "%S has the wrong type", name);
+    bool same = x.layout() == at::kStrided && x.dim() == PyTuple_GET_SIZE(shape);
+    for (int64_t i = 0; same && i < x.dim(); ++i) {
+      const long long v = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
+      if (v == -1 && PyErr_Occurred()) return nullptr;
+      same = x.size(i) == v;
+    }
+    if (!same || !x.is_contiguous())
+      return PyErr_Format(PyExc_ValueError, "%S has to be contiguous of shape %R", name, shape);
+    if (!x.is_cuda() || x.get_device() != device)
+      return PyErr_Format(PyExc_ValueError, "%S has to be on GPU %ld", name, device);
+    return PyLong_FromVoidPtr(x.data_ptr());
+  } catch (const std::exception& e) {
+    return PyErr_Format(PyExc_RuntimeError, "%S: %s", name, e.what());
+  }
+}
+
 PyMethodDef methods[] = {
+    {"at", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(address)), METH_FASTCALL,
+     "the address of a tensor that is as it has to be"},
     {"describe", describe, METH_VARARGS, "addresses, element counts and types of tensors"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,

@@ -142,3 +142,21 @@ def test_clip_same_bits_every_time():
         v = norm.tolist()
         first = first or v
         assert v == first
+
+
+def test_clip_tensors_that_overlap():
+    flat, norm = torch.ones(1000, device="cuda"), torch.empty(2, device="cuda")
+    for views in ([flat, flat], [flat[:10], flat[5:20]], [flat[500:], flat[:501]],
+                  [flat[:1], flat[3:9], flat[0:0], flat[8:9]]):
+        with pytest.raises(ValueError):
+            B.bfly_grad_clip(views, 1.0, norm, workspace(len(views)))
+        with pytest.raises(ValueError):
+            B.bfly_grad_clip([torch.ones_like(v) for v in views], 1.0, norm,
+                             workspace(len(views)), outs=views)
+    assert (flat == 1).all()
+    # read twice, written to different places; and neighbours in any order
+    B.bfly_grad_clip([flat, flat], 1.0, norm, workspace(2),
+                     outs=[torch.empty_like(flat) for _ in range(2)])
+    assert abs(float(norm[0]) - 2000 ** 0.5) <= TOL * 2000 ** 0.5
+    B.bfly_grad_clip([flat[500:], flat[:0], flat[:500]], 1.0, norm, workspace(3))
+    assert abs(float(norm[0]) - 1000 ** 0.5) <= TOL * 1000 ** 0.5

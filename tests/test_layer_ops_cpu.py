@@ -153,14 +153,37 @@ def test_the_binding_refuses_tensors_of_the_host():
         B.bfly_grad_clip([w], 1.0, v, ws)
 
 
-def test_the_list_of_gradients_is_checked():
+def extension():
     if not os.path.exists(os.path.join(os.path.dirname(B.library_path), "_tensors.so")):
         pytest.skip("the extension is not built")
-    ok = torch.zeros(3)
-    assert B._describe([], 0) == (b"", b"", b"")
+    return B._ext()
+
+
+def test_the_list_of_gradients_is_checked():
+    ext, ok = extension(), torch.zeros(3)
+    assert ext.describe([], 0, True) == (b"", b"", b"")
     for bad, error in ((3, TypeError), ([3], TypeError), ([ok.double()], TypeError),
                        ([torch.zeros(2, dtype=torch.int8), ok], TypeError), ([ok], ValueError),
                        ([None], TypeError)):
         for _ in range(3):
             with pytest.raises(error):
-                B._describe(bad, 0)
+                ext.describe(bad, 0, False)
+    with pytest.raises(TypeError):
+        ext.describe([])
+
+
+def test_a_tensor_is_checked():
+    ext, x = extension(), torch.zeros((3, 4))
+    assert ext.at("x", None, (3, 4), 1, 0) is None
+    for args, error in ((("x", 5, (3, 4), 1, 0), TypeError), (("x", x, [3, 4], 1, 0), TypeError),
+                        (("x", x, (3, 4), 2, 0), TypeError), (("x", x, (3, 4), "1", 0), TypeError),
+                        (("x", x, (3, 5), 1, 0), ValueError), (("x", x, (3,), 1, 0), ValueError),
+                        (("x", x, (3, 4, 1), 1, 0), ValueError),
+                        (("x", x, (3, "4"), 1, 0), TypeError),
+                        (("x", x.T, (4, 3), 1, 0), ValueError),
+                        (("x", x.to_sparse(), (3, 4), 1, 0), ValueError),
+                        (("x", x, (3, 4), 1, 0), ValueError),      # not on a GPU
+                        (("x", x, (3, 4), 1, -1), ValueError), (("x", x), TypeError)):
+        for _ in range(3):
+            with pytest.raises(error):
+                ext.at(*args)
