@@ -5,8 +5,8 @@
 //   rstd = (mean_i h_i^2 + eps)^(-1/2),  y_i = (h_i rstd) w_i
 //   scale = fp16(max |y| / top) over a group, code_i = rnd(y_i / scale)
 //
-// One pass: a row stays in the registers of the threads that own it (64, 256
-// or 1024 of them, eight elements a chunk) from its load to its last store.
+// One pass: a row stays in the registers of the threads that own it (16 to
+// 1024 of them, eight elements a chunk) from its load to its last store.
 #include "bfly_norm.h"
 #include "bfly_rows.h"
 
@@ -31,7 +31,7 @@ __device__ __forceinline__ float inv_sqrt(double m) {
 // reading one is never overtaken by a wave that writes it again.
 template <int T, typename F>
 __device__ __forceinline__ F block_sum(F v, F* buf, int t) {
-  if constexpr (T == 64) return v;
+  if constexpr (T <= 64) return v;
   if ((t & 63) == 0) buf[t >> 6] = v;
   __syncthreads();
   F s = buf[0];
@@ -41,7 +41,7 @@ __device__ __forceinline__ F block_sum(F v, F* buf, int t) {
 }
 template <int T>
 __device__ __forceinline__ float block_max(float v, float* buf, int t) {
-  if constexpr (T == 64) return v;
+  if constexpr (T <= 64) return v;
   if ((t & 63) == 0) buf[t >> 6] = v;
   __syncthreads();
   float s = buf[0];
@@ -96,9 +96,12 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
   __shared__ double sums[2][T / 64];
   __shared__ float tops[2][T / 64];
   using X = RowIo<T, VEC, XB>;
+  constexpr int RPW = T < 64 ? 64 / T : 1;  // rows of a wave
   const int t = threadIdx.x & (T - 1);
-  const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / T);
-  const int n = P.n;
+  // the wave's first row in the workgroup, the lane's row in the wave
+  const int sub = T < 256 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64) * RPW : 0;
+  const int mine = T < 64 ? (int)(threadIdx.x & 63) / T : 0;
+  const int n = P.n, off = mine * n;
   const double inv_n = 1.0 / n;
   constexpr int es = XB ? 2 : 4;
 
@@ -111,33 +114,37 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[v][e] = 1.f;
       } else if (P.w_bf16) {
-        RowIo<T, VEC, true>::unpack(RowIo<T, VEC, true>::load(rw, t, v), w[v]);
+        RowIo<T, VEC, true>::unpack(RowIo<T, VEC, true>::load(rw, t, v, 0, n), w[v]);
       } else {
-        RowIo<T, VEC, false>::unpack(RowIo<T, VEC, false>::load(rw, t, v), w[v]);
+        RowIo<T, VEC, false>::unpack(RowIo<T, VEC, false>::load(rw, t, v, 0, n), w[v]);
       }
     }
   }
 
   typename X::Raw qx[V], qr[V];
   const auto load = [&](int64_t row) {  // past the last row: nothing is read
-    const int len = row < P.rows ? n : 0;
-    const __amdgpu_buffer_rsrc_t rx = row_range(P.x, row < P.rows ? row : 0, len, es);
+    const int64_t left = P.rows - row;
+    const int count = left < 0 ? 0 : left < RPW ? (int)left : RPW;
+    const int64_t at = count ? row : 0;
+    const __amdgpu_buffer_rsrc_t rx = row_range(P.x, at, n, es, count);
 #pragma unroll
-    for (int v = 0; v < V; ++v) qx[v] = X::load(rx, t, v);
+    for (int v = 0; v < V; ++v) qx[v] = X::load(rx, t, v, off, n);
     if (P.residual) {
-      const __amdgpu_buffer_rsrc_t rr = row_range(P.residual, row < P.rows ? row : 0, len, es);
+      const __amdgpu_buffer_rsrc_t rr = row_range(P.residual, at, n, es, count);
 #pragma unroll
-      for (int v = 0; v < V; ++v) qr[v] = X::load(rr, t, v);
+      for (int v = 0; v < V; ++v) qr[v] = X::load(rr, t, v, off, n);
     }
   };
   int turn = 0;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + sub;
   load(row);
-  for (; row < P.rows; row += step, turn ^= 1) {  // uniform over the rows' threads
+  for (; row < P.rows; row += step, turn ^= 1) {  // uniform over a row's threads
+    const int count = P.rows - row < RPW ? (int)(P.rows - row) : RPW;
+    const bool first = t == 0 && mine < count;  // the lane that writes a row's statistics
     float h[V][8];
     if (P.residual) {
-      const __amdgpu_buffer_rsrc_t rh = row_range(P.h, row, n, es);
+      const __amdgpu_buffer_rsrc_t rh = row_range(P.h, row, n, es, count);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float a[8], b[8];
@@ -146,7 +153,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] += b[e];
         const typename X::Raw q = X::pack(a);
-        if (P.h) X::store(rh, t, v, q);
+        if (P.h) X::store(rh, t, v, off, n, q);
         X::unpack(q, h[v]);
       }
     } else {
@@ -159,9 +166,9 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fma((double)h[v][e], (double)h[v][e], ss);
-    ss = block_sum<T>(wave_sum(ss), sums[turn], t);
+    ss = block_sum<T>(wave_sum<T < 64 ? T : 64>(ss), sums[turn], t);
     const float rstd = inv_sqrt(fma(ss, inv_n, (double)P.eps));
-    if (P.rstd && t == 0) P.rstd[row] = rstd;
+    if (P.rstd && first) P.rstd[row + mine] = rstd;
     float top = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -169,33 +176,37 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
       for (int e = 0; e < 8; ++e) h[v][e] = (h[v][e] * rstd) * w[v][e];
     if (P.y) {
       if (P.y_bf16) {
-        const __amdgpu_buffer_rsrc_t ry = row_range(P.y, row, n, 2);
+        const __amdgpu_buffer_rsrc_t ry = row_range(P.y, row, n, 2, count);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          RowIo<T, VEC, true>::store(ry, t, v, RowIo<T, VEC, true>::pack(h[v]));
+          RowIo<T, VEC, true>::store(ry, t, v, off, n, RowIo<T, VEC, true>::pack(h[v]));
       } else {
-        const __amdgpu_buffer_rsrc_t ry = row_range(P.y, row, n, 4);
+        const __amdgpu_buffer_rsrc_t ry = row_range(P.y, row, n, 4, count);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          RowIo<T, VEC, false>::store(ry, t, v, RowIo<T, VEC, false>::pack(h[v]));
+          RowIo<T, VEC, false>::store(ry, t, v, off, n, RowIo<T, VEC, false>::pack(h[v]));
       }
     }
     if constexpr (Q != 0) {
       constexpr float qtop = Q == 2 ? 448.f : 127.f;
-      const __amdgpu_buffer_rsrc_t rc = row_range(P.codes, row, n, 1);
+      const __amdgpu_buffer_rsrc_t rc = row_range(P.codes, row, n, 1, count);
       const int per_row = n / P.group;
-      uint16_t* const sc = P.scales + row * per_row;
+      uint16_t* const sc = P.scales + (row + mine) * per_row;
+      const auto code_offset = [&](int v, int e) {
+        const int i = X::index(t, v, e);
+        return T < 64 && i >= n ? kOutOfRange - 64u : (uint32_t)(off + i);
+      };
       float d = 0.f, r = 0.f;
       if (P.group == n) {  // one scale for the row
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(h[v][e]));
-        top = block_max<T>(run_max(top, 64), tops[turn], t);
+        top = block_max<T>(run_max(top, T < 64 ? T : 64), tops[turn], t);
         const _Float16 s = group_scale(top, qtop);
         d = (float)s;
         r = reciprocal(d);
-        if (t == 0) sc[0] = __builtin_bit_cast(uint16_t, s);
+        if (first) sc[0] = __builtin_bit_cast(uint16_t, s);
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -208,19 +219,19 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
           d = (float)s;
           r = reciprocal(d);
           const int i = X::index(t, v, 0);
-          if (i < n && (i & (P.group - 1)) == 0)
+          if (i < n && mine < count && (i & (P.group - 1)) == 0)
             sc[i / P.group] = __builtin_bit_cast(uint16_t, s);
         }
         const uint2 c = codes8<Q == 2>(h[v], d, r);
         if constexpr (VEC) {
           typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
           const u32x2 cw = {c.x, c.y};
-          __builtin_amdgcn_raw_buffer_store_b64(cw, rc, (v * T + t) * 8, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b64(cw, rc, (int)code_offset(v, 0), 0, 0);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             __builtin_amdgcn_raw_buffer_store_b8(
-                (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3))), rc, X::index(t, v, e), 0, 0);
+                (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3))), rc, (int)code_offset(v, e), 0, 0);
         }
       }
     }
@@ -242,9 +253,12 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
   __shared__ float sums[2][T / 64];
   using H = RowIo<T, VEC, HB>;
   using G = RowIo<T, VEC, GB>;
+  constexpr int RPW = T < 64 ? 64 / T : 1;  // rows of a wave
   const int t = threadIdx.x & (T - 1);
-  const int sub = __builtin_amdgcn_readfirstlane((int)threadIdx.x / T);
-  const int n = P.n;
+  // the wave's first row in the workgroup, the lane's row in the wave
+  const int sub = T < 256 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64) * RPW : 0;
+  const int mine = T < 64 ? (int)(threadIdx.x & 63) / T : 0;
+  const int n = P.n, off = mine * n;
   const float inv_n = 1.f / (float)n;
 
   float w[V][8], dw[V][8];
@@ -256,9 +270,9 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[v][e] = 1.f;
       } else if (P.w_bf16) {
-        RowIo<T, VEC, true>::unpack(RowIo<T, VEC, true>::load(rw, t, v), w[v]);
+        RowIo<T, VEC, true>::unpack(RowIo<T, VEC, true>::load(rw, t, v, 0, n), w[v]);
       } else {
-        RowIo<T, VEC, false>::unpack(RowIo<T, VEC, false>::load(rw, t, v), w[v]);
+        RowIo<T, VEC, false>::unpack(RowIo<T, VEC, false>::load(rw, t, v, 0, n), w[v]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) dw[v][e] = 0.f;
@@ -270,27 +284,27 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
   float rstd;
   const auto load = [&](int64_t row, typename H::Raw (&h)[V], typename G::Raw (&g)[V],
                         typename G::Raw (&d)[V], float& r) {
-    const bool in = row < P.rows;  // past the last row: nothing is read
-    const int len = in ? n : 0;
-    const int64_t at = in ? row : 0;
-    const __amdgpu_buffer_rsrc_t rh = row_range(P.h, at, len, HB ? 2 : 4);
-    const __amdgpu_buffer_rsrc_t rg = row_range(P.dy, at, len, GB ? 2 : 4);
+    const int64_t left = P.rows - row;  // past the last row: nothing is read
+    const int count = left < 0 ? 0 : left < RPW ? (int)left : RPW;
+    const int64_t at = count ? row : 0;
+    const __amdgpu_buffer_rsrc_t rh = row_range(P.h, at, n, HB ? 2 : 4, count);
+    const __amdgpu_buffer_rsrc_t rg = row_range(P.dy, at, n, GB ? 2 : 4, count);
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = H::load(rh, t, v);
+    for (int v = 0; v < V; ++v) h[v] = H::load(rh, t, v, off, n);
 #pragma unroll
-    for (int v = 0; v < V; ++v) g[v] = G::load(rg, t, v);
+    for (int v = 0; v < V; ++v) g[v] = G::load(rg, t, v, off, n);
     if (P.dh) {
-      const __amdgpu_buffer_rsrc_t rd = row_range(P.dh, at, len, GB ? 2 : 4);
+      const __amdgpu_buffer_rsrc_t rd = row_range(P.dh, at, n, GB ? 2 : 4, count);
 #pragma unroll
-      for (int v = 0; v < V; ++v) d[v] = G::load(rd, t, v);
+      for (int v = 0; v < V; ++v) d[v] = G::load(rd, t, v, off, n);
     }
-    r = P.rstd[at];
+    r = mine < count ? P.rstd[at + mine] : 0.f;
   };
   int turn = 0;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + sub;
   load(row, qh, qg, qd, rstd);
-  for (; row < P.rows; row += step, turn ^= 1) {  // uniform over the rows' threads
+  for (; row < P.rows; row += step, turn ^= 1) {  // uniform over a row's threads
     typename H::Raw nh[V];
     typename G::Raw ng[V], nd[V];
     float next;
@@ -308,8 +322,9 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
         c = fmaf(a, w[v][e], c);
       }
     }
-    c = block_sum<T>(wave_sum(c), sums[turn], t) * inv_n;
-    const __amdgpu_buffer_rsrc_t ro = row_range(P.dx, row, n, GB ? 2 : 4);
+    c = block_sum<T>(wave_sum<T < 64 ? T : 64>(c), sums[turn], t) * inv_n;
+    const __amdgpu_buffer_rsrc_t ro = row_range(
+        P.dx, row, n, GB ? 2 : 4, P.rows - row < RPW ? (int)(P.rows - row) : RPW);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float h[8], g[8], d[8];
@@ -324,7 +339,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         d[e] = fmaf(fmaf(-c, h[e] * rstd, g[e] * w[v][e]), rstd, d[e]);
-      G::store(ro, t, v, G::pack(d));
+      G::store(ro, t, v, off, n, G::pack(d));
     }
     if constexpr (AHEAD) {
 #pragma unroll
@@ -341,14 +356,14 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
 
   if (!P.dweight) return;
   const __amdgpu_buffer_rsrc_t rp = row_range(P.partials, blockIdx.x, n, 4);
-  if constexpr (RPB > 1) {  // the rows of a workgroup's waves, added in order
-    __shared__ float all[RPB][V * 8][64];
+  if constexpr (RPB > 1) {  // the rows of a workgroup, added in order
+    __shared__ float all[RPB][V * 8][T];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) all[sub][v * 8 + e][t] = dw[v][e];
+      for (int e = 0; e < 8; ++e) all[sub + mine][v * 8 + e][t] = dw[v][e];
     __syncthreads();
-    if (sub != 0) return;
+    if (sub + mine != 0) return;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -358,7 +373,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_bwd_kernel(NormBwdPara
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    RowIo<T, VEC, false>::store(rp, t, v, RowIo<T, VEC, false>::pack(dw[v]));
+    RowIo<T, VEC, false>::store(rp, t, v, 0, n, RowIo<T, VEC, false>::pack(dw[v]));
 }
 
 // dweight[i] = sum over slots of partials[slot][i]: 64 columns to a workgroup,
@@ -390,27 +405,31 @@ __global__ void __launch_bounds__(64 * kDwWays) norm_dw_kernel(const float* part
   if (n <= T * V * 8) return f(std::integral_constant<int, T>{}, std::integral_constant<int, V>{})
 template <typename F>
 hipError_t by_width(int n, F f) {
+  BFLY_WIDTH(16, 1);
   BFLY_WIDTH(64, 1);
   BFLY_WIDTH(64, 2);
   BFLY_WIDTH(256, 1);
   BFLY_WIDTH(256, 2);
   BFLY_WIDTH(256, 3);
   BFLY_WIDTH(256, 4);
+  BFLY_WIDTH(512, 3);
   BFLY_WIDTH(1024, 2);
   return hipErrorInvalidValue;
 }
 template <typename F>
 hipError_t by_width_bwd(int n, F f) {  // dw and the next row's loads need registers too
+  BFLY_WIDTH(16, 1);
   BFLY_WIDTH(64, 1);
   BFLY_WIDTH(64, 2);
   BFLY_WIDTH(256, 1);
   BFLY_WIDTH(256, 2);
   BFLY_WIDTH(512, 2);
+  BFLY_WIDTH(512, 3);
   BFLY_WIDTH(1024, 2);
   return hipErrorInvalidValue;
 }
 #undef BFLY_WIDTH
-int rows_per_block(int n) { return n <= 1024 ? 4 : 1; }
+int rows_per_block(int n) { return n <= 128 ? 16 : n <= 1024 ? 4 : 1; }
 
 // Workgroups of a forward launch at most: enough to give each of 8192 rows its
 // own (8192 x 4096: 44.0 us; 1024 workgroups that load their next row ahead

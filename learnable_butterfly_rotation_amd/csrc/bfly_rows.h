@@ -12,7 +12,8 @@ namespace bfly {
 //   not VEC element (8v + e)*T + t: accesses of one element, consecutive over
 //           the lanes (rows of any length)
 // Reads past the row's end give zeros and writes there are dropped (the
-// buffer's range check).
+// buffer's range check).  With T < 64 the buffer holds the 64 / T rows of a
+// wave, `row` is the element its lane's row starts at and `n` the rows' length.
 template <int T, bool VEC, bool BF>
 struct RowIo {
   // eight elements as they lie in memory (BF: four words, else eight)
@@ -22,10 +23,18 @@ struct RowIo {
   static __device__ __forceinline__ int index(int t, int v, int e) {
     return VEC ? (v * T + t) * 8 + e : (v * 8 + e) * T + t;
   }
-  static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t r, int t, int v) {
+  static constexpr uint32_t es = BF ? 2u : 4u;
+  // byte offset of element (v, e), beyond every range where it is past the row
+  static __device__ __forceinline__ uint32_t offset(int t, int v, int e, int row, int n) {
+    const int i = index(t, v, e);
+    if constexpr (T < 64) return i < n ? (uint32_t)(row + i) * es : kOutOfRange - 64u;
+    return (uint32_t)i * es;
+  }
+  static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t r, int t, int v, int row,
+                                             int n) {
     Raw q;
     if constexpr (VEC) {
-      const uint32_t off = (uint32_t)(v * T + t) * (BF ? 16u : 32u);
+      const uint32_t off = offset(t, v, 0, row, n);
       const uint4 a = buf_ld16(r, off);
       q.w[0] = a.x;
       q.w[1] = a.y;
@@ -41,11 +50,11 @@ struct RowIo {
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t i = (uint32_t)index(t, v, e);
+        const uint32_t off = offset(t, v, e, row, n);
         if constexpr (BF)
-          q.w[e] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(2u * i), 0, 0);
+          q.w[e] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
         else
-          q.w[e] = buf_ld4(r, 4u * i);
+          q.w[e] = buf_ld4(r, off);
       }
     }
     return q;
@@ -76,31 +85,32 @@ struct RowIo {
     return q;
   }
   template <int POLICY = kCached>
-  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int t, int v,
-                                               const Raw& q) {
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int t, int v, int row,
+                                               int n, const Raw& q) {
     if constexpr (VEC) {
-      const uint32_t off = (uint32_t)(v * T + t) * (BF ? 16u : 32u);
+      const uint32_t off = offset(t, v, 0, row, n);
       buf_st16<POLICY>(r, off, make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]));
       if constexpr (!BF)
         buf_st16<POLICY>(r, off + 16u, make_uint4(q.w[4], q.w[5], q.w[6], q.w[7]));
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t i = (uint32_t)index(t, v, e);
+        const uint32_t off = offset(t, v, e, row, n);
         if constexpr (BF)
-          buf_st2<POLICY>(r, 2u * i, (uint16_t)q.w[e]);
+          buf_st2<POLICY>(r, off, (uint16_t)q.w[e]);
         else
-          buf_st4<POLICY>(r, 4u * i, q.w[e]);
+          buf_st4<POLICY>(r, off, q.w[e]);
       }
     }
   }
 };
 
-// Row r of a matrix of n elements of es bytes; empty where there is no matrix.
+// Rows r .. r + count - 1 of n elements of es bytes; empty where there is no
+// matrix.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_range(const void* base, int64_t r, int n,
-                                                            int es) {
+                                                            int es, int count = 1) {
   return buffer_range32(static_cast<const char*>(base) + r * n * es,
-                        base ? (uint32_t)n * (uint32_t)es : 0u);
+                        base ? (uint32_t)count * (uint32_t)n * (uint32_t)es : 0u);
 }
 
 // The value of another lane of the same 16 (DPP): 0xB1 lane ^ 1, 0x4E lane ^ 2,
@@ -129,13 +139,16 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
   return __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
 }
-// Sum over the wave's 64 lanes, in a fixed order, the same in every lane.
-template <typename F>
+// Sum over the wave's 64 lanes (or each 16 of them), in a fixed order, the
+// same in every lane.
+template <int LANES = 64, typename F>
 __device__ __forceinline__ F wave_sum(F v) {
+  static_assert(LANES == 16 || LANES == 64, "16 or 64 lanes");
   v += dpp<0xB1>(v);
   v += dpp<0x4E>(v);
   v += dpp<0x141>(v);
   v += dpp<0x140>(v);
+  if constexpr (LANES == 16) return v;
   return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 // Maximum over 1, 2, 4 .. 64 consecutive lanes (an aligned run of `lanes`).

@@ -109,7 +109,7 @@ def check_norm(x, res, w, y_dt, fmt, group, h_out=True):
         assert np.array_equal(codes[:rows].cpu().numpy(), c)
 
 
-WIDTHS = [1, 2, 7, 8, 63, 64, 200, 256, 511, 512, 520, 1000, 1023, 1024, 1025, 1032, 2047, 2048,
+WIDTHS = [1, 2, 7, 8, 63, 64, 72, 127, 128, 129, 136, 200, 256, 511, 512, 520, 1000, 1023, 1024, 1025, 1032, 2047, 2048,
           2056, 4095, 4096, 4104, 5120, 8191, 8192, 8200, 11008, 16383, 16384]
 
 
@@ -126,8 +126,10 @@ def test_norm_widths(n, x_dt):
 
 
 @pytest.mark.parametrize("group", [8, 16, 32, 64, 128, 256, 512])
-@pytest.mark.parametrize("n", [512, 1024, 2048, 1536, 4096, 5120, 11776, 16384])
+@pytest.mark.parametrize("n", [64, 128, 512, 1024, 2048, 1536, 4096, 5120, 11776, 16384])
 def test_norm_groups(group, n):
+    if group > n:
+        pytest.skip("the group is longer than the row")
     x, res = rows_of(n + group, 6, n, BF16), rows_of(n + group + 1, 6, n, BF16)
     w = 1 + 0.1 * torch.randn(n, generator=torch.Generator().manual_seed(n))
     check_norm(x, res, w, None, B.BFLY_Q8_INT8, group)
@@ -135,7 +137,7 @@ def test_norm_groups(group, n):
 
 
 @pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 2047, 2048, 2049, 8191, 8195])
-@pytest.mark.parametrize("n", [64, 256, 1031, 4096])
+@pytest.mark.parametrize("n", [64, 100, 128, 256, 1031, 4096])
 def test_norm_rows(rows, n):
     x, res = rows_of(rows, rows, n, BF16), rows_of(rows + 1, rows, n, BF16)
     check_norm(x, res, None, BF16, B.BFLY_Q8_INT8, n)
@@ -226,9 +228,10 @@ def check_backward(h, w, dy, dh, in_place=False):
     tol = r64 * (4 * U * (np.abs(g) + np.abs(xhat * c)) + np.abs(xhat) * (38 + 5) * U * cabs)
     tol = 1.01 * tol + (U if dy.dtype == F32 else half(BF16)) * (np.abs(want) + tol) + U * np.abs(want)
     assert (np.abs(np64(dx[:rows]) - want) <= tol).all()
-    slots = -(-rows // (4 if n <= 1024 else 1))
+    together = 16 if n <= 128 else 4 if n <= 1024 else 1  # rows of a workgroup
+    slots = -(-rows // together)
     slots = min(slots, 1024 if n <= 1024 else 256 if n >= 4096 else (1 << 20) // n)
-    depth = -(-rows // slots) + 3 + -(-slots // 16) + 15 + 2
+    depth = -(-rows // slots) + together - 1 + -(-slots // 16) + 15 + 2
     term = dy64 * xhat
     tol = 1.01 * depth * U * np.abs(term).sum(0)
     assert (np.abs(np64(dw) - term.sum(0)) <= tol).all()
@@ -245,7 +248,7 @@ def test_backward_widths(n, h_dt, g_dt):
 
 
 @pytest.mark.parametrize("rows", [1, 3, 4, 1023, 1025, 4097, 5000])
-@pytest.mark.parametrize("n", [256, 1023, 2048])
+@pytest.mark.parametrize("n", [64, 101, 256, 1023, 2048])
 def test_backward_rows(rows, n):
     check_backward(rows_of(rows, rows, n, BF16), None, rows_of(rows + 1, rows, n, BF16),
                    rows_of(rows + 2, rows, n, BF16))
