@@ -376,8 +376,13 @@ struct Expand {
   }
 };
 
+// Waves to a SIMD asked for where the compiler would give one fewer: what the
+// loads of one workgroup wait for, another's fill (8192 x 4096 to 4096, rank
+// 128: 61 us with 2 waves, 49 with 3, a few registers of it spilled; all of a
+// tile's base loaded ahead instead, 2 waves at rank 64: 44 us for 34).
 template <int TERMS, bool BB, bool YB, int DK>
-__global__ void __launch_bounds__(kThreads) expand_kernel(LoraParams P, int splits, int stride) {
+__global__ void __launch_bounds__(kThreads, DK == 2 ? 4 : DK == 4 && TERMS == 2 ? 3 : 1)
+    expand_kernel(LoraParams P, int splits, int stride) {
   using E = Expand<TERMS, BB, YB, DK>;
   constexpr int JT = E::JT;
   __shared__ Tiles tiles;
