@@ -11,11 +11,13 @@ namespace bfly {
 // workgroup.  A tensor's granules start at the 16-byte boundary at or below
 // its first element, so that every whole vector in them is aligned.
 constexpr int kClipGranule = 4096;
-// Slots at most, of a call of up to kClipFew granules (64M elements: about
-// what the last-level cache holds of them) and of a larger one (300 tensors, 27M
-// bf16 elements: 40.8 us with 2048, 44.7 with 1024).
+// Slots at most, of a call of up to kClipFewBytes bytes of gradients and of a
+// larger one.  300 tensors, 27M bf16 elements (54 MB): 40.8 us with 2048, 44.7
+// with 1024.  The larger calls' way (bfly_clip.hip) against the other: 52 MB
+// 32.3 us and 31.5, 54 MB in 300 tensors 46 and 41, 67 MB 33.4 and 39.7, 108 MB
+// 63.5 and 74.4, 154 MB 80 and 104.
 constexpr int kClipSlots = 2048, kClipManySlots = 8192;
-constexpr int kClipFew = 16384;
+constexpr int64_t kClipFewBytes = 56 << 20;
 
 // One tensor of the table.
 struct ClipTensor {

@@ -6,7 +6,7 @@
 // Squares are summed in fp64 (an fp32 square overflows above 1.8e19 and loses
 // everything below 1e-23, and a sum over 10^9 elements loses half its digits).
 // Two passes over the data, both bound by memory: the slots' sums, then the
-// scaling.  With few granules its every workgroup first adds the (at most
+// scaling.  With few bytes its every workgroup first adds the (at most
 // 2048) slot sums itself, in a fixed order; with many a launch between does.
 #include "bfly_clip.h"
 #include "bfly_rows.h"
@@ -218,7 +218,7 @@ __device__ __forceinline__ void scale_slot(const ClipTensor* tab, const Slots& S
   });
 }
 
-// Many granules: the norm by one workgroup, then a granule to a workgroup at
+// Many bytes: the norm by one workgroup, then a granule to a workgroup at
 // a time, neighbours together, past the caches (721M fp32 elements: 1429 us
 // as 1024 ranges through the caches).
 __global__ void __launch_bounds__(kThreads) factor_kernel(Slots S, const double* sums,
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) scale_many_few_kernel(Batch b, Slots
 hipError_t launch_grad_clip(const ClipParams& p, hipStream_t s) {
   double* sums = static_cast<double*>(p.workspace);
   ClipTensor* tab = reinterpret_cast<ClipTensor*>(static_cast<char*>(p.workspace) + kClipTableOffset);
-  int64_t granules = 0;
+  int64_t granules = 0, bytes = 0;
   int count = 0, held = 0;  // tensors that are not empty; those of them in the batch
   for (int i = 0; i < p.count; ++i) count += p.numel[i] > 0;
   const bool few = count <= kClipBatch;
@@ -287,6 +287,7 @@ hipError_t launch_grad_clip(const ClipParams& p, hipStream_t s) {
     t.first = (int32_t)granules;
     t.kind = p.dtype[i] + 2 * skip;
     granules += (t.end + kClipGranule - 1) / kClipGranule;
+    bytes += p.numel[i] * es;
     ++at;
     if (!few && (held == kClipBatch || at == count)) {
       hipLaunchKernelGGL(table_kernel, dim3(1), dim3(128), 0, s, b, held, tab + at - held);
@@ -299,7 +300,7 @@ hipError_t launch_grad_clip(const ClipParams& p, hipStream_t s) {
   S.table = tab;
   S.count = count;
   S.granules = (int)granules;
-  const bool many = granules > kClipFew;
+  const bool many = bytes > kClipFewBytes;
   const int most = many ? kClipManySlots : kClipSlots;
   S.per_slot = (int)(granules > most ? (granules + most - 1) / most : 1);
   S.slots = (int)((granules + S.per_slot - 1) / S.per_slot);

@@ -72,8 +72,8 @@ def test_clip_sizes(sizes, dtypes, in_place):
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("count", [3, 300])
 def test_clip_many_elements(count, in_place):
-    # beyond 2^26 elements the norm has a launch of its own; the sizes are odd
-    # and the tensors views that start anywhere
+    # beyond 56 MiB the norm has a launch of its own; the sizes are odd and the
+    # tensors views that start anywhere
     g = torch.Generator().manual_seed(count)
     each = (70 << 20) // count
     sizes = [each - 7 * i for i in range(count)]
