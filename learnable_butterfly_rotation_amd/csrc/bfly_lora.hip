@@ -316,7 +316,10 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int spli
 // The matrix cores' columns are columns of y: tile j of JT takes columns
 // JT n + j as its columns n, so that a lane is left with JT consecutive
 // columns of a row and 16 lanes with a run of 16 JT (memory in whole lines).
-// DK: runs of 32 ranks.
+// DK: runs of 32 ranks.  base and y go past the caches (nt): through them they
+// drive out B and t, which every column tile and block of rows reads again
+// (8192 rows, 4096 to 11008, rank 32: 458 MB fetched and 134.6 us, 399 MB and
+// 120.4 so; either of the two alone 130 and 136 us).
 template <int TERMS, bool BB, bool YB, int DK>
 struct Expand {
   static constexpr int JT = 4;                 // 8: 138 us for 135 of a prompt's call
@@ -337,13 +340,13 @@ struct Expand {
       const bool in = ro[i] != kOutOfRange && c < n_out;
       const uint32_t at = in ? (ro[i] + (uint32_t)c) * (BB ? 2u : 4u) : kOutOfRange;
       if constexpr (kBaseWords == 2) {
-        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, 0);
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, kNonTemporal);
         f.w[i][0] = v.x;
         f.w[i][1] = v.y;
       } else {
 #pragma unroll
         for (int k = 0; k < kBaseWords; k += 4) {
-          const uint4 v = buf_ld16(r, in ? at + 4u * k : kOutOfRange);
+          const uint4 v = buf_ld16<kNonTemporal>(r, in ? at + 4u * k : kOutOfRange);
           f.w[i][k] = v.x;
           f.w[i][k + 1] = v.y;
           f.w[i][k + 2] = v.z;
@@ -366,11 +369,11 @@ struct Expand {
       w[k] = YB ? pack_bf16(v[(2 * k) % JT], v[(2 * k + 1) % JT]) : __float_as_uint(v[k % JT]);
     if constexpr (kYWords == 2) {
       const u32x2 q = {w[0], w[1]};
-      __builtin_amdgcn_raw_buffer_store_b64(q, r, (int)at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(q, r, (int)at, 0, kNonTemporal);
     } else {
 #pragma unroll
       for (int k = 0; k < kYWords; k += 4)
-        buf_st16(r, in ? at + 4u * k : kOutOfRange,
+        buf_st16<kNonTemporal>(r, in ? at + 4u * k : kOutOfRange,
                  make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]));
     }
   }
