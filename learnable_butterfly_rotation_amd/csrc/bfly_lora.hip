@@ -41,25 +41,81 @@ struct Tiles {
   __device__ int id(int place) const { return (int)(sorted[place] >> 8); }
 };
 
-// Every thread ranks its own row against all the others (the keys are in LDS,
-// read four at a time as broadcasts): no sort, no atomics, and any ids.
+// A row's place by counting, for adapters below 256 (`none`: the number that
+// stands for no adapter): its rank among its wave's rows of the same adapter
+// from ballots over the number's bits, after the rows of the same adapter in
+// earlier waves and those of smaller numbers.  Every workgroup of a block gets
+// the same order, which atomics would not give.
+__device__ __forceinline__ int count_place(uint16_t (&bins)[kBlockRows / 64][256],
+                                           int (&totals)[kBlockRows / 64], int id, bool valid) {
+  const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
+  uint32_t* const words = reinterpret_cast<uint32_t*>(bins);
+  words[i] = 0;
+  words[i + 256] = 0;
+  uint64_t same = __ballot(valid);
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const bool bit = (id >> b) & 1;
+    const uint64_t m = __ballot(bit);
+    same &= bit ? m : ~m;
+  }
+  const int before = __popcll(same & ((1ull << lane) - 1));
+  __syncthreads();
+  if (valid && before == 0) bins[wave][id] = (uint16_t)__popcll(same);
+  __syncthreads();
+  // thread i adds bin i of the waves up, then all bins below it
+  int of[kBlockRows / 64], sum = 0;
+#pragma unroll
+  for (int w = 0; w < kBlockRows / 64; ++w) {
+    of[w] = sum;
+    sum += bins[w][i];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int v = __shfl_up(upto, d);
+    upto += lane >= d ? v : 0;
+  }
+  if (lane == 63) totals[wave] = upto;
+  __syncthreads();
+  int base = upto - sum;
+  for (int w = 0; w < wave; ++w) base += totals[w];
+#pragma unroll
+  for (int w = 0; w < kBlockRows / 64; ++w) bins[w][i] = (uint16_t)(base + of[w]);
+  __syncthreads();
+  return valid ? bins[wave][id] + before : i;
+}
+
+// The places come from counting where the rows are many and the adapters few,
+// else every thread ranks its own row against all the others (the keys are in
+// LDS, read four at a time as broadcasts): no sort, no atomics, and any ids.
+// Counting and ranking, a whole call: 512 rows of 4 adapters, rank 16, 14.7 us
+// and 16.5; 257 rows of 32, rank 64, 28.1 and 29.9; 16 rows of 8 10.2 and 9.5.
 __device__ __forceinline__ void make_tiles(Tiles& s, const int32_t* ids, int nr, int n_adapters) {
   const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
   uint32_t key = ~0u;
+  int id = kNoAdapter;
   if (i < nr) {
-    const int id = ids[i];
-    key = (uint32_t)(id >= 0 && id < n_adapters ? id : kNoAdapter) << 8 | (uint32_t)i;
+    id = ids[i];
+    if (id < 0 || id >= n_adapters) id = kNoAdapter;
+    key = (uint32_t)id << 8 | (uint32_t)i;
   }
   s.key[i] = key;
   __syncthreads();
   int place = i;
   // packed prompts mostly come in order: nothing to rank then
   if (!__syncthreads_and(i == 0 || s.key[i - 1] <= key)) {
-    place = 0;
+    if (n_adapters < 256 && nr > 64) {
+      __shared__ uint16_t bins[kBlockRows / 64][256];
+      __shared__ int totals[kBlockRows / 64];
+      place = count_place(bins, totals, id == kNoAdapter ? n_adapters : id, i < nr);
+    } else {
+      place = 0;
 #pragma unroll 4
-    for (int j = 0; j < nr; j += 4) {  // past nr: the largest value, never below
-      const uint4 o = *reinterpret_cast<const uint4*>(s.key + j);
-      place += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
+      for (int j = 0; j < nr; j += 4) {  // past nr: the largest value, never below
+        const uint4 o = *reinterpret_cast<const uint4*>(s.key + j);
+        place += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
+      }
     }
   }
   if (i < nr) s.sorted[place] = key;

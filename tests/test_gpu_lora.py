@@ -150,6 +150,16 @@ def test_every_row_its_own_adapter():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("num", [1, 2, 255, 256, 257])
+@pytest.mark.parametrize("rows", [64, 65, 128, 200, 256, 321])
+def test_numbers_of_adapters(num, rows):
+    rng = np.random.default_rng(num + rows)
+    for ids in (rng.integers(-1, num, rows), num - 1 - np.arange(rows) % min(num, 7),
+                np.where(np.arange(rows) % 3 == 0, num - 1, 0)):
+        c = Case(rows, 128, 64, 8, num, ids=ids)
+        c.check(c.run())
+
+
 def test_ids_out_of_range():
     c = Case(7, 128, 64, 8, 3, ids=[0, 3, 2, -2147483648, 2147483647, -1, 1])
     c.check(c.run())
