@@ -461,10 +461,13 @@ hipError_t norm_bwd_run(const NormBwdParams& p, hipStream_t s) {
 // 256 to 1024 slots, 4 MiB of partial sums where that allows it: writing and
 // adding them costs 16384 x 5120 fp32 6 us at 256 slots and 18 at 1024
 // (182 and 194 us in all), while narrow rows need the workgroups to have
-// enough loads in flight.
+// enough loads in flight.  With many rows more of them, so that a thread's
+// fp32 sum goes over about 128 rows.
 int rmsnorm_bwd_slots(int64_t rows, int n) {
   const int64_t need = (rows + rows_per_block(n) - 1) / rows_per_block(n);
-  const int64_t most = n <= 1024 ? 1024 : n >= 4096 ? 256 : (1 << 20) / n;
+  int64_t most = n <= 1024 ? 1024 : n >= 4096 ? 256 : (1 << 20) / n;
+  const int64_t many = need / 128 < 2048 ? need / 128 : 2048;
+  if (most < many) most = many;
   return (int)(need < most ? need : most);
 }
 

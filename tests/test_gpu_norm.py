@@ -230,8 +230,9 @@ def check_backward(h, w, dy, dh, in_place=False):
     assert (np.abs(np64(dx[:rows]) - want) <= tol).all()
     together = 16 if n <= 128 else 4 if n <= 1024 else 1  # rows of a workgroup
     slots = -(-rows // together)
-    slots = min(slots, 1024 if n <= 1024 else 256 if n >= 4096 else (1 << 20) // n)
-    depth = -(-rows // slots) + together - 1 + -(-slots // 16) + 15 + 2
+    most = 1024 if n <= 1024 else 256 if n >= 4096 else (1 << 20) // n
+    groups, slots = slots, min(slots, max(most, min(2048, slots // 128)))
+    depth = -(-groups // slots) + together - 1 + -(-slots // 16) + 15 + 2
     term = dy64 * xhat
     tol = 1.01 * depth * U * np.abs(term).sum(0)
     assert (np.abs(np64(dw) - term.sum(0)) <= tol).all()
@@ -252,6 +253,31 @@ def test_backward_widths(n, h_dt, g_dt):
 def test_backward_rows(rows, n):
     check_backward(rows_of(rows, rows, n, BF16), None, rows_of(rows + 1, rows, n, BF16),
                    rows_of(rows + 2, rows, n, BF16))
+
+
+@pytest.mark.parametrize("rows,n", [(70000, 1500), (40000, 4096), (500000, 16)])
+def test_backward_many_rows(rows, n):
+    # beyond 128 rows to a thread's sum there are more partial sums
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    h, dy = (torch.randn((rows, n), generator=g, device="cuda") for _ in range(2))
+    rstd = torch.rsqrt(h.double().square().mean(1) + EPS).float()
+    dx, dw = torch.empty_like(h), torch.empty(n, device="cuda")
+    ws = torch.empty(B.bfly_rmsnorm_backward_workspace_bytes(rows, n), dtype=torch.uint8,
+                     device="cuda")
+    B.bfly_rmsnorm_backward(h, None, rstd, dy, dx, dweight=dw, workspace=ws)
+    want = torch.zeros(n, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for i in range(0, rows, 10000):
+        t = dy[i:i + 10000].double() * h[i:i + 10000].double() * rstd[i:i + 10000, None].double()
+        want += t.sum(0)
+        size += t.abs().sum(0)
+    # two roundings of a term; 200 of a thread, its workgroup's and the slots'
+    # sums (at most 16 + 128 + 16) at the very most
+    assert ((dw.double() - want).abs() <= 1.01 * (2 + 200 + 160) * U * size).all()
+    # and as random roundings add up, far closer: 2^-24 sqrt(362) of the 2-norm
+    # of the terms' partial sums, which the sum's own size (~ sqrt(rows)) bounds
+    err = float((dw.double() - want).norm() / want.norm())
+    assert err <= 362 ** 0.5 * U
 
 
 def test_backward_in_place():
