@@ -181,23 +181,29 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-_extension = None
+_extension = _torch = _bfloat16 = None
 
 
 def _ext():
     """The extension that checks tensors: at(name, tensor, shape, kinds,
     device) gives the address of a contiguous tensor of that shape, of one of
     these types and on that GPU (None for None), or raises."""
-    global _extension
+    global _extension, _torch, _bfloat16
     if _extension is None:
         import importlib
-        import torch  # noqa: F401  (the extension needs its libraries loaded)
+        import torch  # before the extension, which needs its libraries loaded
+        _torch, _bfloat16 = torch, torch.bfloat16
         try:
             _extension = importlib.import_module("._tensors", __name__)
         except ImportError as e:
             raise RuntimeError("the _tensors extension is not built: run "
                                "`python -m learnable_butterfly_rotation_amd.build`") from e
     return _extension
+
+
+def _kind(t):
+    """The bfly_dtype of rows that at() has found to be float32 or bfloat16."""
+    return BFLY_BF16 if t.dtype is _bfloat16 else BFLY_F32
 
 
 # the types of at(), as bits
@@ -217,16 +223,15 @@ def _scratch(workspace, device):
 def _call(name, device, stream, *args):
     """The library's `name` with `args` and a stream: the caller's, or torch's
     current one of the arguments' device, which is made current for the call."""
-    import torch
     if device < 0:
         raise ValueError("%s: the tensors have to be on a GPU" % name)
-    f = getattr(lib(), name)
+    f = getattr(_lib or lib(), name)
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
+        stream = _torch._C._cuda_getCurrentRawStream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() != device:
-        with torch.cuda.device(device):
+    if _torch.cuda.current_device() != device:
+        with _torch.cuda.device(device):
             status = f(*args, stream)
     else:
         status = f(*args, stream)
@@ -438,12 +443,12 @@ def bfly_rmsnorm(x, weight, eps, y=None, codes=None, scales=None, residual=None,
         group = n
     dev = x.get_device()
     px = at("x", x, shape, _ROWS, dev)
-    x_dt = _dt(x)
+    x_dt = _kind(x)
     same = _BF16 if x_dt else _F32
     _call("bfly_rmsnorm", dev, stream, px, x_dt, at("residual", residual, shape, same, dev),
           at("h", h, shape, same, dev), at("weight", weight, (n,), _ROWS, dev),
-          0 if weight is None else _dt(weight), at("y", y, shape, _ROWS, dev),
-          0 if y is None else _dt(y), at("codes", codes, shape, _BYTES, dev),
+          0 if weight is None else _kind(weight), at("y", y, shape, _ROWS, dev),
+          0 if y is None else _kind(y), at("codes", codes, shape, _BYTES, dev),
           at("scales", scales, (rows, n // group if group > 0 else 0), _F16, dev),
           at("rstd", rstd, (rows,), _F32, dev), rows, n, eps, format, group)
 
@@ -462,11 +467,11 @@ def bfly_rmsnorm_backward(h, weight, rstd, dy, dx, dweight=None, dh=None, worksp
     shape = rows, n = h.shape
     dev = h.get_device()
     pdy = at("dy", dy, shape, _ROWS, dev)
-    g_dt = _dt(dy)
+    g_dt = _kind(dy)
     same = _BF16 if g_dt else _F32
     ws, ws_bytes = _scratch(workspace, dev)
-    _call("bfly_rmsnorm_backward", dev, stream, at("h", h, shape, _ROWS, dev), _dt(h),
-          at("weight", weight, (n,), _ROWS, dev), 0 if weight is None else _dt(weight),
+    _call("bfly_rmsnorm_backward", dev, stream, at("h", h, shape, _ROWS, dev), _kind(h),
+          at("weight", weight, (n,), _ROWS, dev), 0 if weight is None else _kind(weight),
           at("rstd", rstd, (rows,), _F32, dev), pdy, at("dh", dh, shape, same, dev),
           at("dx", dx, shape, same, dev), g_dt, at("dweight", dweight, (n,), _F32, dev), rows, n,
           ws, ws_bytes)
@@ -494,8 +499,8 @@ def bfly_lora_matmul(x, ids, lora_a, lora_b, scaling, y, workspace, base=None,
           at("ids", ids, (rows,), _I32, dev), at("lora_a", lora_a, (num, rank, k), _BF16, dev),
           at("lora_b", lora_b, (num, n_out, rank), _BF16, dev),
           at("scaling", scaling, (num,), _F32, dev),
-          at("base", base, (rows, n_out), _ROWS, dev), 0 if base is None else _dt(base),
-          at("y", y, (rows, n_out), _ROWS, dev), _dt(y), rows, n_out, k, num, rank, ws, ws_bytes)
+          at("base", base, (rows, n_out), _ROWS, dev), 0 if base is None else _kind(base),
+          at("y", y, (rows, n_out), _ROWS, dev), _kind(y), rows, n_out, k, num, rank, ws, ws_bytes)
 
 
 def bfly_grad_clip_workspace_bytes(count: int) -> int:

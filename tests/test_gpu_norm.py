@@ -125,11 +125,10 @@ def test_norm_widths(n, x_dt):
     check_norm(x, res, None, BF16, None, None, h_out=False)
 
 
-@pytest.mark.parametrize("group", [8, 16, 32, 64, 128, 256, 512])
-@pytest.mark.parametrize("n", [64, 128, 512, 1024, 2048, 1536, 4096, 5120, 11776, 16384])
+@pytest.mark.parametrize("group,n", [(g, n) for g in (8, 16, 32, 64, 128, 256, 512) for n in
+                                     (64, 128, 512, 1024, 2048, 1536, 4096, 5120, 11776, 16384)
+                                     if g <= n])
 def test_norm_groups(group, n):
-    if group > n:
-        pytest.skip("the group is longer than the row")
     x, res = rows_of(n + group, 6, n, BF16), rows_of(n + group + 1, 6, n, BF16)
     w = 1 + 0.1 * torch.randn(n, generator=torch.Generator().manual_seed(n))
     check_norm(x, res, w, None, B.BFLY_Q8_INT8, group)
