@@ -434,7 +434,8 @@ bfly_status bfly_quant_matmul(const void* a, bfly_dtype a_dt, const uint8_t* cod
 /* ---- the norm in front of a layer ----------------------------------------- */
 
 /* Formats of the 8-bit rows of bfly_rmsnorm.  Both take one fp16 scale per
- * group, scale = fp16(max |y| / top) (saturated at 65504), and store
+ * group, scale = fp16(max |y| / top) (saturated at 65504; the quotient as a
+ * product with top's fp32 reciprocal, as in the quantizers above), and store
  * code = rnd(clamp(y / scale, -top, top)), to nearest, ties to even; a zero
  * scale gives zero codes.
  *   BFLY_Q8_INT8 : top = 127, two's-complement bytes (BFLY_SYM_ABSMAX at 8 bits)

@@ -50,9 +50,11 @@ __device__ __forceinline__ float block_max(float v, float* buf, int t) {
   return s;
 }
 
-// fp16(amax / top), saturated at the largest fp16 value.
-__device__ __forceinline__ _Float16 group_scale(float amax, float top) {
-  return (_Float16)fminf(amax / top, 65504.f);
+// fp16(amax / top), saturated at the largest fp16 value; the quotient as a
+// product with top's fp32 reciprocal, as the forward's quantizer takes it (it
+// can differ from the rounded quotient only next to an fp16 rounding midpoint).
+__device__ __forceinline__ _Float16 group_scale(float amax, float inv_top) {
+  return (_Float16)fminf(amax * inv_top, 65504.f);
 }
 
 // The codes of eight values, four to a word; d the group's scale, r = 1 / d
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
       }
     }
     if constexpr (Q != 0) {
-      constexpr float qtop = Q == 2 ? 448.f : 127.f;
+      constexpr float inv_top = 1.f / (Q == 2 ? 448.f : 127.f);
       const __amdgpu_buffer_rsrc_t rc = row_range(P.codes, row, n, 1, count);
       const int per_row = n / P.group;
       uint16_t* const sc = P.scales + (row + mine) * per_row;
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(h[v][e]));
         top = block_max<T>(run_max(top, T < 64 ? T : 64), tops[turn], t);
-        const _Float16 s = group_scale(top, qtop);
+        const _Float16 s = group_scale(top, inv_top);
         d = (float)s;
         r = reciprocal(d);
         if (first) sc[0] = __builtin_bit_cast(uint16_t, s);
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[v][e]));
           m = run_max(m, P.group >> 3);
-          const _Float16 s = group_scale(m, qtop);
+          const _Float16 s = group_scale(m, inv_top);
           d = (float)s;
           r = reciprocal(d);
           const int i = X::index(t, v, 0);

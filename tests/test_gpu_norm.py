@@ -57,7 +57,8 @@ def quantized(y32, group, e4m3):
     rows, n = y32.shape
     top = np.float32(448.0 if e4m3 else 127.0)
     v = y32.reshape(rows, n // group, group)
-    s = np.minimum(np.abs(v).max(2) / top, np.float32(65504)).astype(np.float16)
+    # the quotient by top is a product with its fp32 reciprocal
+    s = np.minimum(np.abs(v).max(2) * (np.float32(1) / top), np.float32(65504)).astype(np.float16)
     d = s.astype(np.float32)[:, :, None]
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
         q = np.where(d > 0, v / d, np.float32(0))
