@@ -13,12 +13,9 @@
 #include "bfly_lora.h"
 #include "bfly_rows.h"
 
-#include <type_traits>
-
 namespace bfly {
 namespace {
 
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -49,9 +46,8 @@ struct Tiles {
 __device__ __forceinline__ int count_place(uint16_t (&bins)[kBlockRows / 64][256],
                                            int (&totals)[kBlockRows / 64], int id, bool valid) {
   const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
-  uint32_t* const words = reinterpret_cast<uint32_t*>(bins);
-  words[i] = 0;
-  words[i + 256] = 0;
+#pragma unroll
+  for (int w = 0; w < kBlockRows / 64; ++w) bins[w][i] = 0;
   uint64_t same = __ballot(valid);
 #pragma unroll
   for (int b = 0; b < 8; ++b) {
@@ -372,14 +368,17 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int spli
 // The matrix cores' columns are columns of y: tile j of JT takes columns
 // JT n + j as its columns n, so that a lane is left with JT consecutive
 // columns of a row and 16 lanes with a run of 16 JT (memory in whole lines).
-// DK: runs of 32 ranks.  base and y go past the caches (nt): through them they
-// drive out B and t, which every column tile and block of rows reads again
-// (8192 rows, 4096 to 11008, rank 32: 458 MB fetched and 134.6 us, 399 MB and
-// 120.4 so; either of the two alone 130 and 136 us).
+// DK: runs of 32 ranks at a time, H times after each other.  H is 2 above 128
+// ranks, with the sums of a tile's rows waiting in registers: all of B's 256
+// ranks at once leave one wave to a SIMD (8192 x 4096 to 4096: 157 us, 104 so).
+// base and y go past the caches (nt): through them they drive out B and t,
+// which every column tile and block of rows reads again (8192 rows, 4096 to
+// 11008, rank 32: 458 MB fetched and 134.6 us, 399 MB and 120.4 so; either of
+// the two alone 130 and 136 us).
 template <int TERMS, bool BB, bool YB, int DK>
 struct Expand {
-  static constexpr int JT = 4;                 // 8: 138 us for 135 of a prompt's call
-  static constexpr int QN = DK == 8 ? 2 : 4;  // 16-row tiles at a time
+  static constexpr int JT = 4;  // 8: 138 us for 135 of a prompt's call
+  static constexpr int QN = 4;  // 16-row tiles at a time
   static constexpr int kRows = QN * 16;
   static constexpr int kDepth = DK * 32;
   static constexpr int kPitch = kDepth + 8;
@@ -439,8 +438,9 @@ struct Expand {
 // loads of one workgroup wait for, another's fill (8192 x 4096 to 4096, rank
 // 128: 61 us with 2 waves, 49 with 3, a few registers of it spilled; all of a
 // tile's base loaded ahead instead, 2 waves at rank 64: 44 us for 34).
-template <int TERMS, bool BB, bool YB, int DK>
-__global__ void __launch_bounds__(kThreads, DK == 2 ? 4 : DK == 4 && TERMS == 2 ? 3 : 1)
+template <int TERMS, bool BB, bool YB, int DK, int H>
+__global__ void __launch_bounds__(kThreads,
+                                  H > 1 ? 2 : DK == 2 ? 4 : DK == 4 && TERMS == 2 ? 3 : 1)
     expand_kernel(LoraParams P, int splits, int stride) {
   using E = Expand<TERMS, BB, YB, DK>;
   constexpr int JT = E::JT;
@@ -465,89 +465,126 @@ __global__ void __launch_bounds__(kThreads, DK == 2 ? 4 : DK == 4 && TERMS == 2 
     const Tile t = tile_at(tiles, tile, nr);
     const bool none = t.id == kNoAdapter;
     if (none && P.base == P.y) break;  // in place: those rows stay as they are
+    // B's operands of depth run h
     uint4 fb[JT][DK];
-    if (!none) {
+    const auto load_b = [&](int h) {
       const __amdgpu_buffer_rsrc_t rb = buffer_range(
           P.b + (int64_t)t.id * P.n_out * P.rank, (int64_t)P.n_out * P.rank * 2);
 #pragma unroll
       for (int j = 0; j < JT; ++j)
 #pragma unroll
         for (int d = 0; d < DK; ++d) {
-          const int r = d * 32 + 8 * g;
+          const int r = h * E::kDepth + d * 32 + 8 * g;
           fb[j][d] = buf_ld16(rb, r < P.rank && col + j < P.n_out
                                       ? ((uint32_t)(col + j) * (uint32_t)P.rank + r) * 2u
                                       : kOutOfRange);
         }
+    };
+    if (!none) load_b(0);
+    const int len = t.len;  // kRows at most
+    // offsets of the lane's rows 16 q + 4 g + i, and their base one tile ahead
+    const auto rows_of = [&](int q, uint32_t (&ro)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = 16 * q + 4 * g + i;
+        ro[i] = at < len ? (uint32_t)tiles.row(t.start + at) * (uint32_t)P.n_out : kOutOfRange;
+      }
+    };
+    uint32_t ro[2][4];
+    typename E::Base base[2];
+    rows_of(0, ro[0]);
+    if (P.base) E::load_base(rbase, ro[0], col, P.n_out, base[0]);
+    // the terms of s t in depth run h, four ranks to a thread at a time
+    const auto stage = [&](int h) {
+      const float s = P.scaling[t.id];
+      __syncthreads();  // the turn before has read them
+      for (int i = threadIdx.x; i < len * (E::kDepth / 4); i += kThreads) {
+        const int r = i / (E::kDepth / 4), c = i % (E::kDepth / 4) * 4;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        if (h * E::kDepth + c < stride) {
+          const float* from =
+              t_all + (row0 + tiles.row(t.start + r)) * stride + h * E::kDepth + c;
+          int k = 0;
+          for (; k + 4 <= splits; k += 4) {
+            f32x4 w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = *reinterpret_cast<const f32x4*>(from + (k + u) * P.rows * stride);
+            // all four on their way before the first is waited for: the
+            // compiler, short of registers, would take them one by one (512
+            // rows of 4 adapters, rank 64: 25.8 us for 20.0)
+            asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v += w[u];
+          }
+          for (; k < splits; ++k)
+            v += *reinterpret_cast<const f32x4*>(from + k * P.rows * stride);
+          v *= s;
+        }
+#pragma unroll
+        for (int q = 0; q < TERMS; ++q) {
+          const uint32_t lo = pack_bf16(v.x, v.y), hi = pack_bf16(v.z, v.w);
+          *reinterpret_cast<uint2*>(terms + (q * E::kRows + r) * E::kPitch + c) =
+              make_uint2(lo, hi);
+          v -= f32x4{bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
+        }
+      }
+      __syncthreads();
+    };
+    const auto multiply = [&](int q, f32x4 (&acc)[JT]) {
+      const int at = q * 16 + n < len ? q * 16 + n : len - 1;
+#pragma unroll
+      for (int d = 0; d < DK; ++d)
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) {
+          const uint4 ft = *reinterpret_cast<const uint4*>(
+              terms + (k * E::kRows + at) * E::kPitch + d * 32 + 8 * g);
+#pragma unroll
+          for (int j = 0; j < JT; ++j) acc[j] = mfma(ft, fb[j][d], acc[j]);
+        }
+    };
+    f32x4 acc[H > 1 ? E::QN : 1][JT];
+    if constexpr (H > 1) {
+#pragma unroll
+      for (int q = 0; q < E::QN; ++q)
+#pragma unroll
+        for (int j = 0; j < JT; ++j) acc[q][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    for (int part = 0; part < t.len; part += E::kRows) {
-      const int len = t.len - part < E::kRows ? t.len - part : E::kRows;
-      const int first = t.start + part;
-      // offsets of the lane's rows 16 q + 4 g + i, and their base one tile ahead
-      const auto rows_of = [&](int q, uint32_t (&ro)[4]) {
+    if (!none) {
+      stage(0);
+      if constexpr (H > 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = 16 * q + 4 * g + i;
-          ro[i] = at < len ? (uint32_t)tiles.row(first + at) * (uint32_t)P.n_out : kOutOfRange;
-        }
-      };
-      uint32_t ro[2][4];
-      typename E::Base base[2];
-      rows_of(0, ro[0]);
-      if (P.base) E::load_base(rbase, ro[0], col, P.n_out, base[0]);
-      if (!none) {
-        // the terms of s t, four ranks to a thread at a time
-        const float s = P.scaling[t.id];
-        __syncthreads();  // the turn before has read them
-        for (int i = threadIdx.x; i < len * (E::kDepth / 4); i += kThreads) {
-          const int r = i / (E::kDepth / 4), c = i % (E::kDepth / 4) * 4;
-          f32x4 v = {0.f, 0.f, 0.f, 0.f};
-          if (c < stride) {
-            const float* from = t_all + (row0 + tiles.row(first + r)) * stride + c;
-#pragma unroll 4
-            for (int k = 0; k < splits; ++k)
-              v += *reinterpret_cast<const f32x4*>(from + k * P.rows * stride);
-            v *= s;
+        for (int h = 0; h < H; ++h) {
+          if (h > 0) {
+            load_b(h);
+            stage(h);
           }
 #pragma unroll
-          for (int q = 0; q < TERMS; ++q) {
-            const uint32_t lo = pack_bf16(v.x, v.y), hi = pack_bf16(v.z, v.w);
-            *reinterpret_cast<uint2*>(terms + (q * E::kRows + r) * E::kPitch + c) =
-                make_uint2(lo, hi);
-            v -= f32x4{bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
-          }
+          for (int q = 0; q < E::QN; ++q)
+            if (q * 16 < len) multiply(q, acc[q]);
         }
-        __syncthreads();
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < E::QN; ++q) {
+      if (q * 16 >= len) break;
+      if (q + 1 < E::QN) {
+        rows_of(q + 1, ro[(q + 1) & 1]);
+        if (P.base) E::load_base(rbase, ro[(q + 1) & 1], col, P.n_out, base[(q + 1) & 1]);
+      }
+      f32x4(&sum)[JT] = acc[H > 1 ? q : 0];
+      if constexpr (H == 1) {
+#pragma unroll
+        for (int j = 0; j < JT; ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (!none) multiply(q, sum);
       }
 #pragma unroll
-      for (int q = 0; q < E::QN; ++q) {
-        if (q * 16 >= len) break;
-        if (q + 1 < E::QN) {
-          rows_of(q + 1, ro[(q + 1) & 1]);
-          if (P.base) E::load_base(rbase, ro[(q + 1) & 1], col, P.n_out, base[(q + 1) & 1]);
-        }
-        f32x4 acc[JT];
+      for (int i = 0; i < 4; ++i) {
+        float v[JT];
 #pragma unroll
-        for (int j = 0; j < JT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (!none) {
-          const int at = q * 16 + n < len ? q * 16 + n : len - 1;
-#pragma unroll
-          for (int d = 0; d < DK; ++d)
-#pragma unroll
-            for (int k = 0; k < TERMS; ++k) {
-              const uint4 ft = *reinterpret_cast<const uint4*>(
-                  terms + (k * E::kRows + at) * E::kPitch + d * 32 + 8 * g);
-#pragma unroll
-              for (int j = 0; j < JT; ++j) acc[j] = mfma(ft, fb[j][d], acc[j]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v[JT];
-#pragma unroll
-          for (int j = 0; j < JT; ++j)
-            v[j] = P.base ? acc[j][i] + E::base_at(base[q & 1], i, j) : acc[j][i];
-          E::store(ry, ro[q & 1][i], col, P.n_out, v);
-        }
+        for (int j = 0; j < JT; ++j)
+          v[j] = P.base ? sum[j][i] + E::base_at(base[q & 1], i, j) : sum[j][i];
+        E::store(ry, ro[q & 1][i], col, P.n_out, v);
       }
     }
   }
@@ -604,20 +641,21 @@ void shrink(const LoraParams& p, const Cut& c, hipStream_t s) {
                      dim3(kThreads), 0, s, p, c.splits, c.slice, c.stride);
 }
 
-template <int TERMS, bool BB, bool YB, int DK>
+template <int TERMS, bool BB, bool YB, int DK, int H>
 void expand(const LoraParams& p, const Cut& c, hipStream_t s) {
   using E = Expand<TERMS, BB, YB, DK>;
-  hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB, DK>),
+  static_assert(E::kRows == kTileRows, "a tile's rows are taken at once");
+  hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB, DK, H>),
                      dim3((p.n_out + E::kCols - 1) / E::kCols, (unsigned)c.blocks,
                           tile_lanes(p.rows, c.blocks, p.n_adapters)),
                      dim3(kThreads), 0, s, p, c.splits, c.stride);
 }
 template <int TERMS, bool BB, bool YB>
 void expand_by_rank(const LoraParams& p, const Cut& c, hipStream_t s) {
-  if (c.stride <= 32) expand<TERMS, BB, YB, 1>(p, c, s);
-  else if (c.stride <= 64) expand<TERMS, BB, YB, 2>(p, c, s);
-  else if (c.stride <= 128) expand<TERMS, BB, YB, 4>(p, c, s);
-  else expand<TERMS, BB, YB, 8>(p, c, s);
+  if (c.stride <= 32) expand<TERMS, BB, YB, 1, 1>(p, c, s);
+  else if (c.stride <= 64) expand<TERMS, BB, YB, 2, 1>(p, c, s);
+  else if (c.stride <= 128) expand<TERMS, BB, YB, 4, 1>(p, c, s);
+  else expand<TERMS, BB, YB, 4, 2>(p, c, s);
 }
 
 }  // namespace
