@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads,
       for (int i = threadIdx.x; i < len * (E::kDepth / 4); i += kThreads) {
         const int r = i / (E::kDepth / 4), c = i % (E::kDepth / 4) * 4;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (h * E::kDepth + c < stride) {
+        if (h * E::kDepth + c < P.rank) {  // t's other columns may be infinity times 0
           const float* from =
               t_all + (row0 + tiles.row(t.start + r)) * stride + h * E::kDepth + c;
           int k = 0;
@@ -526,7 +526,10 @@ __global__ void __launch_bounds__(kThreads,
           const uint32_t lo = pack_bf16(v.x, v.y), hi = pack_bf16(v.z, v.w);
           *reinterpret_cast<uint2*>(terms + (q * E::kRows + r) * E::kPitch + c) =
               make_uint2(lo, hi);
-          v -= f32x4{bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
+          // what is left of v; nothing of an infinity, where it would be NaN
+          const f32x4 term = {bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = isinf(term[e]) ? 0.f : v[e] - term[e];
         }
       }
       __syncthreads();

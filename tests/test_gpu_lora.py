@@ -199,3 +199,28 @@ def test_same_bits_every_time():
     y = c.run()
     for _ in range(3):
         assert torch.equal(c.run(), y)
+
+
+@pytest.mark.parametrize("rank", [8, 24, 64, 136, 256])
+@pytest.mark.parametrize("y", [F32, BF16])
+def test_rows_with_an_infinity(rank, y):
+    # t is an infinity in every rank; a column of B of one sign passes it on,
+    # one of both signs gives NaN; the other rows stay as they are
+    c = Case(70, 264, 136, rank, 3, ids="mixed", y=y)
+    c.a = c.a.abs() + 0.01
+    c.b = c.b.abs() + 0.01
+    c.b[:, 1::3] *= -1
+    c.b[:, 2::3, 0] *= -1
+    want = c.run()
+    c.check(want)
+    c.ids[5], c.ids[66] = 1, 2
+    keep = torch.ones(70, dtype=torch.bool)
+    for r, v in ((5, float("inf")), (66, -float("inf"))):
+        c.x[r, 77] = v
+        keep[r] = False
+    got = c.run().cpu()
+    assert torch.equal(got[keep], want.cpu()[keep])
+    for r, sign in ((5, 1.0), (66, -1.0)):
+        assert (got[r, 0::3] == sign * float("inf")).all()
+        assert (got[r, 1::3] == -sign * float("inf")).all()
+        assert torch.isnan(got[r, 2::3]).all()
