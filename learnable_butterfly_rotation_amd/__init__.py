@@ -512,7 +512,8 @@ def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> 
     float32 or bfloat16 of any shape), norm[1] = min(1, max_norm / norm[0]),
     and every gradient times norm[1], in place or into `outs`.  norm: [2]
     float32; workspace: a uint8 tensor of bfly_grad_clip_workspace_bytes.  No
-    two of the tensors that are written may overlap."""
+    two of the tensors that are written may overlap, nor an output a gradient
+    other than its own."""
     ext = _ext()
     dev = norm.get_device()
     ws, ws_bytes = _scratch(workspace, dev)
@@ -522,5 +523,7 @@ def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> 
         to, *like = ext.describe(outs, dev, True)
         if like != [numels, types]:
             raise ValueError("the outputs have to be like their gradients")
+        if not ext.apart(at, to, numels, types):
+            raise ValueError("an output overlaps a gradient that is not its own")
     _call("bfly_grad_clip", dev, stream, len(types) // 4, at, to, numels, types, max_norm,
           ext.at("norm", norm, (2,), _F32, dev), ws, ws_bytes)

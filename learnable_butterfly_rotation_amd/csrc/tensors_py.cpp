@@ -3,6 +3,7 @@
 // contiguity of 96 gradients and their outputs through Python costs 50 us, four
 // times what the GPU needs to clip them, and of the eight tensors of a norm 4 us,
 // as long as its kernel takes for a token.
+#define PY_SSIZE_T_CLEAN  // lengths of bytes as Py_ssize_t
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -92,6 +93,43 @@ PyObject* describe(PyObject*, PyObject* args) {
   return result;
 }
 
+// apart(inputs, outputs, element counts, types), as describe gives them for two
+// lists of like tensors whose outputs do not overlap: whether an output shares
+// bytes with an input other than, exactly, its own.
+PyObject* apart(PyObject*, PyObject* args) {
+  const char *in, *out, *count, *kind;
+  Py_ssize_t in_len, out_len, count_len, kind_len;
+  if (!PyArg_ParseTuple(args, "y#y#y#y#", &in, &in_len, &out, &out_len, &count, &count_len, &kind,
+                        &kind_len))
+    return nullptr;
+  const Py_ssize_t n = kind_len / 4;
+  if (kind_len % 4 || in_len != n * 8 || out_len != n * 8 || count_len != n * 8)
+    return PyErr_Format(PyExc_ValueError, "apart() takes four lists of one length");
+  const auto* const from = reinterpret_cast<const uint64_t*>(in);
+  const auto* const to = reinterpret_cast<const uint64_t*>(out);
+  const auto* const numel = reinterpret_cast<const int64_t*>(count);
+  const auto* const type = reinterpret_cast<const int32_t*>(kind);
+  const auto bytes = [&](Py_ssize_t i) { return (uint64_t)numel[i] * (type[i] ? 2 : 4); };
+  try {
+    std::vector<std::pair<uint64_t, Py_ssize_t>> outs;  // address, index
+    outs.reserve(n);
+    for (Py_ssize_t i = 0; i < n; ++i)
+      if (numel[i]) outs.emplace_back(to[i], i);
+    if (!std::is_sorted(outs.begin(), outs.end())) std::sort(outs.begin(), outs.end());
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      if (!numel[i]) continue;
+      // the first output that ends behind the input's start, and those after it
+      auto o = std::upper_bound(outs.begin(), outs.end(), std::make_pair(from[i], n));
+      if (o != outs.begin() && (o - 1)->first + bytes((o - 1)->second) > from[i]) --o;
+      for (; o != outs.end() && o->first < from[i] + bytes(i); ++o)
+        if (o->second != i || o->first != from[i]) Py_RETURN_FALSE;
+    }
+  } catch (const std::exception& e) {
+    return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+  }
+  Py_RETURN_TRUE;
+}
+
 // The types that `at` is told to take, as bits.
 int kind_of(at::ScalarType s) {
   switch (s) {
@@ -142,6 +180,7 @@ PyMethodDef methods[] = {
     {"at", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(address)), METH_FASTCALL,
      "the address of a tensor that is as it has to be"},
     {"describe", describe, METH_VARARGS, "addresses, element counts and types of tensors"},
+    {"apart", apart, METH_VARARGS, "whether outputs overlap no input but their own"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -160,3 +160,17 @@ def test_clip_tensors_that_overlap():
     assert abs(float(norm[0]) - 2000 ** 0.5) <= TOL * 2000 ** 0.5
     B.bfly_grad_clip([flat[500:], flat[:0], flat[:500]], 1.0, norm, workspace(3))
     assert abs(float(norm[0]) - 1000 ** 0.5) <= TOL * 1000 ** 0.5
+
+
+def test_clip_outputs_that_overlap_other_gradients():
+    a, b, norm = torch.ones(300, device="cuda"), torch.ones(300, device="cuda"), \
+        torch.empty(2, device="cuda")
+    for grads, outs in (([a, b], [b, a]), ([a, b], [torch.empty_like(a), a]),
+                        ([a[:200]], [a[1:201]]), ([a, a], [a, b])):
+        with pytest.raises(ValueError):
+            B.bfly_grad_clip(grads, 1.0, norm, workspace(len(grads)), outs=outs)
+    assert (a == 1).all() and (b == 1).all()
+    out = torch.empty_like(b)
+    B.bfly_grad_clip([a, b], 1.0, norm, workspace(2), outs=[a, out])
+    assert torch.equal(a, out) and (b == 1).all()
+    assert abs(float(a[7]) - 600 ** -0.5) <= 4 * TOL

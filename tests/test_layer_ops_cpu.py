@@ -172,6 +172,38 @@ def test_the_list_of_gradients_is_checked():
         ext.describe([])
 
 
+def test_outputs_and_other_gradients_are_told_apart():
+    ext = extension()
+
+    def apart(ins, outs, numels, types=None):
+        n = len(ins)
+        pack = lambda t, v: bytes((t * n)(*v))
+        return ext.apart(pack(ctypes.c_uint64, ins), pack(ctypes.c_uint64, outs),
+                         pack(ctypes.c_int64, numels), pack(ctypes.c_int32, types or [0] * n))
+
+    assert apart([], [], []) is True
+    assert apart([64], [64], [4]) is True                         # in place
+    assert apart([64], [68], [4]) is False                        # moved by an element
+    assert apart([64], [60], [4]) is False
+    assert apart([64], [80], [4]) is True and apart([64], [48], [4]) is True
+    assert apart([64], [72], [4], [1]) is True                    # bf16: 8 bytes
+    assert apart([64, 128], [128, 64], [4, 4]) is False           # swapped
+    assert apart([64, 128], [256, 64], [4, 4]) is False
+    assert apart([64, 128], [256, 64], [0, 4]) is True            # the first is empty
+    assert apart([64, 64], [64, 256], [4, 4]) is False            # read again after it is written
+    assert apart([64, 64], [128, 256], [4, 4]) is True
+    assert apart([64, 64], [100, 72], [16, 1]) is False           # an output inside an input
+    assert apart([72, 300], [500, 64], [1, 16]) is False          # an input inside an output
+    n = 50
+    ins = [4096 + 64 * (i * 7 % n) for i in range(n)]
+    assert apart(ins, ins, [16] * n) is True
+    assert apart(ins, [1 << 20 | 64 * i for i in range(n)], [16] * n) is True
+    assert apart(ins, [a + 4 for a in ins], [15] * n) is False
+    for bad in ((b"", b"", b"", b"1"), (b"", b"", b"", b"1234"), (b"",), (b"", b"", b"", 3)):
+        with pytest.raises((TypeError, ValueError)):
+            ext.apart(*bad)
+
+
 def test_a_tensor_is_checked():
     ext, x = extension(), torch.zeros((3, 4))
     assert ext.at("x", None, (3, 4), 1, 0) is None
