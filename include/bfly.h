@@ -497,7 +497,8 @@ bfly_status bfly_rmsnorm(const void* x, bfly_dtype x_dt, const void* residual, v
  *            where h_dt is g_dt
  *   dweight: may be NULL (the workspace is then not used and may be NULL)
  *   workspace: >= bfly_rmsnorm_backward_workspace_bytes(rows, n) bytes of
- *            device scratch, 16-byte aligned
+ *            device scratch, 16-byte aligned; two calls that may overlap need
+ *            one each
  * dweight's sum has a fixed order that depends on (rows, n) only: the same
  * bits from run to run.  Sizes, alignment and errors as bfly_rmsnorm, plus
  * BFLY_ERR_WORKSPACE. */

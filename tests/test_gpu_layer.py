@@ -334,3 +334,86 @@ def test_what_the_binding_refuses():
     assert e.value.status == 6
     with pytest.raises(B.BflyError):
         B.bfly_grad_clip([x], float("nan"), n2, cws)
+
+
+def test_norm_past_32_bit_offsets():
+    # 4.4 GB of rows: a row's results are those of a call with few rows
+    rows, n = 540000, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty((rows, n), dtype=BF16, device="cuda").normal_(generator=g)
+    w = 1 + 0.1 * torch.randn(n, device="cuda", generator=g)
+    y, rstd = torch.empty_like(x), torch.empty(rows, device="cuda")
+    codes = torch.empty((rows, n), dtype=torch.int8, device="cuda")
+    scales = torch.empty((rows, n // 128), dtype=F16, device="cuda")
+    B.bfly_rmsnorm(x, w, EPS, y=y, codes=codes, scales=scales, rstd=rstd, group=128)
+    few = [slice(0, 200), slice(524200, 524400), slice(rows - 200, rows)]
+    small = []
+    for at in few:
+        part = x[at].clone()
+        out = [torch.empty_like(t[at]) for t in (y, codes, scales, rstd)]
+        B.bfly_rmsnorm(part, w, EPS, y=out[0], codes=out[1], scales=out[2], rstd=out[3], group=128)
+        small.append((part, out[3]))
+        for a, b in zip(out, (y, codes, scales, rstd)):
+            assert torch.equal(a, b[at])
+    # the gradient, in place of dy, which is zero but in those rows
+    dy = y.zero_()
+    ws = scratch(B.bfly_rmsnorm_backward_workspace_bytes(rows, n))
+    ws2 = scratch(B.bfly_rmsnorm_backward_workspace_bytes(200, n))
+    dw, want, total, size = (torch.zeros(n, device="cuda") for _ in range(4))
+    for at, (part, r) in zip(few, small):
+        d = torch.empty((200, n), dtype=BF16, device="cuda").normal_(generator=g)
+        dy[at] = d
+        total += (d.double() * part.double() * r.double()[:, None]).sum(0).float()
+        size += (d.double() * part.double() * r.double()[:, None]).abs().sum(0).float()
+        small[few.index(at)] = (part, r, d)
+    B.bfly_rmsnorm_backward(x, w, rstd, dy, dy, dweight=dw, workspace=ws)
+    for at, (part, r, d) in zip(few, small):
+        B.bfly_rmsnorm_backward(part, w, r, d, d, dweight=want, workspace=ws2)
+        assert torch.equal(dy[at], d)
+    # 600 products (two roundings each) among zeros, and both references' roundings
+    assert ((dw - total).abs() <= 1.01 * (600 + 8) * U * size).all()
+    assert not dy[200:524200].any()
+
+
+def test_adapters_past_32_bit_offsets():
+    # 4.4 GB of x and of y: a block of rows, again and again
+    blocks, k, out, num, rank = 1056, 8192, 8192, 5, 16
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g)
+    x, base = rand(256, k).to(BF16), rand(256, out).to(BF16)
+    ids = torch.randint(-1, num, (256,), device="cuda", generator=g, dtype=torch.int32)
+    a, b, s = (rand(num, rank, k) / k ** 0.5).to(BF16), rand(num, out, rank).to(BF16), \
+        0.5 + torch.rand(num, device="cuda", generator=g)
+    rows = 256 * blocks
+    y = base.repeat(blocks, 1)
+    ws = scratch(B.bfly_lora_matmul_workspace_bytes(rows, out, k, rank))
+    B.bfly_lora_matmul(x.repeat(blocks, 1), ids.repeat(blocks), a, b, s, y, ws, base=y)
+    first = y[:256]
+    assert (y.view(blocks, 256, out) == first).all()
+    for i in range(num):
+        at = ids == i
+        t = x[at].double() @ a[i].double().T * s[i].double()
+        tabs = x[at].double().abs() @ a[i].double().abs().T * s[i].double()
+        add, b64 = t @ b[i].double().T, b[i].double().abs().T
+        # t's sum over k and its 16 bits, the second sum, the base's addition, y
+        err = (1.01 * (k + 64) * U * tabs + (2 * U + 2.0 ** -16) * t.abs()) @ b64 \
+            + 1.01 * 2 * rank * U * (t.abs() @ b64)
+        want = base[at].double() + add
+        tol = err + U * (want.abs() + err) + 2.0 ** -8 * (want.abs() + 2 * err)
+        assert ((first[at].double() - want).abs() <= tol).all()
+    assert torch.equal(first[ids < 0], base[ids < 0])
+
+
+def test_clipping_past_32_bit_offsets():
+    n = 2 ** 32 + 37
+    g = torch.full((n,), 2.0 ** -8, dtype=BF16, device="cuda")
+    g[-1] = 96.0
+    norm = torch.empty(2, device="cuda")
+    ws = scratch(B.bfly_grad_clip_workspace_bytes(1))
+    B.bfly_grad_clip([g], 1.0, norm, ws)
+    exact = ((n - 1) * 2.0 ** -16 + 96.0 ** 2) ** 0.5
+    # an fp64 sum, rounded once; the factor likewise
+    assert abs(float(norm[0]) - exact) <= 1.01 * U * exact
+    assert abs(float(norm[1]) - 1 / exact) <= 1.01 * U / exact
+    assert (g[:-1] == (norm[1] * 2.0 ** -8).to(BF16)).all()
+    assert g[-1] == (norm[1] * 96.0).to(BF16)
