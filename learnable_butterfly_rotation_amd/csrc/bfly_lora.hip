@@ -194,7 +194,7 @@ constexpr int kRun = 64;
 constexpr int kRunPitch = 2 * kRun + 16;
 
 // t[split][row][j] = sum over the split's k of A_id[j][k] x[row][k].
-// Grid: (blocks of rows, tile lanes, splits * rank blocks).  RT tiles of 16
+// Grid: (blocks' tile lanes, splits * rank blocks).  RT tiles of 16
 // ranks; the four waves take every fourth run of 64 k, each by itself, and
 // add their sums through LDS at the end.
 //
@@ -331,18 +331,37 @@ __device__ __forceinline__ void shrink_rows(const ShrinkArgs<RT>& P, int start, 
   __syncthreads();  // the next turn writes over the sums
 }
 
+// The tile lanes of the blocks of rows (workgroups that share a block's tiles),
+// numbered block by block within a lane.  The last block, with fewer rows, has
+// `last` of `lanes`: workgroups without a tile would take the places of others
+// (257 rows of 32 adapters, k = 11008, rank 64: 27.7 us in all for 25.5).
+struct TileLanes {
+  int blocks, lanes, last;
+  __host__ __device__ int64_t count() const { return (int64_t)(blocks - 1) * lanes + last; }
+  __device__ __forceinline__ int of(int block) const { return block + 1 < blocks ? lanes : last; }
+  __device__ __forceinline__ void place(int i, int& block, int& lane) const {
+    block = 0, lane = i;
+    if (blocks == 1) return;
+    const bool all = i < blocks * last;  // lanes that every block has
+    const int j = all ? i : i - blocks * last, n = all ? blocks : blocks - 1;
+    block = j % n;
+    lane = j / n + (all ? 0 : last);
+  }
+};
+
 template <int RT>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int splits, int slice,
-                                                          int stride) {
+__global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, TileLanes L, int splits,
+                                                          int slice, int stride) {
   using S = ShrinkArgs<RT>;
   __shared__ Tiles tiles;
   __shared__ __align__(16) uint8_t lds[4 * S::kWaveBytes];
-  const int64_t row0 = (int64_t)blockIdx.x * kBlockRows;
+  int block, first;
+  L.place(blockIdx.x, block, first);
+  const int64_t row0 = (int64_t)block * kBlockRows;
   const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
-  if ((int)blockIdx.y >= nr) return;  // no more tiles than rows: a last block's may be few
-  const int split = blockIdx.z % splits, rank0 = blockIdx.z / splits * (RT * 16);
+  const int split = blockIdx.y % splits, rank0 = blockIdx.y / splits * (RT * 16);
   make_tiles(tiles, P.ids + row0, nr, P.n_adapters);
-  if (blockIdx.y == 0 && blockIdx.z == 0) put_order(order_at(P) + blockIdx.x, tiles);
+  if (first == 0 && blockIdx.y == 0) put_order(order_at(P) + block, tiles);
   S a;
   a.rx = buffer_range(P.x + row0 * P.k, (int64_t)nr * P.k * 2);
   a.tiles = &tiles;
@@ -353,7 +372,8 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, int spli
   a.kend = P.k - a.kbeg < slice ? P.k : a.kbeg + slice;
   a.stride = stride;
   const int count = tiles.count;
-  for (int tile = blockIdx.y; tile < count; tile += gridDim.y) {
+  const int lanes = L.of(block);
+  for (int tile = first; tile < count; tile += lanes) {
     const Tile t = tile_at(tiles, tile, nr);
     if (t.id == kNoAdapter) break;  // the rows without an adapter come last
     a.ra = buffer_range(P.a + ((int64_t)t.id * P.rank + rank0) * P.k,
@@ -606,11 +626,17 @@ struct Cut {
 // more for every change of adapter within 256 rows): the others would start
 // only to find nothing (257 rows of 32 adapters: 36.3 us with 16, 31.0 with 33;
 // 8192 rows of 6 adapters: 137 us with 8 and no less with more).
-int tile_lanes(int64_t rows, int64_t blocks, int n_adapters) {
-  const int64_t r = rows < kBlockRows ? rows : kBlockRows;
-  const int64_t most = (r < n_adapters ? r : n_adapters) + r / kTileRows + 1;
-  const int64_t cap = blocks <= 2 ? 64 : blocks <= 8 ? 16 : 8;
-  return (int)(most < cap ? most : cap);
+TileLanes tile_lanes(int64_t rows, int64_t blocks, int n_adapters) {
+  const int cap = blocks <= 2 ? 64 : blocks <= 8 ? 16 : 8;
+  const auto lanes = [&](int r) {
+    const int most = (r < n_adapters ? r : n_adapters) + r / kTileRows + 1;
+    return most < r ? (most < cap ? most : cap) : (r < cap ? r : cap);
+  };
+  TileLanes t;
+  t.blocks = (int)blocks;
+  t.last = lanes((int)(rows - (blocks - 1) * kBlockRows));
+  t.lanes = blocks > 1 ? lanes(kBlockRows) : t.last;
+  return t;
 }
 Cut cut(int64_t rows, int k, int n_adapters, int rank) {
   Cut c;
@@ -638,10 +664,9 @@ Cut cut(int64_t rows, int k, int n_adapters, int rank) {
 
 template <int RT>
 void shrink(const LoraParams& p, const Cut& c, hipStream_t s) {
-  hipLaunchKernelGGL((shrink_kernel<RT>),
-                     dim3((unsigned)c.blocks, tile_lanes(p.rows, c.blocks, p.n_adapters),
-                          c.splits * c.ranks),
-                     dim3(kThreads), 0, s, p, c.splits, c.slice, c.stride);
+  const TileLanes lanes = tile_lanes(p.rows, c.blocks, p.n_adapters);
+  hipLaunchKernelGGL((shrink_kernel<RT>), dim3((unsigned)lanes.count(), c.splits * c.ranks),
+                     dim3(kThreads), 0, s, p, lanes, c.splits, c.slice, c.stride);
 }
 
 template <int TERMS, bool BB, bool YB, int DK, int H>
@@ -650,7 +675,7 @@ void expand(const LoraParams& p, const Cut& c, hipStream_t s) {
   static_assert(E::kRows == kTileRows, "a tile's rows are taken at once");
   hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB, DK, H>),
                      dim3((p.n_out + E::kCols - 1) / E::kCols, (unsigned)c.blocks,
-                          tile_lanes(p.rows, c.blocks, p.n_adapters)),
+                          tile_lanes(p.rows, c.blocks, p.n_adapters).lanes),
                      dim3(kThreads), 0, s, p, c.splits, c.stride);
 }
 template <int TERMS, bool BB, bool YB>
