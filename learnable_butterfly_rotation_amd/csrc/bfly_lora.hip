@@ -334,10 +334,10 @@ __device__ __forceinline__ void shrink_rows(const ShrinkArgs<RT>& P, int start, 
 // The tile lanes of the blocks of rows (workgroups that share a block's tiles),
 // numbered block by block within a lane.  The last block, with fewer rows, has
 // `last` of `lanes`: workgroups without a tile would take the places of others
-// (257 rows of 32 adapters, k = 11008, rank 64: 27.7 us in all for 25.5).
+// (257 rows of 32 adapters, k = 11008, rank 64: 27.7 us in all for 23.6).
 struct TileLanes {
   int blocks, lanes, last;
-  __host__ __device__ int64_t count() const { return (int64_t)(blocks - 1) * lanes + last; }
+  __host__ __device__ int count() const { return (blocks - 1) * lanes + last; }
   __device__ __forceinline__ int of(int block) const { return block + 1 < blocks ? lanes : last; }
   __device__ __forceinline__ void place(int i, int& block, int& lane) const {
     block = 0, lane = i;
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, TileLane
   }
 }
 
-// y = base + B_id (s_id t).  Grid: (column tiles, blocks of rows, tile lanes).
+// y = base + B_id (s_id t).  Grid: (column tiles, blocks' tile lanes in two axes).
 // The matrix cores' columns are columns of y: tile j of JT takes columns
 // JT n + j as its columns n, so that a lane is left with JT consecutive
 // columns of a row and 16 lanes with a run of 16 JT (memory in whole lines).
@@ -461,18 +461,21 @@ struct Expand {
 template <int TERMS, bool BB, bool YB, int DK, int H>
 __global__ void __launch_bounds__(kThreads,
                                   H > 1 ? 2 : DK == 2 ? 4 : DK == 4 && TERMS == 2 ? 3 : 1)
-    expand_kernel(LoraParams P, int splits, int stride) {
+    expand_kernel(LoraParams P, TileLanes L, int splits, int stride) {
   using E = Expand<TERMS, BB, YB, DK>;
   constexpr int JT = E::JT;
   __shared__ Tiles tiles;
   __shared__ __align__(16) uint16_t terms[TERMS * E::kRows * E::kPitch];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int64_t row0 = (int64_t)blockIdx.y * kBlockRows;
+  const int at = blockIdx.y + blockIdx.z * gridDim.y;
+  if (at >= L.count()) return;
+  int block, first;
+  L.place(at, block, first);
+  const int64_t row0 = (int64_t)block * kBlockRows;
   const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
-  if ((int)blockIdx.z >= nr) return;
   const int col = blockIdx.x * E::kCols + wave * 16 * JT + JT * n;  // the lane's first column
-  get_order(tiles, order_at(P) + blockIdx.y);
+  get_order(tiles, order_at(P) + block);
   constexpr int bs = BB ? 2 : 4, ys = YB ? 2 : 4;
   const __amdgpu_buffer_rsrc_t rbase =
       buffer_range(static_cast<const char*>(P.base) + row0 * P.n_out * bs,
@@ -480,8 +483,8 @@ __global__ void __launch_bounds__(kThreads,
   const __amdgpu_buffer_rsrc_t ry =
       buffer_range(static_cast<char*>(P.y) + row0 * P.n_out * ys, (int64_t)nr * P.n_out * ys);
   const float* const t_all = t_at(P);
-  const int count = tiles.count;
-  for (int tile = blockIdx.z; tile < count; tile += gridDim.z) {
+  const int count = tiles.count, lanes = L.of(block);
+  for (int tile = first; tile < count; tile += lanes) {
     const Tile t = tile_at(tiles, tile, nr);
     const bool none = t.id == kNoAdapter;
     if (none && P.base == P.y) break;  // in place: those rows stay as they are
@@ -669,14 +672,16 @@ void shrink(const LoraParams& p, const Cut& c, hipStream_t s) {
                      dim3(kThreads), 0, s, p, lanes, c.splits, c.slice, c.stride);
 }
 
+constexpr int kMaxGridY = 32768;
 template <int TERMS, bool BB, bool YB, int DK, int H>
 void expand(const LoraParams& p, const Cut& c, hipStream_t s) {
   using E = Expand<TERMS, BB, YB, DK>;
   static_assert(E::kRows == kTileRows, "a tile's rows are taken at once");
+  const TileLanes lanes = tile_lanes(p.rows, c.blocks, p.n_adapters);
+  const int y = lanes.count() < kMaxGridY ? lanes.count() : kMaxGridY;
   hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB, DK, H>),
-                     dim3((p.n_out + E::kCols - 1) / E::kCols, (unsigned)c.blocks,
-                          tile_lanes(p.rows, c.blocks, p.n_adapters).lanes),
-                     dim3(kThreads), 0, s, p, c.splits, c.stride);
+                     dim3((p.n_out + E::kCols - 1) / E::kCols, y, (lanes.count() + y - 1) / y),
+                     dim3(kThreads), 0, s, p, lanes, c.splits, c.stride);
 }
 template <int TERMS, bool BB, bool YB>
 void expand_by_rank(const LoraParams& p, const Cut& c, hipStream_t s) {

@@ -189,6 +189,12 @@ def test_unused_adapters_and_missing_ranks_are_not_read():
     c.check(y)
 
 
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+def test_many_blocks_of_rows(ids):
+    c = Case(4300 * 256 + 77, 16, 8, 8, 9, ids=ids, y=F32)
+    c.check(c.run())
+
+
 def test_no_rows():
     c = Case(0, 128, 64, 8, 2)
     c.run()
