@@ -649,9 +649,9 @@ Cut cut(int64_t rows, int k, int n_adapters, int rank) {
   c.blocks = (rows + kBlockRows - 1) / kBlockRows;
   // The k axis is split until there is a workgroup for every CU, counting the
   // tiles there can be: one to 64 rows, and one more for every adapter of a
-  // block.  More of them cost more to start than they save (257 rows of 32
-  // adapters, k = 11008, rank 64: 31 us with 256 workgroups wanted, 38 with
-  // 384; 2048 rows of 4, k = 4096: 30 us with 192, 27 with 256, 29 with 384).
+  // block.  More of them cost more to start than they save (2048 rows of 4
+  // adapters, k = 4096, rank 64: 30 us with 192 workgroups wanted, 26.1 with
+  // 256, 29.1 with 384; 257 rows of 32, k = 11008: 23.8 with 256, 24.3 with 384).
   // A workgroup takes 512 k at least, which its waves wait for twice.
   const int64_t tail = rows - (c.blocks - 1) * kBlockRows;
   const int64_t tiles = (rows + kTileRows - 1) / kTileRows +
