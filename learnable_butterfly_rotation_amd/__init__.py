@@ -187,7 +187,8 @@ _extension = _torch = _bfloat16 = None
 def _ext():
     """The extension that checks tensors: at(name, tensor, shape, kinds,
     device) gives the address of a contiguous tensor of that shape, of one of
-    these types and on that GPU (None for None), or raises."""
+    these types and on that GPU (None for None), scratch(workspace, device) an
+    address and bytes; or they raise."""
     global _extension, _torch, _bfloat16
     if _extension is None:
         import importlib
@@ -211,15 +212,6 @@ _F32, _BF16, _F16, _BYTES, _I32 = 1, 2, 4, 8 | 16 | 32, 64
 _ROWS = _F32 | _BF16
 
 
-def _scratch(workspace, device):
-    """A workspace's address and bytes (None: NULL, 0)."""
-    if workspace is None:
-        return None, 0
-    if workspace.get_device() != device or not workspace.is_contiguous():
-        raise ValueError("the workspace has to be contiguous and on the first argument's device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
 def _call(name, device, stream, *args):
     """The library's `name` with `args` and a stream: the caller's, or torch's
     current one of the arguments' device, which is made current for the call."""
@@ -230,7 +222,7 @@ def _call(name, device, stream, *args):
         stream = _torch._C._cuda_getCurrentRawStream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if _torch.cuda.current_device() != device:
+    if _torch._C._cuda_getDevice() != device:
         with _torch.cuda.device(device):
             status = f(*args, stream)
     else:
@@ -463,13 +455,14 @@ def bfly_rmsnorm_backward(h, weight, rstd, dy, dx, dweight=None, dh=None, worksp
     gradient.  h: [rows, n]; dy, dh, dx: [rows, n] of one type; rstd: [rows]
     and dweight: [n] float32; workspace: a uint8 tensor of
     bfly_rmsnorm_backward_workspace_bytes (needed with dweight)."""
-    at = _ext().at
+    ext = _ext()
+    at = ext.at
     shape = rows, n = h.shape
     dev = h.get_device()
     pdy = at("dy", dy, shape, _ROWS, dev)
     g_dt = _kind(dy)
     same = _BF16 if g_dt else _F32
-    ws, ws_bytes = _scratch(workspace, dev)
+    ws, ws_bytes = ext.scratch(workspace, dev)
     _call("bfly_rmsnorm_backward", dev, stream, at("h", h, shape, _ROWS, dev), _kind(h),
           at("weight", weight, (n,), _ROWS, dev), 0 if weight is None else _kind(weight),
           at("rstd", rstd, (rows,), _F32, dev), pdy, at("dh", dh, shape, same, dev),
@@ -489,12 +482,13 @@ def bfly_lora_matmul(x, ids, lora_a, lora_b, scaling, y, workspace, base=None,
     bfloat16; scaling: [adapters] float32; base, y: [rows, n_out] float32 or
     bfloat16 (base None: zeros; y may be base); workspace: a uint8 tensor of
     bfly_lora_matmul_workspace_bytes."""
-    at = _ext().at
+    ext = _ext()
+    at = ext.at
     rows, k = x.shape
     num, rank, _ = lora_a.shape
     _, n_out = y.shape
     dev = x.get_device()
-    ws, ws_bytes = _scratch(workspace, dev)
+    ws, ws_bytes = ext.scratch(workspace, dev)
     _call("bfly_lora_matmul", dev, stream, at("x", x, (rows, k), _BF16, dev), BFLY_BF16,
           at("ids", ids, (rows,), _I32, dev), at("lora_a", lora_a, (num, rank, k), _BF16, dev),
           at("lora_b", lora_b, (num, n_out, rank), _BF16, dev),
@@ -516,7 +510,7 @@ def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> 
     other than its own."""
     ext = _ext()
     dev = norm.get_device()
-    ws, ws_bytes = _scratch(workspace, dev)
+    ws, ws_bytes = ext.scratch(workspace, dev)
     at, numels, types = ext.describe(grads, dev, outs is None)
     to = None
     if outs is not None:

@@ -176,7 +176,30 @@ PyObject* address(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
+// scratch(workspace, device) -> its address and bytes; (None, 0) for None.
+PyObject* scratch(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != 2) return PyErr_Format(PyExc_TypeError, "scratch() takes two arguments");
+  const long device = PyLong_AsLong(args[1]);
+  if (PyErr_Occurred()) return nullptr;
+  if (args[0] == Py_None) return Py_BuildValue("Oi", Py_None, 0);
+  if (!THPVariable_Check(args[0]))
+    return PyErr_Format(PyExc_TypeError, "the workspace is not a tensor");
+  try {
+    const at::Tensor& x = THPVariable_Unpack(args[0]);
+    if (!x.is_cuda() || x.get_device() != device || x.layout() != at::kStrided ||
+        !x.is_contiguous())
+      return PyErr_Format(PyExc_ValueError, "the workspace has to be contiguous and on GPU %ld",
+                          device);
+    return Py_BuildValue("KK", (unsigned long long)reinterpret_cast<uintptr_t>(x.data_ptr()),
+                         (unsigned long long)x.nbytes());
+  } catch (const std::exception& e) {
+    return PyErr_Format(PyExc_RuntimeError, "the workspace: %s", e.what());
+  }
+}
+
 PyMethodDef methods[] = {
+    {"scratch", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scratch)),
+     METH_FASTCALL, "a workspace's address and bytes"},
     {"at", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(address)), METH_FASTCALL,
      "the address of a tensor that is as it has to be"},
     {"describe", describe, METH_VARARGS, "addresses, element counts and types of tensors"},

@@ -219,3 +219,13 @@ def test_a_tensor_is_checked():
         for _ in range(3):
             with pytest.raises(error):
                 ext.at(*args)
+
+
+def test_a_workspace_is_checked():
+    ext, x = extension(), torch.zeros((3, 4))
+    assert ext.scratch(None, 0) == (None, 0)
+    for args, error in (((5, 0), TypeError), ((x, 0), ValueError), ((x, -1), ValueError),
+                        ((x.to_sparse(), 0), ValueError), ((x, "0"), TypeError), ((x,), TypeError)):
+        for _ in range(3):
+            with pytest.raises(error):
+                ext.scratch(*args)
