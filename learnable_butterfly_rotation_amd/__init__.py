@@ -181,54 +181,46 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-_extension = _torch = _bfloat16 = None
+_extension = _torch = None
 
 
 def _ext():
-    """The extension that checks tensors: at(name, tensor, shape, kinds,
-    device) gives the address of a contiguous tensor of that shape, of one of
-    these types and on that GPU (None for None), scratch(workspace, device) an
-    address and bytes; or they raise."""
-    global _extension, _torch, _bfloat16
+    """The extension that takes the tensors of the norm, the adapters and the
+    clipping: it checks that they are contiguous, of the right types and
+    shapes and on one GPU, or raises, and gives the library's status."""
+    global _extension, _torch
     if _extension is None:
         import importlib
         import torch  # before the extension, which needs its libraries loaded
-        _torch, _bfloat16 = torch, torch.bfloat16
         try:
-            _extension = importlib.import_module("._tensors", __name__)
+            ext = importlib.import_module("._tensors", __name__)
         except ImportError as e:
             raise RuntimeError("the _tensors extension is not built: run "
                                "`python -m learnable_butterfly_rotation_amd.build`") from e
+        L = lib()
+        ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.bfly_rmsnorm, L.bfly_rmsnorm_backward, L.bfly_lora_matmul, L.bfly_grad_clip)))
+        _torch, _extension = torch, ext
     return _extension
 
 
-def _kind(t):
-    """The bfly_dtype of rows that at() has found to be float32 or bfloat16."""
-    return BFLY_BF16 if t.dtype is _bfloat16 else BFLY_F32
-
-
-# the types of at(), as bits
-_F32, _BF16, _F16, _BYTES, _I32 = 1, 2, 4, 8 | 16 | 32, 64
-_ROWS = _F32 | _BF16
-
-
-def _call(name, device, stream, *args):
-    """The library's `name` with `args` and a stream: the caller's, or torch's
-    current one of the arguments' device, which is made current for the call."""
+def _call(f, like, stream, *args):
+    """The extension's f on a stream: the caller's, or torch's current one of
+    the GPU of the tensor `like`, which is made current for the call."""
+    device = like.get_device()
     if device < 0:
-        raise ValueError("%s: the tensors have to be on a GPU" % name)
-    f = getattr(_lib or lib(), name)
+        raise ValueError("bfly_%s: the tensors have to be on a GPU" % f.__name__)
     if stream is None:
         stream = _torch._C._cuda_getCurrentRawStream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     if _torch._C._cuda_getDevice() != device:
         with _torch.cuda.device(device):
-            status = f(*args, stream)
+            status = f(stream, device, *args)
     else:
-        status = f(*args, stream)
+        status = f(stream, device, *args)
     if status != 0:
-        raise BflyError(status, name)
+        raise BflyError(status, "bfly_" + f.__name__)
 
 
 def _table_ws(n, theta, coeffs, workspace, like):
@@ -429,20 +421,8 @@ def bfly_rmsnorm(x, weight, eps, y=None, codes=None, scales=None, residual=None,
     bfloat16; codes: [rows, n] of one byte an element with scales [rows,
     n/group] float16 (group None: one scale per row); rstd: [rows] float32;
     weight: [n] or None (ones).  Outputs that are None are not computed."""
-    at = _ext().at
-    shape = rows, n = x.shape
-    if group is None or codes is None:
-        group = n
-    dev = x.get_device()
-    px = at("x", x, shape, _ROWS, dev)
-    x_dt = _kind(x)
-    same = _BF16 if x_dt else _F32
-    _call("bfly_rmsnorm", dev, stream, px, x_dt, at("residual", residual, shape, same, dev),
-          at("h", h, shape, same, dev), at("weight", weight, (n,), _ROWS, dev),
-          0 if weight is None else _kind(weight), at("y", y, shape, _ROWS, dev),
-          0 if y is None else _kind(y), at("codes", codes, shape, _BYTES, dev),
-          at("scales", scales, (rows, n // group if group > 0 else 0), _F16, dev),
-          at("rstd", rstd, (rows,), _F32, dev), rows, n, eps, format, group)
+    _call(_ext().rmsnorm, x, stream, eps, format, group, x, weight, y, codes, scales, residual, h,
+          rstd)
 
 
 def bfly_rmsnorm_backward_workspace_bytes(rows: int, n: int) -> int:
@@ -455,19 +435,7 @@ def bfly_rmsnorm_backward(h, weight, rstd, dy, dx, dweight=None, dh=None, worksp
     gradient.  h: [rows, n]; dy, dh, dx: [rows, n] of one type; rstd: [rows]
     and dweight: [n] float32; workspace: a uint8 tensor of
     bfly_rmsnorm_backward_workspace_bytes (needed with dweight)."""
-    ext = _ext()
-    at = ext.at
-    shape = rows, n = h.shape
-    dev = h.get_device()
-    pdy = at("dy", dy, shape, _ROWS, dev)
-    g_dt = _kind(dy)
-    same = _BF16 if g_dt else _F32
-    ws, ws_bytes = ext.scratch(workspace, dev)
-    _call("bfly_rmsnorm_backward", dev, stream, at("h", h, shape, _ROWS, dev), _kind(h),
-          at("weight", weight, (n,), _ROWS, dev), 0 if weight is None else _kind(weight),
-          at("rstd", rstd, (rows,), _F32, dev), pdy, at("dh", dh, shape, same, dev),
-          at("dx", dx, shape, same, dev), g_dt, at("dweight", dweight, (n,), _F32, dev), rows, n,
-          ws, ws_bytes)
+    _call(_ext().rmsnorm_backward, h, stream, h, weight, rstd, dy, dx, dweight, dh, workspace)
 
 
 def bfly_lora_matmul_workspace_bytes(rows: int, n_out: int, k: int, rank: int) -> int:
@@ -482,19 +450,7 @@ def bfly_lora_matmul(x, ids, lora_a, lora_b, scaling, y, workspace, base=None,
     bfloat16; scaling: [adapters] float32; base, y: [rows, n_out] float32 or
     bfloat16 (base None: zeros; y may be base); workspace: a uint8 tensor of
     bfly_lora_matmul_workspace_bytes."""
-    ext = _ext()
-    at = ext.at
-    rows, k = x.shape
-    num, rank, _ = lora_a.shape
-    _, n_out = y.shape
-    dev = x.get_device()
-    ws, ws_bytes = ext.scratch(workspace, dev)
-    _call("bfly_lora_matmul", dev, stream, at("x", x, (rows, k), _BF16, dev), BFLY_BF16,
-          at("ids", ids, (rows,), _I32, dev), at("lora_a", lora_a, (num, rank, k), _BF16, dev),
-          at("lora_b", lora_b, (num, n_out, rank), _BF16, dev),
-          at("scaling", scaling, (num,), _F32, dev),
-          at("base", base, (rows, n_out), _ROWS, dev), 0 if base is None else _kind(base),
-          at("y", y, (rows, n_out), _ROWS, dev), _kind(y), rows, n_out, k, num, rank, ws, ws_bytes)
+    _call(_ext().lora_matmul, x, stream, x, lora_a, y, ids, lora_b, scaling, base, workspace)
 
 
 def bfly_grad_clip_workspace_bytes(count: int) -> int:
@@ -508,16 +464,4 @@ def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> 
     float32; workspace: a uint8 tensor of bfly_grad_clip_workspace_bytes.  No
     two of the tensors that are written may overlap, nor an output a gradient
     other than its own."""
-    ext = _ext()
-    dev = norm.get_device()
-    ws, ws_bytes = ext.scratch(workspace, dev)
-    at, numels, types = ext.describe(grads, dev, outs is None)
-    to = None
-    if outs is not None:
-        to, *like = ext.describe(outs, dev, True)
-        if like != [numels, types]:
-            raise ValueError("the outputs have to be like their gradients")
-        if not ext.apart(at, to, numels, types):
-            raise ValueError("an output overlaps a gradient that is not its own")
-    _call("bfly_grad_clip", dev, stream, len(types) // 4, at, to, numels, types, max_norm,
-          ext.at("norm", norm, (2,), _F32, dev), ws, ws_bytes)
+    _call(_ext().grad_clip, norm, stream, max_norm, norm, workspace, grads, outs)

@@ -53,7 +53,8 @@ def extension_command(out: str):
     import sysconfig
     import torch
     from torch.utils import cpp_extension
-    dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    dirs = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+            os.path.join(os.path.dirname(HERE), "include")]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,

@@ -159,73 +159,120 @@ def extension():
     return B._ext()
 
 
-def test_the_list_of_gradients_is_checked():
+def refused(call, *args, error):
+    for _ in range(3):
+        with pytest.raises(error):
+            call(0, 0, *args)
+
+
+def test_the_lists_of_gradients_are_checked():
     ext, ok = extension(), torch.zeros(3)
-    assert ext.describe([], 0, True) == (b"", b"", b"")
-    for bad, error in ((3, TypeError), ([3], TypeError), ([ok.double()], TypeError),
-                       ([torch.zeros(2, dtype=torch.int8), ok], TypeError), ([ok], ValueError),
-                       ([None], TypeError)):
-        for _ in range(3):
-            with pytest.raises(error):
-                ext.describe(bad, 0, False)
-    with pytest.raises(TypeError):
-        ext.describe([])
+    clip = lambda grads, error, outs=None: refused(ext.grad_clip, 1.0, None, None, grads, outs,
+                                                   error=error)
+    assert ext.grad_clip(0, 0, 1.0, None, None, [], None) == NULL      # the library's answer
+    assert ext.grad_clip(0, 0, 1.0, None, None, (), []) == NULL
+    assert ext.grad_clip(0, 0, 0.0, None, None, [], None) == SIZE
+    for bad, error in ((3, TypeError), (None, TypeError), ([3], TypeError),
+                       ([ok.double()], TypeError), ([torch.zeros(2, dtype=torch.int8), ok], TypeError),
+                       ([None], TypeError), ([ok.to_sparse()], ValueError),
+                       ([torch.zeros((3, 4)).T], ValueError), ([ok], ValueError)):
+        clip(bad, error)
+        if bad is not None:
+            clip([], error, bad)
+    refused(ext.grad_clip, "1", None, None, [], None, error=TypeError)
+    refused(ext.grad_clip, 1.0, ok.half(), None, [], None, error=TypeError)
+    refused(ext.grad_clip, 1.0, ok, None, [], None, error=ValueError)       # [3]
+    refused(ext.grad_clip, 1.0, ok[:2], None, [], None, error=ValueError)   # not on a GPU
+    refused(ext.grad_clip, 1.0, None, None, [], error=TypeError)
 
 
-def test_outputs_and_other_gradients_are_told_apart():
+def test_overlapping_outputs_are_found():
     ext = extension()
 
     def apart(ins, outs, numels, types=None):
-        n = len(ins)
-        pack = lambda t, v: bytes((t * n)(*v))
-        return ext.apart(pack(ctypes.c_uint64, ins), pack(ctypes.c_uint64, outs),
-                         pack(ctypes.c_int64, numels), pack(ctypes.c_int32, types or [0] * n))
+        return ext.overlaps(tuple(ins), None if outs is None else tuple(outs), tuple(numels),
+                            tuple(types or [0] * len(ins))) is None
 
-    assert apart([], [], []) is True
-    assert apart([64], [64], [4]) is True                         # in place
-    assert apart([64], [68], [4]) is False                        # moved by an element
-    assert apart([64], [60], [4]) is False
-    assert apart([64], [80], [4]) is True and apart([64], [48], [4]) is True
-    assert apart([64], [72], [4], [1]) is True                    # bf16: 8 bytes
-    assert apart([64, 128], [128, 64], [4, 4]) is False           # swapped
-    assert apart([64, 128], [256, 64], [4, 4]) is False
-    assert apart([64, 128], [256, 64], [0, 4]) is True            # the first is empty
-    assert apart([64, 64], [64, 256], [4, 4]) is False            # read again after it is written
-    assert apart([64, 64], [128, 256], [4, 4]) is True
-    assert apart([64, 64], [100, 72], [16, 1]) is False           # an output inside an input
-    assert apart([72, 300], [500, 64], [1, 16]) is False          # an input inside an output
+    assert apart([], [], []) and apart([], None, [])
+    assert apart([64], [64], [4]) and apart([64], None, [4])      # in place
+    assert not apart([64], [68], [4])                             # moved by an element
+    assert not apart([64], [60], [4])
+    assert apart([64], [80], [4]) and apart([64], [48], [4])
+    assert apart([64], [72], [4], [1])                            # bf16: 8 bytes
+    assert not apart([64, 128], [128, 64], [4, 4])                # swapped
+    assert not apart([64, 128], [256, 64], [4, 4])
+    assert apart([64, 128], [256, 64], [0, 4])                    # the first is empty
+    assert not apart([64, 64], [64, 256], [4, 4])                 # read again after it is written
+    assert apart([64, 64], [128, 256], [4, 4])
+    assert not apart([64, 64], None, [4, 4]) and not apart([64, 64], [128, 140], [4, 4])
+    assert not apart([64, 60], None, [4, 2]) and apart([64, 60], None, [4, 2], [0, 1])
+    assert not apart([64, 64], [100, 72], [16, 1])                # an output inside an input
+    assert not apart([72, 300], [500, 64], [1, 16])               # an input inside an output
     n = 50
     ins = [4096 + 64 * (i * 7 % n) for i in range(n)]
-    assert apart(ins, ins, [16] * n) is True
-    assert apart(ins, [1 << 20 | 64 * i for i in range(n)], [16] * n) is True
-    assert apart(ins, [a + 4 for a in ins], [15] * n) is False
-    for bad in ((b"", b"", b"", b"1"), (b"", b"", b"", b"1234"), (b"",), (b"", b"", b"", 3)):
+    assert apart(ins, ins, [16] * n) and apart(ins, None, [16] * n)
+    assert not apart(ins, None, [17] * n)
+    assert apart(ins, [1 << 20 | 64 * i for i in range(n)], [16] * n)
+    assert not apart(ins, [a + 4 for a in ins], [15] * n)
+    for bad in (((), (), ()), ((1,), (), (), ()), ((), (), (1,), ()), ((), (), (), [])):
         with pytest.raises((TypeError, ValueError)):
-            ext.apart(*bad)
+            ext.overlaps(*bad)
 
 
-def test_a_tensor_is_checked():
-    ext, x = extension(), torch.zeros((3, 4))
-    assert ext.at("x", None, (3, 4), 1, 0) is None
-    for args, error in ((("x", 5, (3, 4), 1, 0), TypeError), (("x", x, [3, 4], 1, 0), TypeError),
-                        (("x", x, (3, 4), 2, 0), TypeError), (("x", x, (3, 4), "1", 0), TypeError),
-                        (("x", x, (3, 5), 1, 0), ValueError), (("x", x, (3,), 1, 0), ValueError),
-                        (("x", x, (3, 4, 1), 1, 0), ValueError),
-                        (("x", x, (3, "4"), 1, 0), TypeError),
-                        (("x", x.T, (4, 3), 1, 0), ValueError),
-                        (("x", x.to_sparse(), (3, 4), 1, 0), ValueError),
-                        (("x", x, (3, 4), 1, 0), ValueError),      # not on a GPU
-                        (("x", x, (3, 4), 1, -1), ValueError), (("x", x), TypeError)):
-        for _ in range(3):
-            with pytest.raises(error):
-                ext.at(*args)
+def test_the_tensors_of_a_norm_are_checked():
+    ext, x = extension(), torch.zeros((3, 64))
+    w, v, c = torch.zeros(64), torch.zeros(3), torch.zeros((3, 64), dtype=torch.int8)
+    # eps, format, group, x, weight, y, codes, scales, residual, h, rstd: a call
+    # whose tensors are as they have to be stops at the GPU they are not on
+    good = [1e-5, 0, None, x, w, x, c, torch.zeros((3, 1), dtype=torch.float16), x, x, v]
+    refused(ext.rmsnorm, *good, error=ValueError)
+    for at, value, error in ((0, "1", TypeError), (0, None, TypeError), (1, 1.5, TypeError),
+                             (1, 1 << 40, ValueError), (2, "n", TypeError), (2, 1 << 32, ValueError),
+                             (3, None, TypeError), (3, 5, TypeError), (3, x.half(), TypeError),
+                             (3, x[0], ValueError), (3, x.to_sparse(), ValueError),
+                             (3, x[:, ::2], ValueError), (4, 5, TypeError),
+                             (4, w.double(), TypeError), (4, w[1:], ValueError),
+                             (5, x.half(), TypeError), (5, x[1:], ValueError), (6, x, TypeError),
+                             (6, c[:, 1:], ValueError), (7, v, TypeError),
+                             (7, x.half(), ValueError), (2, 32, ValueError), (2, 0, ValueError),
+                             (8, x.bfloat16(), TypeError), (9, x.bfloat16(), TypeError),
+                             (8, x.T, ValueError), (9, w, ValueError), (10, v.double(), TypeError),
+                             (10, w, ValueError)):
+        refused(ext.rmsnorm, *good[:at], value, *good[at + 1:], error=error)
+    refused(ext.rmsnorm, *good[:-1], error=TypeError)
+    # h, weight, rstd, dy, dx, dweight, dh, workspace
+    good = [x, w, v, x, x, w, x, v]
+    refused(ext.rmsnorm_backward, *good, error=ValueError)
+    for at, value, error in ((0, None, TypeError), (0, x.long(), TypeError), (0, x[0], ValueError),
+                             (1, v, ValueError), (2, w, ValueError), (3, x.half(), TypeError),
+                             (3, x[:2], ValueError), (4, x.bfloat16(), TypeError),
+                             (5, w.bfloat16(), TypeError), (6, x.bfloat16(), TypeError),
+                             (6, x.T, ValueError), (7, 5, TypeError), (7, x.T, ValueError),
+                             (7, x.to_sparse(), ValueError)):
+        refused(ext.rmsnorm_backward, *good[:at], value, *good[at + 1:], error=error)
+    refused(ext.rmsnorm_backward, *good, None, error=TypeError)
 
 
-def test_a_workspace_is_checked():
-    ext, x = extension(), torch.zeros((3, 4))
-    assert ext.scratch(None, 0) == (None, 0)
-    for args, error in (((5, 0), TypeError), ((x, 0), ValueError), ((x, -1), ValueError),
-                        ((x.to_sparse(), 0), ValueError), ((x, "0"), TypeError), ((x,), TypeError)):
-        for _ in range(3):
-            with pytest.raises(error):
-                ext.scratch(*args)
+def test_the_tensors_of_adapters_are_checked():
+    ext, b = extension(), torch.zeros((3, 64), dtype=torch.bfloat16)
+    a, up = torch.zeros((2, 8, 64), dtype=torch.bfloat16), torch.zeros((2, 16, 8), dtype=torch.bfloat16)
+    y, ids = torch.zeros((3, 16)), torch.zeros(3, dtype=torch.int32)
+    # x, lora_a, y, ids, lora_b, scaling, base, workspace
+    v2 = torch.zeros(2)
+    good = [b, a, y, ids, up, v2, y, ids]
+    refused(ext.lora_matmul, *good, error=ValueError)
+    for at, value, error in ((0, None, TypeError), (0, b.float(), TypeError), (0, b[0], ValueError),
+                             (0, b[:, ::2], ValueError), (1, a[0], ValueError),
+                             (1, a.float(), TypeError), (1, a[:, :, :8], ValueError),
+                             (2, None, TypeError), (2, y.half(), TypeError), (2, y[1:], ValueError),
+                             (3, ids.long(), TypeError), (3, ids[1:], ValueError),
+                             (4, a, ValueError), (4, up.float(), TypeError),
+                             (5, v2.double(), TypeError), (5, ids, TypeError), (5, y[0], ValueError),
+                             (6, y.T, ValueError), (6, y.half(), TypeError), (7, "w", TypeError)):
+        refused(ext.lora_matmul, *good[:at], value, *good[at + 1:], error=error)
+    with pytest.raises(TypeError):
+        ext.lora_matmul(0, "0", *good)
+    with pytest.raises(TypeError):
+        ext.lora_matmul()
+    with pytest.raises(ValueError):
+        ext.bind(0, 1, 2, 3)
