@@ -28,8 +28,8 @@ struct ClipTensor {
   int32_t kind;    // 1: bf16, 0: fp32; + 2 * the elements before the tensor's first
 };
 // Tensors whose table goes into a launch's arguments; for more of them it is
-// written to the workspace first, this many to a launch.
-constexpr int kClipBatch = 112;
+// written to the workspace first, kClipSources to a launch.
+constexpr int kClipBatch = 112, kClipSources = 160;
 
 // Workspace: the slots' sums of squares, then the table.
 constexpr size_t kClipTableOffset = kClipManySlots * sizeof(double);

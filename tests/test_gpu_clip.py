@@ -69,6 +69,14 @@ def test_clip_sizes(sizes, dtypes, in_place):
     check(tensors(len(sizes), sizes, dtypes), 0.01, in_place)
 
 
+@pytest.mark.parametrize("count", [111, 112, 113, 159, 160, 161, 320, 321, 500])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_clip_counts(count, in_place):
+    # lengths of all kinds, every ninth tensor empty
+    sizes = [0 if i % 9 == 4 else 1 + i * 977 % 9001 for i in range(count + (count + 4) // 8)]
+    check(tensors(len(sizes), sizes, (F32, BF16), 1.0), 0.7, in_place)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("count", [3, 300])
 def test_clip_many_elements(count, in_place):
