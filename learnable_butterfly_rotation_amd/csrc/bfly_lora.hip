@@ -28,15 +28,19 @@ constexpr int kNoAdapter = kLoraMaxAdapters;
 // The rows of a block in the order of their adapters, cut into tiles of at
 // most kTileRows rows of one adapter; rows without one come last.
 struct Tiles {
-  uint32_t key[kBlockRows];    // by row, adapter * 256 + row; a missing row: the largest value
-  uint32_t sorted[kBlockRows];  // the keys in their order
-  uint64_t heads[kBlockRows / 64];  // places where a tile begins
-  uint64_t runs[kBlockRows / 64];   // places where an adapter's rows begin
-  uint16_t start[kBlockRows];  // by tile: its first place
+  __align__(16) uint32_t key[kBlockRows];  // by row, adapter * 256 + row; missing: the largest
+  uint32_t sorted[kBlockRows];             // the keys in their order
+  uint64_t runs[kBlockRows / 64];          // places where an adapter's rows begin
+  uint64_t ordered[kBlockRows / 64];       // rows whose key is not below the one before
+  uint16_t start[kBlockRows];              // by tile: its first place
   int count;
   __device__ int row(int place) const { return (int)(sorted[place] & 255u); }
   __device__ int id(int place) const { return (int)(sorted[place] >> 8); }
 };
+
+__device__ __forceinline__ int adapter_of(int id, int n_adapters) {
+  return id < 0 || id >= n_adapters ? kNoAdapter : id;
+}
 
 // A row's place by counting, for adapters below 256 (`none`: the number that
 // stands for no adapter): its rank among its wave's rows of the same adapter
@@ -82,65 +86,103 @@ __device__ __forceinline__ int count_place(uint16_t (&bins)[kBlockRows / 64][256
   return valid ? bins[wave][id] + before : i;
 }
 
-// The places come from counting where the rows are many and the adapters few,
-// else every thread ranks its own row against all the others (the keys are in
-// LDS, read four at a time as broadcasts): no sort, no atomics, and any ids.
-// Counting and ranking, a whole call: 512 rows of 4 adapters, rank 16, 14.7 us
-// and 16.5; 257 rows of 32, rank 64, 28.1 and 29.9; 16 rows of 8 10.2 and 9.5.
-__device__ __forceinline__ void make_tiles(Tiles& s, const int32_t* ids, int nr, int n_adapters) {
+// Up to 64 rows: every wave works the order out by itself and all write the
+// same values down, without a barrier.  A row's place is the number of smaller
+// keys, counted lane by lane.
+__device__ __forceinline__ void make_few_tiles(Tiles& s, const int32_t* ids, int nr,
+                                               int n_adapters, int tile_rows) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key = ~0u;
+  if (lane < nr) key = (uint32_t)adapter_of(ids[lane], n_adapters) << 8 | (uint32_t)lane;
+  int place = lane;
+  const uint32_t before = (uint32_t)__shfl_up((int)key, 1);
+  if (__ballot(lane > 0 && before > key)) {  // packed prompts mostly come in order
+    place = 0;
+    for (int j = 0; j < nr; j += 8)
+#pragma unroll
+      for (int u = 0; u < 8; ++u)  // past nr: the largest value, never below
+        place += (uint32_t)__builtin_amdgcn_readlane((int)key, j + u) < key ? 1 : 0;
+  }
+  if (lane < nr) s.sorted[place] = key;
+  wave_lds_sync();
+  const uint32_t mine = s.sorted[lane] >> 8, left = s.sorted[lane ? lane - 1 : 0] >> 8;
+  const uint64_t runs = __ballot(lane == 0 || mine != left) & (~0ull >> (63 - lane));
+  const int first = 63 - __clzll((long long)runs);  // of this place's adapter
+  const bool head = lane < nr && ((lane - first) & (tile_rows - 1)) == 0;
+  const uint64_t heads = __ballot(head);
+  if (head) s.start[__popcll(heads & ((1ull << lane) - 1))] = (uint16_t)lane;
+  if (lane == 0) s.count = __popcll(heads);
+  wave_lds_sync();
+}
+
+// More rows.  Where they are not in order already, the places come from
+// counting where the adapters are below 256, and every thread ranks its own row
+// against all the others where they are not (the keys are in LDS, read four at
+// a time as broadcasts): no sort, no atomics, and any ids.
+// Counting and ranking, a whole call: 512 rows of 4 adapters, rank 16, 12.0 us
+// and 13.8; 257 rows of 32, rank 64, 23.2 and 25.0.
+__device__ __forceinline__ void make_tiles(Tiles& s, const int32_t* ids, int nr, int n_adapters,
+                                           int tile_rows) {
+  if (nr <= 64) return make_few_tiles(s, ids, nr, n_adapters, tile_rows);
   const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
   uint32_t key = ~0u;
-  int id = kNoAdapter;
+  int id = kNoAdapter, before = -1;
   if (i < nr) {
-    id = ids[i];
-    if (id < 0 || id >= n_adapters) id = kNoAdapter;
+    id = adapter_of(ids[i], n_adapters);
+    if (i > 0) before = adapter_of(ids[i - 1], n_adapters);
     key = (uint32_t)id << 8 | (uint32_t)i;
   }
-  s.key[i] = key;
+  s.key[i] = s.sorted[i] = key;
+  const uint64_t runs = __ballot(i < nr && id != before);
+  const uint64_t ordered = __ballot(before <= id);
+  if (lane == 0) {
+    s.runs[wave] = runs;
+    s.ordered[wave] = ordered;
+  }
   __syncthreads();
-  int place = i;
-  // packed prompts mostly come in order: nothing to rank then
-  if (!__syncthreads_and(i == 0 || s.key[i - 1] <= key)) {
-    if (n_adapters < 256 && nr > 64) {
+  uint64_t all = ~0ull;
+#pragma unroll
+  for (int w = 0; w < kBlockRows / 64; ++w) all &= s.ordered[w];
+  if (all != ~0ull) {
+    int place = 0;
+    if (n_adapters < 256) {
       __shared__ uint16_t bins[kBlockRows / 64][256];
       __shared__ int totals[kBlockRows / 64];
       place = count_place(bins, totals, id == kNoAdapter ? n_adapters : id, i < nr);
     } else {
-      place = 0;
 #pragma unroll 4
       for (int j = 0; j < nr; j += 4) {  // past nr: the largest value, never below
         const uint4 o = *reinterpret_cast<const uint4*>(s.key + j);
         place += (o.x < key) + (o.y < key) + (o.z < key) + (o.w < key);
       }
     }
+    if (i < nr) s.sorted[place] = key;
+    __syncthreads();
+    const uint32_t mine = s.sorted[i] >> 8, left = s.sorted[i ? i - 1 : 0] >> 8;
+    const uint64_t again = __ballot(i < nr && (i == 0 || mine != left));
+    if (lane == 0) s.runs[wave] = again;
+    __syncthreads();
   }
-  if (i < nr) s.sorted[place] = key;
-  __syncthreads();
-  const uint32_t mine = i < nr ? s.sorted[i] >> 8 : ~0u;
-  const uint32_t left = i > 0 && i < nr ? s.sorted[i - 1] >> 8 : ~0u;
-  const uint64_t runs = __ballot(i < nr && mine != left);
-  if (lane == 0) s.runs[wave] = runs;
-  __syncthreads();
-  // the first place of this place's adapter: the last run mark not beyond it
-  int first = 0;
-  for (int w = 0; w <= wave; ++w) {
-    const uint64_t m = w < wave ? s.runs[w] : runs & (~0ull >> (63 - lane));
-    if (m) first = w * 64 + 63 - __clzll((long long)m);
-  }
-  const bool head = i < nr && ((i - first) & (kTileRows - 1)) == 0;
-  const uint64_t heads = __ballot(head);
-  if (lane == 0) s.heads[wave] = heads;
-  __syncthreads();
-  int before = 0, all = 0;
+  // the tiles' first places: every wave goes through all places by itself and
+  // they all write the same values down
+  int count = 0;
 #pragma unroll
   for (int w = 0; w < kBlockRows / 64; ++w) {
-    const int c = __popcll(s.heads[w]);
-    before += w < wave ? c : 0;
-    all += c;
+    const int at = w * 64 + lane;
+    // the first place of this place's adapter: the last run mark not beyond it
+    int first = 0;
+#pragma unroll
+    for (int v = 0; v <= w; ++v) {
+      const uint64_t m = s.runs[v] & (v < w ? ~0ull : ~0ull >> (63 - lane));
+      if (m) first = v * 64 + 63 - __clzll((long long)m);
+    }
+    const bool head = at < nr && ((at - first) & (tile_rows - 1)) == 0;
+    const uint64_t heads = __ballot(head);
+    if (head) s.start[count + __popcll(heads & ((1ull << lane) - 1))] = (uint16_t)at;
+    count += __popcll(heads);
   }
-  if (head) s.start[before + __popcll(heads & ((1ull << lane) - 1))] = (uint16_t)i;
-  if (i == 0) s.count = all;
-  __syncthreads();
+  if (lane == 0) s.count = count;
+  wave_lds_sync();
 }
 
 // The order that shrink works out, as it leaves it for expand in the workspace.
@@ -214,6 +256,7 @@ struct ShrinkArgs {
   float* t;      // the split's sums of the block's first row, at the rank block
   uint8_t* lds;  // [4][kWaveBytes]; then the sums of two waves
   int k, kbeg, kend, stride;
+  int ranks;  // of t from the rank block's first on
 };
 
 // NT * 16 rows of a tile (`len` of them, the others read as zeros).
@@ -323,8 +366,9 @@ __device__ __forceinline__ void shrink_rows(const ShrinkArgs<RT>& P, int start, 
             P.t + (int64_t)P.tiles->row(start + q * 16 + n) * P.stride + 4 * g;
 #pragma unroll
         for (int j = 0; j < RT; ++j)
-          *reinterpret_cast<f32x4*>(to + 16 * j) =
-              acc[j][q] + part[half + (j * NT + q) * 64 + lane];
+          if (16 * j < P.ranks)
+            *reinterpret_cast<f32x4*>(to + 16 * j) =
+                acc[j][q] + part[half + (j * NT + q) * 64 + lane];
       }
     }
   }
@@ -337,6 +381,7 @@ __device__ __forceinline__ void shrink_rows(const ShrinkArgs<RT>& P, int start, 
 // (257 rows of 32 adapters, k = 11008, rank 64: 27.7 us in all for 23.6).
 struct TileLanes {
   int blocks, lanes, last;
+  int tile_rows;  // of a tile at most: a power of two up to kTileRows
   __host__ __device__ int count() const { return (blocks - 1) * lanes + last; }
   __device__ __forceinline__ int of(int block) const { return block + 1 < blocks ? lanes : last; }
   __device__ __forceinline__ void place(int i, int& block, int& lane) const {
@@ -360,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, TileLane
   const int64_t row0 = (int64_t)block * kBlockRows;
   const int nr = P.rows - row0 < kBlockRows ? (int)(P.rows - row0) : kBlockRows;
   const int split = blockIdx.y % splits, rank0 = blockIdx.y / splits * (RT * 16);
-  make_tiles(tiles, P.ids + row0, nr, P.n_adapters);
+  make_tiles(tiles, P.ids + row0, nr, P.n_adapters, L.tile_rows);
   if (first == 0 && blockIdx.y == 0) put_order(order_at(P) + block, tiles);
   S a;
   a.rx = buffer_range(P.x + row0 * P.k, (int64_t)nr * P.k * 2);
@@ -371,6 +416,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(LoraParams P, TileLane
   a.kbeg = split * slice;
   a.kend = P.k - a.kbeg < slice ? P.k : a.kbeg + slice;
   a.stride = stride;
+  a.ranks = stride - rank0;
   const int count = tiles.count;
   const int lanes = L.of(block);
   for (int tile = first; tile < count; tile += lanes) {
@@ -623,29 +669,29 @@ struct Cut {
   int stride;    // floats of a row of t
   int64_t blocks;  // blocks of rows
   int splits, slice;  // of the k axis
+  int tile_rows;      // 16, 32 or 64
 };
 // Workgroups that share a block's tiles: as many as it can have tiles, and
 // where there are many blocks as many as packed prompts have (four, and one
 // more for every change of adapter within 256 rows): the others would start
 // only to find nothing (257 rows of 32 adapters: 36.3 us with 16, 31.0 with 33;
 // 8192 rows of 6 adapters: 137 us with 8 and no less with more).
-TileLanes tile_lanes(int64_t rows, int64_t blocks, int n_adapters) {
+TileLanes tile_lanes(int64_t rows, int64_t blocks, int n_adapters, int tile_rows) {
   const int cap = blocks <= 2 ? 64 : blocks <= 8 ? 16 : 8;
   const auto lanes = [&](int r) {
-    const int most = (r < n_adapters ? r : n_adapters) + r / kTileRows + 1;
+    const int most = (r < n_adapters ? r : n_adapters) + r / tile_rows + 1;
     return most < r ? (most < cap ? most : cap) : (r < cap ? r : cap);
   };
   TileLanes t;
   t.blocks = (int)blocks;
+  t.tile_rows = tile_rows;
   t.last = lanes((int)(rows - (blocks - 1) * kBlockRows));
   t.lanes = blocks > 1 ? lanes(kBlockRows) : t.last;
   return t;
 }
-Cut cut(int64_t rows, int k, int n_adapters, int rank) {
+Cut cut(int64_t rows, int n_out, int k, int n_adapters, int rank) {
   Cut c;
-  c.rt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
-  c.ranks = (rank + 16 * c.rt - 1) / (16 * c.rt);
-  c.stride = c.ranks * c.rt * 16;
+  c.stride = (rank + 15) / 16 * 16;
   c.blocks = (rows + kBlockRows - 1) / kBlockRows;
   // The k axis is split until there is a workgroup for every CU, counting the
   // tiles there can be: one to 64 rows, and one more for every adapter of a
@@ -654,20 +700,43 @@ Cut cut(int64_t rows, int k, int n_adapters, int rank) {
   // 256, 29.1 with 384; 257 rows of 32, k = 11008: 23.8 with 256, 24.3 with 384).
   // A workgroup takes 512 k at least, which its waves wait for twice.
   const int64_t tail = rows - (c.blocks - 1) * kBlockRows;
-  const int64_t tiles = (rows + kTileRows - 1) / kTileRows +
-                        (c.blocks - 1) * (n_adapters < kBlockRows ? n_adapters : kBlockRows) +
-                        (n_adapters < tail ? n_adapters : tail);
+  const int64_t changes =
+      (c.blocks - 1) * (n_adapters < kBlockRows ? n_adapters : kBlockRows) +
+      (n_adapters < tail ? n_adapters : tail);
+  const auto tiles_of = [&](int tile_rows) { return (rows + tile_rows - 1) / tile_rows + changes; };
+  const auto ranks_of = [&](int rt) { return (rank + 16 * rt - 1) / (16 * rt); };
+  const int64_t tiles = tiles_of(kTileRows);
   const int most = (k + 511) / 512;
-  const int64_t want = 256 / (tiles * c.ranks);
+  c.rt = rank <= 16 ? 1 : rank <= 32 ? 2 : 4;
+  const int64_t want = 256 / (tiles * ranks_of(c.rt));
   c.splits = (int)(want < 1 ? 1 : want < most ? want : most);
   c.slice = ((k + c.splits - 1) / c.splits + 127) / 128 * 128;
   c.splits = (k + c.slice - 1) / c.slice;
+  // Where that leaves CUs idle, tiles of fewer rows, as far as the adapters have
+  // rows for them on average (99 rows of 2, 1024 to 1024, rank 40: 14.2 us for
+  // 10.2; 512 of 4, 4096 to 4096, rank 16: 14.0 for 12.0; up to 256 workgroups
+  // instead of 512: 1000 of 6, 8192 to 4096, rank 32 19.8 for 17.6), with at most
+  // 1024 workgroups of expand (132 of 3, 5120 to 11008, rank 64: 15.3 us, up to
+  // 512 16.9); then workgroups of fewer ranks (64 of 1, 4096 to 4096, rank 64:
+  // 13.0 us for 11.6; up to 512 workgroups instead of 256: 2048 of 4 26.4 for
+  // 25.7, 64 of 8 14.4 for 14.9).
+  c.tile_rows = kTileRows;
+  const int64_t cols = (n_out + 255) / 256;
+  const int64_t mean = (rows < kBlockRows ? rows : kBlockRows) / n_adapters;
+  const auto work = [&](int tile_rows, int rt) {
+    return tiles_of(tile_rows) * c.splits * ranks_of(rt);
+  };
+  while (c.tile_rows > 16 && mean > c.tile_rows / 2 && work(c.tile_rows / 2, c.rt) <= 512 &&
+         tiles_of(c.tile_rows / 2) * cols <= 1024)
+    c.tile_rows /= 2;
+  while (c.rt > 1 && work(c.tile_rows, c.rt / 2) <= 256) c.rt /= 2;
+  c.ranks = ranks_of(c.rt);
   return c;
 }
 
 template <int RT>
 void shrink(const LoraParams& p, const Cut& c, hipStream_t s) {
-  const TileLanes lanes = tile_lanes(p.rows, c.blocks, p.n_adapters);
+  const TileLanes lanes = tile_lanes(p.rows, c.blocks, p.n_adapters, c.tile_rows);
   hipLaunchKernelGGL((shrink_kernel<RT>), dim3((unsigned)lanes.count(), c.splits * c.ranks),
                      dim3(kThreads), 0, s, p, lanes, c.splits, c.slice, c.stride);
 }
@@ -677,7 +746,7 @@ template <int TERMS, bool BB, bool YB, int DK, int H>
 void expand(const LoraParams& p, const Cut& c, hipStream_t s) {
   using E = Expand<TERMS, BB, YB, DK>;
   static_assert(E::kRows == kTileRows, "a tile's rows are taken at once");
-  const TileLanes lanes = tile_lanes(p.rows, c.blocks, p.n_adapters);
+  const TileLanes lanes = tile_lanes(p.rows, c.blocks, p.n_adapters, c.tile_rows);
   const int y = lanes.count() < kMaxGridY ? lanes.count() : kMaxGridY;
   hipLaunchKernelGGL((expand_kernel<TERMS, BB, YB, DK, H>),
                      dim3((p.n_out + E::kCols - 1) / E::kCols, y, (lanes.count() + y - 1) / y),
@@ -694,13 +763,13 @@ void expand_by_rank(const LoraParams& p, const Cut& c, hipStream_t s) {
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t rows, int k, int rank) {
-  const Cut c = cut(rows, k, 1, rank);  // most splits
+  const Cut c = cut(rows, 8, k, 1, rank);  // most splits
   return (size_t)c.blocks * sizeof(Order) +
          (size_t)c.splits * (size_t)rows * (size_t)c.stride * sizeof(float);
 }
 
 hipError_t launch_lora(const LoraParams& p, hipStream_t s) {
-  const Cut c = cut(p.rows, p.k, p.n_adapters, p.rank);
+  const Cut c = cut(p.rows, p.n_out, p.k, p.n_adapters, p.rank);
   switch (c.rt) {
     case 1: shrink<1>(p, c, s); break;
     case 2: shrink<2>(p, c, s); break;
