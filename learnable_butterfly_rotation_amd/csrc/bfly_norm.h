@@ -41,6 +41,6 @@ struct NormBwdParams {
 // Row slots of the weight gradient: a function of (rows, n) only, so that the
 // order of its sum never depends on the device.
 int rmsnorm_bwd_slots(int64_t rows, int n);
-hipError_t launch_rmsnorm_backward(const NormBwdParams& p, hipStream_t s);
+hipError_t launch_rmsnorm_backward(NormBwdParams p, hipStream_t s);
 
 }  // namespace bfly

@@ -464,9 +464,12 @@ hipError_t norm_bwd_run(const NormBwdParams& p, hipStream_t s) {
 // adding them costs 16384 x 5120 fp32 6 us at 256 slots and 18 at 1024
 // (182 and 194 us in all), while narrow rows need the workgroups to have
 // enough loads in flight.  With many rows more of them, so that a thread's
-// fp32 sum goes over about 128 rows.
+// fp32 sum goes over about 128 rows.  A single one for two or three groups of
+// rows: it is the sum already, and a launch less (3 rows of 4096: 4.6 us in a
+// graph for 5.3, but 4 rows 5.4; 2 rows of 11008 5.7 for 6.6, 3 rows 7.0).
 int rmsnorm_bwd_slots(int64_t rows, int n) {
   const int64_t need = (rows + rows_per_block(n) - 1) / rows_per_block(n);
+  if (need > 0 && need <= (n <= 8192 ? 3 : 2)) return 1;
   int64_t most = n <= 1024 ? 1024 : n >= 4096 ? 256 : (1 << 20) / n;
   const int64_t many = need / 128 < 2048 ? need / 128 : 2048;
   if (most < many) most = many;
@@ -485,15 +488,19 @@ hipError_t launch_rmsnorm(const NormParams& p, hipStream_t s) {
 #undef BFLY_NORM
 }
 
-hipError_t launch_rmsnorm_backward(const NormBwdParams& p, hipStream_t s) {
+hipError_t launch_rmsnorm_backward(NormBwdParams p, hipStream_t s) {
   const bool vec = p.n % 8 == 0;
+  // one partial sum: straight to its place, where 16-byte stores can go there
+  const bool alone = p.rows > 0 && rmsnorm_bwd_slots(p.rows, p.n) == 1 &&
+                     ((uintptr_t)p.dweight & 15) == 0;
+  if (alone) p.partials = p.dweight;
   hipError_t e = hipSuccess;
 #define BFLY_NORM_BWD(HB, GB) (vec ? norm_bwd_run<true, HB, GB>(p, s) : norm_bwd_run<false, HB, GB>(p, s))
   if (p.rows > 0)
     e = p.h_bf16 ? (p.g_bf16 ? BFLY_NORM_BWD(true, true) : BFLY_NORM_BWD(true, false))
                  : (p.g_bf16 ? BFLY_NORM_BWD(false, true) : BFLY_NORM_BWD(false, false));
 #undef BFLY_NORM_BWD
-  if (e != hipSuccess || !p.dweight) return e;
+  if (e != hipSuccess || !p.dweight || alone) return e;
   hipLaunchKernelGGL(norm_dw_kernel, dim3((p.n + 63) / 64), dim3(64 * kDwWays), 0, s,
                      p.partials, p.dweight, rmsnorm_bwd_slots(p.rows, p.n), p.n);
   return hipGetLastError();

@@ -280,6 +280,29 @@ def test_backward_many_rows(rows, n):
     assert err <= 362 ** 0.5 * U
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 12, 13, 48, 49])
+@pytest.mark.parametrize("n", [64, 100, 520, 4096, 11008])
+def test_backward_weight_gradient_at_any_address(rows, n):
+    g = torch.Generator().manual_seed(rows * n)
+    h, dy = (torch.randn((rows, n), generator=g).cuda() for _ in range(2))
+    r = torch.rand(rows, generator=g).cuda() + 0.5
+    ws = torch.full((B.bfly_rmsnorm_backward_workspace_bytes(rows, n),), 0x7F, dtype=torch.uint8,
+                    device="cuda")
+    buf, got = torch.full((n + 9,), 7.0, device="cuda"), []
+    for at in (4, 1, 2, 3):
+        B.bfly_rmsnorm_backward(h, None, r, dy, torch.empty_like(h), dweight=buf[at:at + n],
+                                workspace=ws)
+        got.append(buf[at:at + n].clone())
+        assert (buf[:at] == 7.0).all() and (buf[at + n:] == 7.0).all()
+        buf.fill_(7.0)
+    for v in got[1:]:
+        assert torch.equal(v, got[0])
+    exact = (dy.double() * h.double() * r.double()[:, None])
+    # at most rows + 40 additions, and the two products' roundings
+    tol = 1.01 * (rows + 42) * U * exact.abs().sum(0)
+    assert ((got[0].double() - exact.sum(0)).abs() <= tol).all()
+
+
 def test_backward_in_place():
     check_backward(rows_of(1, 40, 4096, F32), None, rows_of(2, 40, 4096, F32), None, in_place=True)
 
