@@ -501,9 +501,10 @@ struct Expand {
 };
 
 // Waves to a SIMD asked for where the compiler would give one fewer: what the
-// loads of one workgroup wait for, another's fill (8192 x 4096 to 4096, rank
-// 128: 61 us with 2 waves, 49 with 3, a few registers of it spilled; all of a
-// tile's base loaded ahead instead, 2 waves at rank 64: 44 us for 34).
+// loads of one workgroup wait for, another's fill (a whole call, 8192 x 4096 to
+// 4096: rank 64 58.0 us unasked, 57.0 with 4 waves; rank 128 91.2 and 81.4 with
+// 3; rank 256 213 and 158 with 2; all of a tile's base loaded ahead instead, 2
+// waves at rank 64: 10 us more).
 template <int TERMS, bool BB, bool YB, int DK, int H>
 __global__ void __launch_bounds__(kThreads,
                                   H > 1 ? 2 : DK == 2 ? 4 : DK == 4 && TERMS == 2 ? 3 : 1)
@@ -674,8 +675,9 @@ struct Cut {
 // Workgroups that share a block's tiles: as many as it can have tiles, and
 // where there are many blocks as many as packed prompts have (four, and one
 // more for every change of adapter within 256 rows): the others would start
-// only to find nothing (257 rows of 32 adapters: 36.3 us with 16, 31.0 with 33;
-// 8192 rows of 6 adapters: 137 us with 8 and no less with more).
+// only to find nothing (257 rows of 32 adapters: 29.8 us with 16, 23.4 with 33;
+// 700 rows of 5 22.7 with 8, 19.3 with 10; 8192 rows of 6 118.9 with 8, 120.2
+// with 11).
 TileLanes tile_lanes(int64_t rows, int64_t blocks, int n_adapters, int tile_rows) {
   const int cap = blocks <= 2 ? 64 : blocks <= 8 ? 16 : 8;
   const auto lanes = [&](int r) {
