@@ -402,15 +402,22 @@ __global__ void __launch_bounds__(64 * kDwWays) norm_dw_kernel(const float* part
 
 // Threads and chunks to a row: the fewest threads that hold it (777 x 5120
 // bf16 to e4m3: 17.6 us with 1024 threads and one chunk, of which 384 threads
-// had nothing, 9.9 with 256 and three).
+// had nothing, 9.9 with 256 and three).  But where a row has a CU to itself,
+// one chunk a thread: the chunks of a thread take their turns (1 x 4096 bf16 to
+// int8 in a graph 3.7 us with 256 threads and 3.3 with 512, 256 x 4096 4.4 and
+// 4.0, 16 x 8192 4.95 and 4.35 with 1024; 320 x 8192 7.6 and 8.1).
 #define BFLY_WIDTH(T, V) \
   if (n <= T * V * 8) return f(std::integral_constant<int, T>{}, std::integral_constant<int, V>{})
 template <typename F>
-hipError_t by_width(int n, F f) {
+hipError_t by_width(int64_t rows, int n, F f) {
   BFLY_WIDTH(16, 1);
   BFLY_WIDTH(64, 1);
   BFLY_WIDTH(64, 2);
   BFLY_WIDTH(256, 1);
+  if (rows <= 256) {
+    BFLY_WIDTH(512, 1);
+    BFLY_WIDTH(1024, 1);
+  }
   BFLY_WIDTH(256, 2);
   BFLY_WIDTH(256, 3);
   BFLY_WIDTH(256, 4);
@@ -440,7 +447,7 @@ constexpr int64_t kNormBlocks = 8192;
 
 template <bool VEC, bool XB, int Q>
 hipError_t norm_run(const NormParams& p, hipStream_t s) {
-  return by_width(p.n, [&](auto T, auto V) {
+  return by_width(p.rows, p.n, [&](auto T, auto V) {
     const int64_t need = (p.rows + rows_per_block(p.n) - 1) / rows_per_block(p.n);
     const int grid = (int)(need < kNormBlocks ? need : kNormBlocks);
     hipLaunchKernelGGL((norm_kernel<T(), V(), VEC, XB, Q>), dim3(grid),

@@ -126,6 +126,18 @@ def test_norm_widths(n, x_dt):
     check_norm(x, res, None, BF16, None, None, h_out=False)
 
 
+@pytest.mark.parametrize("rows", [256, 257])
+@pytest.mark.parametrize("n", [2049, 2056, 4096, 4100, 5120, 6152, 8191, 8192, 8200])
+@pytest.mark.parametrize("x_dt", [F32, BF16])
+def test_norm_widths_of_few_and_more_rows(rows, n, x_dt):
+    x, res = rows_of(n, rows, n, x_dt), rows_of(n + 1, rows, n, x_dt)
+    w = 1 + 0.1 * torch.randn(n, generator=torch.Generator().manual_seed(n + 2))
+    group = 8 if n % 8 == 0 else n
+    check_norm(x, res, w, F32, B.BFLY_Q8_INT8, group)
+    check_norm(x, None, w.to(BF16), BF16, B.BFLY_Q8_E4M3, n)
+    check_norm(x, res, None, BF16, None, None, h_out=False)
+
+
 @pytest.mark.parametrize("group,n", [(g, n) for g in (8, 16, 32, 64, 128, 256, 512) for n in
                                      (64, 128, 512, 1024, 2048, 1536, 4096, 5120, 11776, 16384)
                                      if g <= n])
