@@ -425,13 +425,16 @@ hipError_t by_width(int64_t rows, int n, F f) {
   BFLY_WIDTH(1024, 2);
   return hipErrorInvalidValue;
 }
+// dw and the next row's loads need registers too: one chunk a thread where two
+// would do (16384 x 4096 bf16 104 us with 256 threads and two, 99 with 512; fp32
+// 193 us either way).
 template <typename F>
-hipError_t by_width_bwd(int n, F f) {  // dw and the next row's loads need registers too
+hipError_t by_width_bwd(int n, F f) {
   BFLY_WIDTH(16, 1);
   BFLY_WIDTH(64, 1);
   BFLY_WIDTH(64, 2);
   BFLY_WIDTH(256, 1);
-  BFLY_WIDTH(256, 2);
+  BFLY_WIDTH(512, 1);
   BFLY_WIDTH(512, 2);
   BFLY_WIDTH(512, 3);
   BFLY_WIDTH(1024, 2);
