@@ -534,7 +534,8 @@ size_t bfly_rmsnorm_backward_workspace_bytes(int64_t rows, int32_t n);
  * enters the second product, times scaling, with 16 bits (bf16 y) or 24 (fp32
  * y); y is rounded once.  In calls of the same sizes a row's result does not
  * depend on the other rows'.
- * An infinity or a NaN in x or the adapter gives what the formula gives.
+ * An infinity or a NaN in x or the adapter gives what the formula gives, a
+ * scaled A_id x beyond bf16's largest value (3.39e38) counting as an infinity.
  * Sizes: k and n_out multiples of 8, k <= 65536, n_out <= 1048576, rank a
  * multiple of 8 up to 256, rows <= 8388608, n_adapters <= 4194304.  All pointers
  * 16-byte aligned but ids and scaling (4).  rows == 0 is a no-op.

@@ -9,7 +9,10 @@
 //
 // s_id t is fp32 and goes through the bf16 matrix cores as a sum of bf16
 // terms, each the rounding of what the ones before left: two terms (2^-16 of t
-// is lost at worst) where y is bf16, three (2^-24) where it is fp32.
+// is lost at worst) where y is bf16, three (2^-24) where it is fp32.  An
+// infinity of B times a term of zero or of the other sign would leave NaN where
+// the formula has an infinity: such elements of B enter the products as 2^-100
+// and their own products with t are added to y afterwards.
 #include "bfly_lora.h"
 #include "bfly_rows.h"
 
@@ -228,6 +231,18 @@ __device__ __forceinline__ float* t_at(const LoraParams& P) {
 __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Two bf16: the larger exponent bits of each half so far, and small numbers of
+// the same sign for those that are not finite (an infinite t stays what it is).
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 most_exponent(u16x2 m, uint32_t w) {
+  return __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w & 0x7F807F80u));
+}
+__device__ __forceinline__ uint32_t tamed(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w = (w & 0xFFFF8000u) | 0x0D80u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w = (w & 0x8000FFFFu) | 0x0D800000u;
+  return w;
 }
 
 // A row of 64 k in LDS: 128 bytes and 16 of padding, so that eight lanes
@@ -504,10 +519,11 @@ struct Expand {
 // loads of one workgroup wait for, another's fill (a whole call, 8192 x 4096 to
 // 4096: rank 64 58.0 us unasked, 57.0 with 4 waves; rank 128 91.2 and 81.4 with
 // 3; rank 256 213 and 158 with 2; all of a tile's base loaded ahead instead, 2
-// waves at rank 64: 10 us more).
+// waves at rank 64: 10 us more).  Up to rank 32 a bf16 base leaves room for 4,
+// which fp32 y misses by two registers unasked.
 template <int TERMS, bool BB, bool YB, int DK, int H>
 __global__ void __launch_bounds__(kThreads,
-                                  H > 1 ? 2 : DK == 2 ? 4 : DK == 4 && TERMS == 2 ? 3 : 1)
+                                  H > 1 ? 2 : DK == 2 || (DK == 1 && BB) ? 4 : DK == 4 && TERMS == 2 ? 3 : 1)
     expand_kernel(LoraParams P, TileLanes L, int splits, int stride) {
   using E = Expand<TERMS, BB, YB, DK>;
   constexpr int JT = E::JT;
@@ -616,6 +632,61 @@ __global__ void __launch_bounds__(kThreads,
           for (int j = 0; j < JT; ++j) acc[j] = mfma(ft, fb[j][d], acc[j]);
         }
     };
+    // Tames B's operands at hand and says whether that was called for, in any
+    // lane of the wave.  Looking costs two operations for two elements (whole
+    // calls, 8192 rows of 8 adapters, 4096 to 4096: rank 64 57.4 us without and
+    // 58.2 with, 128 84.8 and 86.1, 256 158 and 160; looking for NaN in every
+    // row's sums instead breaks up the loop: 8192 x 4096 to 11008, rank 32,
+    // 119.1 without, 118.9 so, 122.9).
+    const auto tame_b = [&]() __attribute__((always_inline)) {
+      u16x2 m = {0, 0};
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int d = 0; d < DK; ++d) {
+          const uint4 w = fb[j][d];
+          m = most_exponent(most_exponent(most_exponent(most_exponent(m, w.x), w.y), w.z), w.w);
+        }
+      const bool any = __any(m.x == 0x7F80u || m.y == 0x7F80u) != 0;
+      if (any) {
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+#pragma unroll
+          for (int d = 0; d < DK; ++d) {
+            uint4& w = fb[j][d];
+            w = make_uint4(tamed(w.x), tamed(w.y), tamed(w.z), tamed(w.w));
+          }
+      }
+      return any;
+    };
+    // The products that the lane's columns have with B's elements that are not
+    // finite, added to the rows of y that the lane has stored.
+    const auto add_untamed = [&]() {
+      __threadfence_block();
+      const float s = P.scaling[t.id];
+#pragma unroll 1
+      for (int c = col; c < col + JT && c < P.n_out; ++c)
+#pragma unroll 1
+        for (int r = 0; r < P.rank; ++r) {
+          const float b = bf16_lo(P.b[((int64_t)t.id * P.n_out + c) * P.rank + r]);
+          if (fabsf(b) < __builtin_inff()) continue;
+#pragma unroll 1
+          for (int i = 4 * g; i < len; i += (i & 3) == 3 ? 13 : 1) {  // 16 q + 4 g + 0..3
+            const int64_t row = row0 + tiles.row(t.start + i);
+            float v = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < splits; ++k) v += t_all[(k * P.rows + row) * stride + r];
+            v *= s;
+            if constexpr (YB) {
+              uint16_t* const y = static_cast<uint16_t*>(P.y) + row * P.n_out + c;
+              *y = (uint16_t)pack_bf16(fmaf(v, b, bf16_lo(*y)), 0.f);
+            } else {
+              float* const y = static_cast<float*>(P.y) + row * P.n_out + c;
+              *y = fmaf(v, b, *y);
+            }
+          }
+        }
+    };
     f32x4 acc[H > 1 ? E::QN : 1][JT];
     if constexpr (H > 1) {
 #pragma unroll
@@ -623,14 +694,17 @@ __global__ void __launch_bounds__(kThreads,
 #pragma unroll
         for (int j = 0; j < JT; ++j) acc[q][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    bool untamed = false;
     if (!none) {
       stage(0);
+      untamed = tame_b();
       if constexpr (H > 1) {
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           if (h > 0) {
             load_b(h);
             stage(h);
+            untamed |= tame_b();
           }
 #pragma unroll
           for (int q = 0; q < E::QN; ++q)
@@ -660,6 +734,7 @@ __global__ void __launch_bounds__(kThreads,
         E::store(ry, ro[q & 1][i], col, P.n_out, v);
       }
     }
+    if (untamed) add_untamed();
   }
 }
 

@@ -230,3 +230,61 @@ def test_rows_with_an_infinity(rank, y):
         assert (got[r, 0::3] == sign * float("inf")).all()
         assert (got[r, 1::3] == -sign * float("inf")).all()
         assert torch.isnan(got[r, 2::3]).all()
+
+
+@pytest.mark.parametrize("rank", [8, 24, 64, 136, 256])
+@pytest.mark.parametrize("y", [F32, BF16])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_adapters_with_infinities_in_b(rank, y, in_place):
+    # what the formula gives, from 64 bits: an infinity of t's sign, its
+    # opposite's, NaN where two of them meet and where t is zero; rows whose t
+    # bf16 holds exactly (nothing is left for its second term) among them
+    inf = float("inf")
+    c = Case(70, 264, 136, rank, 3, ids="mixed", y=y, base=y)
+    c.ids[:6] = torch.tensor([1, 1, 1, 0, 2, 1], dtype=torch.int32)
+    c.s[1] = 1.0
+    c.x[0] = 0.0                       # t is zero
+    c.x[1:3] = 0.0
+    c.x[1, 9] = c.x[2, 40] = 1.0       # t is a column of A
+    c.x[5, 7] = inf                    # t is an infinity, of A's sign
+    plain = c.b.clone()
+    c.x[5, 7] = 1.0
+    finite = c.run(in_place).cpu()
+    c.x[5, 7] = inf
+    put = {(0, 3): {0: inf}, (1, 3): {rank - 1: inf}, (1, 4): {5: -inf}, (1, 9): {2: inf, 6: inf},
+           (1, 68): {0: -inf, rank - 1: inf}, (1, 77): {3: float("nan")}, (1, 135): {rank // 2: inf},
+           (2, 0): {1: inf, 4: -inf, 7: 1.0}}
+    hit = torch.zeros((3, 136), dtype=torch.bool)
+    for (i, o), at in put.items():
+        hit[i, o] = True
+        for j, v in at.items():
+            c.b[i, o, j] = v
+    got = c.run(in_place).cpu()
+    # rows and columns without one keep their bits
+    touched = torch.stack([hit[i] if 0 <= i < 3 else torch.zeros(136, dtype=torch.bool)
+                           for i in c.ids.tolist()])
+    touched[5] = True
+    assert torch.equal(got[~touched], finite[~touched])
+    assert torch.equal(plain[~hit], c.b[~hit])
+    count = 0
+    for r, i in enumerate(c.ids.tolist()):
+        if not 0 <= i < 3:
+            continue
+        x, a, b = np64(c.x[r]), np64(c.a[i]), np64(c.b[i])
+        with np.errstate(invalid="ignore"):
+            t = (a * x).sum(1) * float(c.s[i])
+            # t's sign is sure where it is zero exactly or above the sum's error; a
+            # column with an infinity at another rank (one of rank 64 has 1.9e-4, the
+            # error is up to 2.4e-4) is not compared
+            off = 1.01 * (264 + 66) * U * np.abs(a * x).sum(1) * float(c.s[i])
+            sure = (t == 0) & (np.abs(a * x).sum(1) == 0) | (np.abs(t) > off) | np.isinf(t)
+            want = (b * t).sum(1) + np64(c.base[r])
+        for o in np.nonzero(touched[r].numpy())[0]:
+            if not sure[~np.isfinite(b[o])].all():
+                continue
+            if np.isnan(want[o]):
+                assert torch.isnan(got[r, o]), (r, o)
+            elif np.isinf(want[o]):
+                assert got[r, o] == want[o], (r, o, float(got[r, o]), want[o])
+            count += 1
+    assert count >= 136 + 20
