@@ -568,8 +568,9 @@ size_t bfly_lora_matmul_workspace_bytes(int64_t rows, int32_t n_out, int32_t k, 
  *   workspace: >= bfly_grad_clip_workspace_bytes(count) bytes of device
  *            scratch, 16-byte aligned; two calls that may overlap need one each
  * Squares are summed in fp64 in an order that depends on the sizes only.  A
- * norm that is not finite gives factor 1: it is reported in norm[0] and the
- * gradients are left (copied) as they are.  In place with factor 1 nothing is
+ * norm that is not finite in fp32 (also one of finite gradients beyond 3.4e38)
+ * gives factor 1: it is reported in norm[0] and the gradients are left (copied)
+ * as they are.  In place with factor 1 nothing is
  * written to the gradients.  max_norm > 0 (infinity: only the norm).  The
  * pointers need their element's alignment only.  count <= 65536, below 2^42
  * elements in all.  Errors: BFLY_ERR_NULL, BFLY_ERR_SIZE (a negative count or

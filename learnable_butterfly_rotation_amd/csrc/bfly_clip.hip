@@ -217,12 +217,15 @@ __device__ __forceinline__ void square_slot(const ClipTensor* tab, const Slots& 
 }
 
 // The norm and the factor from the sum of squares.  A norm that is not finite
-// scales nothing: it is reported, and the caller drops the step.
+// as it is reported, in fp32, scales nothing: the caller sees it and drops the
+// step.
 __device__ __forceinline__ float factor_of(double squares, float max_norm, float* norm) {
   const double all = sqrt(squares);
-  const float c = all > (double)max_norm && all < __builtin_inf() ? (float)(max_norm / all) : 1.f;
+  const float reported = (float)all;
+  const bool scale = all > (double)max_norm && reported < __builtin_inff();
+  const float c = scale ? (float)(max_norm / all) : 1.f;
   if (norm) {
-    norm[0] = (float)all;
+    norm[0] = reported;
     norm[1] = c;
   }
   return c;

@@ -182,3 +182,33 @@ def test_clip_outputs_that_overlap_other_gradients():
     B.bfly_grad_clip([a, b], 1.0, norm, workspace(2), outs=[a, out])
     assert torch.equal(a, out) and (b == 1).all()
     assert abs(float(a[7]) - 600 ** -0.5) <= 4 * TOL
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("sizes", [[1, 1], [5000, 3, 70001], [9000] * 200, [16 << 20, 16 << 20]],
+                         ids=lambda s: "%dx%d" % (len(s), max(s)))
+def test_clip_norm_beyond_fp32(sizes, dtype):
+    # finite gradients whose norm is not: it is reported as an infinity, with
+    # factor 1, and the gradients stay as they are
+    total = sum(sizes)
+    flat = torch.full((total,), 3e38, device="cuda").to(dtype)
+    flat[1::2] *= -1
+    keep = flat.clone()
+    norm, ws = torch.zeros(2, device="cuda"), workspace(len(sizes))
+    out = torch.zeros_like(flat)
+    for outs in (list(out.split(sizes)), None):
+        norm.zero_()
+        B.bfly_grad_clip(list(flat.split(sizes)), 1.0, norm, ws, outs=outs)
+        assert norm.tolist() == [float("inf"), 1.0]
+        assert torch.equal(flat, keep)
+    assert torch.equal(out, keep)
+
+
+def test_clip_norm_at_the_largest_fp32():
+    # the largest finite norm still scales: the factor 1 / 3.4e38 is a subnormal,
+    # off by 2^-150 at most, 2^-22 of it, and the product by 2^-24
+    g = torch.full((1,), torch.finfo(F32).max, device="cuda")
+    norm = torch.zeros(2, device="cuda")
+    B.bfly_grad_clip([g], 1.0, norm, workspace(1))
+    assert float(norm[0]) == torch.finfo(F32).max and 0 < float(norm[1]) < 3e-39
+    assert abs(float(g[0]) - 1.0) <= (2.0 ** -22 + 2.0 ** -24) * (1 + 1e-3)
