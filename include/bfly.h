@@ -473,7 +473,9 @@ typedef enum {
  * Any n in [1, 16384] (multiples of 8 take the vector path); eps positive and
  * finite.  x, residual, h, weight, y and codes 16-byte aligned.  A row that
  * holds an infinity has rstd = 0; one that holds a NaN has NaN in rstd and y;
- * the codes and scales of such a row are unspecified.  rows == 0 is a no-op.
+ * the codes and scales of such a row are unspecified, and so are those of a
+ * group with a NaN in y.  An infinity in y, by its weight, has code +-top and
+ * scale 65504.  rows == 0 is a no-op.
  * Errors: BFLY_ERR_NULL, BFLY_ERR_DTYPE, BFLY_ERR_SIZE (rows < 0, n < 1, eps
  * not positive and finite), BFLY_ERR_QUANT, BFLY_ERR_ALIGN,
  * BFLY_ERR_UNSUPPORTED (n > 16384), BFLY_ERR_HIP. */

@@ -60,7 +60,8 @@ __device__ __forceinline__ _Float16 group_scale(float amax, float inv_top) {
 // The codes of eight values, four to a word; d the group's scale, r = 1 / d
 // (0 for a zero scale: codes 0).  y / d is the IEEE quotient, as a division
 // gives it: r is the rounded reciprocal and d has 11 bits, so one correction
-// of y r by its exact remainder rounds the quotient correctly (Markstein).
+// of y r by its exact remainder rounds the quotient correctly (Markstein).  y
+// is finite (finite_group).
 template <bool E4M3>
 __device__ __forceinline__ uint2 codes8(const float (&y)[8], float d, float r) {
   constexpr float top = E4M3 ? 448.f : 127.f;
@@ -87,6 +88,17 @@ __device__ __forceinline__ uint2 codes8(const float (&y)[8], float d, float r) {
   }
   const uint32_t any = d > 0.f ? ~0u : 0u;  // a zero scale: no negative zero either
   return make_uint2(w[0] & any, w[1] & any);
+}
+// An infinite y, beyond fp32 by its weight, would have the remainder infinity
+// minus infinity: where the group's maximum says that there is one, the largest
+// number stands for it, whose code is +-top as well.  (4096 rows, one scale
+// each, to e4m3: of 4096 columns 13.9 us without this, 14.2 so, 14.8 with y r
+// held to 2 top in every element; of 11008 34.5, 34.7, 36.4.)
+__device__ __forceinline__ void finite_group(float (&y)[8], float amax) {
+  if (amax < __builtin_inff()) return;
+  constexpr float most = 3.40282347e38f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = __builtin_amdgcn_fmed3f(y[e], -most, most);
 }
 __device__ __forceinline__ float reciprocal(float d) { return d > 0.f ? 1.f / d : 0.f; }
 
@@ -209,6 +221,8 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
         d = (float)s;
         r = reciprocal(d);
         if (first) sc[0] = __builtin_bit_cast(uint16_t, s);
+#pragma unroll
+        for (int v = 0; v < V; ++v) finite_group(h[v], top);
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -217,6 +231,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) norm_kernel(NormParams P) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(h[v][e]));
           m = run_max(m, P.group >> 3);
+          finite_group(h[v], m);
           const _Float16 s = group_scale(m, inv_top);
           d = (float)s;
           r = reciprocal(d);

@@ -345,3 +345,22 @@ def test_backward_against_differences():
         assert abs(num - float((np64(dx) * v).sum())) <= 1e-5 * np.abs(np64(dx) * v).sum() + 1e-6
         num = (loss(np64(h), np64(w) + t * u) - loss(np64(h), np64(w) - t * u)) / (2 * t)
         assert abs(num - float((np64(dw) * u).sum())) <= 1e-5 * np.abs(np64(dw) * u).sum() + 1e-6
+
+
+@pytest.mark.parametrize("n,group", [(100, 100), (128, 16), (520, 520), (1023, 1023), (1024, 64),
+                                     (4096, 4096), (4096, 128), (5120, 512), (11008, 11008),
+                                     (16384, 8), (16383, 16383)])
+@pytest.mark.parametrize("fmt", [B.BFLY_Q8_INT8, B.BFLY_Q8_E4M3])
+@pytest.mark.parametrize("x_dt", [F32, BF16])
+def test_norm_codes_of_a_y_beyond_fp32(n, group, fmt, x_dt):
+    # finite rows and weights whose product is an infinity: its code is +-top
+    # and its group's scale 65504
+    x = rows_of(n + group, 5, n, x_dt)
+    w = 1 + 0.1 * torch.randn(n, generator=torch.Generator().manual_seed(n))
+    w[n // 3::7] = 3e38
+    w[n // 2::11] = -3.4e38
+    with np.errstate(over="ignore"):
+        check_norm(x, None, w, None, fmt, group)
+        r = (x.double().square().mean(1) + EPS) ** -0.5
+        # short rows of a large element stay just below: 2.5e38
+        assert n < 1000 or (x.double() * r[:, None] * w.double()).abs().max() > 3.5e38
