@@ -212,3 +212,19 @@ def test_clip_norm_at_the_largest_fp32():
     B.bfly_grad_clip([g], 1.0, norm, workspace(1))
     assert float(norm[0]) == torch.finfo(F32).max and 0 < float(norm[1]) < 3e-39
     assert abs(float(g[0]) - 1.0) <= (2.0 ** -22 + 2.0 ** -24) * (1 + 1e-3)
+
+
+@pytest.mark.parametrize("count,each", [(5000, 11), (65536, 3), (5000, 5000)])
+def test_clip_thousands_of_tensors(count, each):
+    # 5000 of up to 5000 elements are beyond 56 MiB
+    g = torch.Generator().manual_seed(count)
+    sizes = [each - i % 3 for i in range(count)]
+    flat = torch.randn(sum(sizes), generator=g).cuda()
+    out, norm, ws = torch.zeros_like(flat), torch.zeros(2, device="cuda"), workspace(count)
+    B.bfly_grad_clip(list(flat.split(sizes)), 0.5, norm, ws, outs=list(out.split(sizes)))
+    want = float(flat.double().square().sum().sqrt())
+    assert abs(float(norm[0]) - want) <= TOL * want
+    assert abs(float(norm[1]) - 0.5 / want) <= TOL * 0.5 / want
+    assert torch.equal(out, flat * norm[1])
+    B.bfly_grad_clip(list(flat.split(sizes)), 0.5, norm, ws)
+    assert torch.equal(out, flat)

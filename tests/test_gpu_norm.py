@@ -364,3 +364,34 @@ def test_norm_codes_of_a_y_beyond_fp32(n, group, fmt, x_dt):
         r = (x.double().square().mean(1) + EPS) ** -0.5
         # short rows of a large element stay just below: 2.5e38
         assert n < 1000 or (x.double() * r[:, None] * w.double()).abs().max() > 3.5e38
+
+
+@pytest.mark.parametrize("rows,n", [(131073, 64), (131090, 100), (32769, 520), (32771, 1023),
+                                    (8200, 5120), (8200, 6150), (8200, 11008), (8193, 16384)])
+def test_norm_rows_beyond_the_grid(rows, n):
+    # a workgroup's second turn
+    x, res = rows_of(rows, rows, n, BF16), rows_of(rows + 1, rows, n, BF16)
+    check_norm(x, res, None, BF16, B.BFLY_Q8_INT8, n)
+
+
+@pytest.mark.parametrize("rows", [600, 1025])
+@pytest.mark.parametrize("n", [5120, 8191, 11008, 16384])
+@pytest.mark.parametrize("with_dh", [False, True])
+def test_backward_rows_beyond_the_slots(rows, n, with_dh):
+    check_backward(rows_of(1, rows, n, BF16), None, rows_of(2, rows, n, F32),
+                   rows_of(3, rows, n, F32) if with_dh else None)
+
+
+@pytest.mark.parametrize("into", ["dy", "dh", "h"])
+@pytest.mark.parametrize("rows,n", [(9, 100), (9, 1031), (40, 4096), (600, 5120), (600, 16384)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_backward_into_its_inputs(into, rows, n, dtype):
+    h, dy, dh = (rows_of(k, rows, n, dtype).cuda() for k in (1, 2, 3))
+    rstd = torch.rand(rows, generator=torch.Generator().manual_seed(4)).cuda() + 0.5
+    ws = torch.empty(B.bfly_rmsnorm_backward_workspace_bytes(rows, n), dtype=torch.uint8,
+                     device="cuda")
+    dx, dw, dw2 = torch.empty_like(h), torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    B.bfly_rmsnorm_backward(h, None, rstd, dy, dx, dweight=dw, dh=dh, workspace=ws)
+    to = {"dy": dy, "dh": dh, "h": h}[into]
+    B.bfly_rmsnorm_backward(h, None, rstd, dy, to, dweight=dw2, dh=dh, workspace=ws)
+    assert torch.equal(to, dx) and torch.equal(dw, dw2)
