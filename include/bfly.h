@@ -500,7 +500,7 @@ bfly_status bfly_rmsnorm(const void* x, bfly_dtype x_dt, const void* residual, v
  *   dweight: may be NULL (the workspace is then not used and may be NULL)
  *   workspace: >= bfly_rmsnorm_backward_workspace_bytes(rows, n) bytes of
  *            device scratch, 16-byte aligned; two calls that may overlap need
- *            one each
+ *            one each.  The size never falls with rows
  * dweight's sum has a fixed order that depends on (rows, n) only: the same
  * bits from run to run.  Sizes, alignment and errors as bfly_rmsnorm, plus
  * BFLY_ERR_WORKSPACE. */
@@ -531,7 +531,8 @@ size_t bfly_rmsnorm_backward_workspace_bytes(int64_t rows, int32_t n);
  *             aliasing
  *   workspace: >= bfly_lora_matmul_workspace_bytes(rows, n_out, k, rank)
  *             bytes of device scratch, 16-byte aligned; two calls that may
- *             overlap need one each
+ *             overlap need one each.  The size never falls with rows, k or
+ *             rank: one for the largest call serves the others
  * Rows of one adapter need not lie together.  A_id x is summed in fp32 and
  * enters the second product, times scaling, with 16 bits (bf16 y) or 24 (fp32
  * y); y is rounded once.  In calls of the same sizes a row's result does not

@@ -22,7 +22,8 @@ struct LoraParams {
   int32_t n_out, k, n_adapters, rank;
   int32_t base_bf16, y_bf16;
 };
-// Workspace bytes of a call: a function of the sizes only.
+// Workspace bytes of a call: a function of the sizes only, that never falls
+// with any of them.
 size_t lora_workspace_bytes(int64_t rows, int k, int rank);
 hipError_t launch_lora(const LoraParams& p, hipStream_t s);
 

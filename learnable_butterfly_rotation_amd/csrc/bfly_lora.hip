@@ -839,10 +839,19 @@ void expand_by_rank(const LoraParams& p, const Cut& c, hipStream_t s) {
 
 }  // namespace
 
+// The orders, and t for as many rows as calls of up to `rows` rows can want:
+// more splits than one take 256 workgroups at most, with a tile to 64 rows and
+// one more to 256, so splits * rows <= 256 * 256 / 5 rows of t for every 64
+// ranks, and at most one split to 512 k.  An upper bound that never falls with
+// rows, k or rank, where the splits themselves do (at k = 4096 and rank 64, 2048
+// rows of one adapter take 6 of them and 8192 rows one).
 size_t lora_workspace_bytes(int64_t rows, int k, int rank) {
-  const Cut c = cut(rows, 8, k, 1, rank);  // most splits
-  return (size_t)c.blocks * sizeof(Order) +
-         (size_t)c.splits * (size_t)rows * (size_t)c.stride * sizeof(float);
+  constexpr int64_t kSplitRows = 256 * 256 / 5 + 1;
+  const int64_t stride = (rank + 15) / 16 * 16, most = (k + 511) / 512;
+  const int64_t many = rows * most * stride, cap = kSplitRows * (stride < 64 ? stride : 64);
+  const int64_t split = many < cap ? many : cap, whole = rows * stride;
+  return (size_t)((rows + kBlockRows - 1) / kBlockRows) * sizeof(Order) +
+         (size_t)(split > whole ? split : whole) * sizeof(float);
 }
 
 hipError_t launch_lora(const LoraParams& p, hipStream_t s) {

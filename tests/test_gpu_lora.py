@@ -288,3 +288,22 @@ def test_adapters_with_infinities_in_b(rank, y, in_place):
                 assert got[r, o] == want[o], (r, o, float(got[r, o]), want[o])
             count += 1
     assert count >= 136 + 20
+
+
+@pytest.mark.parametrize("rank", [16, 64, 136])
+def test_one_workspace_for_all_batches(rank):
+    # sized for the most rows, and nothing behind a call's own size is touched
+    k, n_out, most = 4096, 64, 4096
+    ws = torch.empty(B.bfly_lora_matmul_workspace_bytes(most, n_out, k, rank), dtype=torch.uint8,
+                     device="cuda")
+    for rows in (most, 2048, 700, 64, 3):
+        c = Case(rows, k, n_out, rank, 1, ids="0", y=F32)
+        want = c.run()
+        dev = [t.cuda() for t in (c.x, c.ids, c.a, c.b, c.s)]
+        ws.fill_(0x7F)
+        y = torch.empty_like(want)
+        B.bfly_lora_matmul(*dev, y, ws, base=c.base.cuda())
+        assert torch.equal(y, want)
+        assert (ws[B.bfly_lora_matmul_workspace_bytes(rows, n_out, k, rank):] == 0x7F).all()
+        if rows <= 700:
+            c.check(y)

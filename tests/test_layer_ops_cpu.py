@@ -276,3 +276,39 @@ def test_the_tensors_of_adapters_are_checked():
         ext.lora_matmul()
     with pytest.raises(ValueError):
         ext.bind(0, 1, 2, 3)
+
+
+def test_a_workspace_for_the_most_rows_serves_fewer(L):
+    size = B.bfly_lora_matmul_workspace_bytes
+    steps = list(range(1, 4200)) + list(range(4200, 16500, 7)) + [1 << b for b in range(15, 24)]
+    for k, rank in ((4096, 64), (65536, 8), (65536, 256), (8, 8), (1000, 16), (4096, 24),
+                    (11008, 40), (4096, 72), (512, 128), (11008, 200)):
+        sizes = [size(r, 4096, k, rank) for r in steps]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), (k, rank)
+        # and one for the longest rows or the highest rank
+        assert all(size(r, 8, k, rank) <= size(r, 8, min(65536, 2 * k), rank) and
+                   size(r, 8, k, rank) <= size(r, 8, k, min(256, rank + 8)) for r in steps[::17])
+    # a call with the size for the most rows passes its check, one with a byte less does not
+    need = size(4096, 256, 4096, 64)
+    for rows in (1, 64, 300, 2048, 2700, 4096):
+        assert lora(L, rows=rows, k=4096, rank=64, wsb=need, ids=0x10002) == ALIGN
+    assert lora(L, rows=4096, k=4096, rank=64, wsb=need - 1, ids=0x10002) == WORKSPACE
+    for n in (16, 128, 129, 1024, 1025, 4095, 4096, 16384):
+        sizes = [B.bfly_rmsnorm_backward_workspace_bytes(r, n) for r in steps]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), n
+    sizes = [B.bfly_grad_clip_workspace_bytes(c) for c in range(0, 65537, 13)]
+    assert all(a < b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_the_adapters_workspace_holds_their_sums():
+    # how a call is cut up, by itself: 1552 bytes of order to a block of 256 rows,
+    # and the splits' fp32 sums of t in rows of a multiple of 16 ranks
+    for rows in list(range(1, 700)) + list(range(700, 20000, 97)):
+        blocks, tiles = -(-rows // 256), -(-rows // 64)
+        for k in (8, 520, 4096, 11008, 65536):
+            for rank in (8, 16, 24, 32, 40, 64, 72, 128, 136, 192, 200, 256):
+                ways = -(-rank // (16 if rank <= 16 else 32 if rank <= 32 else 64))
+                splits = max(1, min(256 // ((tiles + blocks) * ways), -(-k // 512)))
+                run = -(-(-(-k // splits)) // 128) * 128
+                need = 1552 * blocks + 4 * -(-k // run) * rows * -(-rank // 16) * 16
+                assert B.bfly_lora_matmul_workspace_bytes(rows, 64, k, rank) >= need
