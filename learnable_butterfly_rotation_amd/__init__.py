@@ -418,9 +418,10 @@ def bfly_rmsnorm(x, weight, eps, y=None, codes=None, scales=None, residual=None,
                  format=BFLY_Q8_INT8, group=None, stream=None) -> None:
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight per row, and y
     in 8 bits.  x, residual, h: [rows, n] of one type; y: [rows, n] float32 or
-    bfloat16; codes: [rows, n] of one byte an element with scales [rows,
-    n/group] float16 (group None: one scale per row); rstd: [rows] float32;
-    weight: [n] or None (ones).  Outputs that are None are not computed."""
+    bfloat16; codes: [rows, n] uint8 (or int8 for BFLY_Q8_INT8, float8_e4m3fn
+    for BFLY_Q8_E4M3) with scales [rows, n/group] float16 (group None: one
+    scale per row); rstd: [rows] float32; weight: [n] or None (ones).  Outputs
+    that are None are not computed."""
     _call(_ext().rmsnorm, x, stream, eps, format, group, x, weight, y, codes, scales, residual, h,
           rstd)
 

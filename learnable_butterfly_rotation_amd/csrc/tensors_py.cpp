@@ -36,15 +36,16 @@ template <typename... T>
 }
 
 // The types that a tensor may have, as bits.
-constexpr int kF32 = 1, kBF16 = 2, kF16 = 4, kBytes = 8, kI32 = 16, kRows = kF32 | kBF16;
+constexpr int kF32 = 1, kBF16 = 2, kF16 = 4, kBytes = 8, kI32 = 16, kI8 = 32, kE4M3 = 64,
+              kRows = kF32 | kBF16;
 int kind_of(at::ScalarType s) {
   switch (s) {
     case at::kFloat: return kF32;
     case at::kBFloat16: return kBF16;
     case at::kHalf: return kF16;
-    case at::kChar:
-    case at::kByte:
-    case at::kFloat8_e4m3fn: return kBytes;
+    case at::kByte: return kBytes;
+    case at::kChar: return kI8;
+    case at::kFloat8_e4m3fn: return kE4M3;
     case at::kInt: return kI32;
     default: return 0;
   }
@@ -174,7 +175,9 @@ PyObject* rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t count) {
     const int same = kind_of(x->scalar_type());
     const at::Tensor* const weight = a.tensor("weight", kRows, {n});
     const at::Tensor* const y = a.tensor("y", kRows, {rows, n});
-    void* const codes = a.at("codes", kBytes, {rows, n});
+    // uint8 holds the bytes of either format, a type that names one only its own
+    const int named = format == BFLY_Q8_E4M3 ? kE4M3 : kI8;
+    void* const codes = a.at("codes", kBytes | named, {rows, n});
     if (by_row || !codes) group = width;
     void* const scales = a.at("scales", kF16, {rows, group > 0 ? n / group : 0});
     const void* const residual = a.at("residual", same, {rows, n});

@@ -312,3 +312,18 @@ def test_the_adapters_workspace_holds_their_sums():
                 run = -(-(-(-k // splits)) // 128) * 128
                 need = 1552 * blocks + 4 * -(-k // run) * rows * -(-rank // 16) * 16
                 assert B.bfly_lora_matmul_workspace_bytes(rows, 64, k, rank) >= need
+
+
+def test_codes_of_a_type_that_names_another_format_are_refused():
+    ext, x = extension(), torch.zeros((3, 64))
+    v, i8 = torch.zeros(3), torch.zeros((3, 64), dtype=torch.int8)
+    scales = torch.zeros((3, 1), dtype=torch.float16)
+    call = lambda codes, fmt, error: refused(ext.rmsnorm, 1e-5, fmt, None, x, None, None, codes,
+                                             scales, None, None, v, error=error)
+    e4m3, u8 = i8.view(torch.float8_e4m3fn), i8.view(torch.uint8)
+    call(e4m3, B.BFLY_Q8_INT8, TypeError)
+    call(i8, B.BFLY_Q8_E4M3, TypeError)
+    # what names the format, and bytes for either, stop at the GPU they are not on
+    for codes, fmt in ((i8, B.BFLY_Q8_INT8), (e4m3, B.BFLY_Q8_E4M3), (u8, B.BFLY_Q8_INT8),
+                       (u8, B.BFLY_Q8_E4M3)):
+        call(codes, fmt, ValueError)
