@@ -501,7 +501,8 @@ bfly_status bfly_rmsnorm(const void* x, bfly_dtype x_dt, const void* residual, v
  *   workspace: >= bfly_rmsnorm_backward_workspace_bytes(rows, n) bytes of
  *            device scratch, 16-byte aligned; two calls that may overlap need
  *            one each.  The size never falls with rows
- * dweight's sum has a fixed order that depends on (rows, n) only: the same
+ * dweight's sum is held in fp32 (a thread's over its rows, a workgroup's, the
+ * workspace's) and has a fixed order that depends on (rows, n) only: the same
  * bits from run to run.  Sizes, alignment and errors as bfly_rmsnorm, plus
  * BFLY_ERR_WORKSPACE. */
 bfly_status bfly_rmsnorm_backward(const void* h, bfly_dtype h_dt, const void* weight,
@@ -570,7 +571,8 @@ size_t bfly_lora_matmul_workspace_bytes(int64_t rows, int32_t n_out, int32_t k, 
  *   norm   : device fp32 [2], receives the norm and the factor
  *   workspace: >= bfly_grad_clip_workspace_bytes(count) bytes of device
  *            scratch, 16-byte aligned; two calls that may overlap need one each
- * Squares are summed in fp64 in an order that depends on the sizes only.  A
+ * Squares are summed in fp64 in an order that depends on the sizes, the types
+ * and where the tensors start within 16 bytes only.  A
  * norm that is not finite in fp32 (also one of finite gradients beyond 3.4e38)
  * gives factor 1: it is reported in norm[0] and the gradients are left (copied)
  * as they are.  In place with factor 1 nothing is

@@ -1,10 +1,11 @@
 """learnable_butterfly_rotation_amd -- MI355X (gfx950) learnable butterfly
 rotation fused with round-to-nearest group quantization.
 
-Thin ctypes binding over the C ABI of ``libbfly.so`` (include/bfly.h).  The
-functions carry the C names; they only marshal torch tensors into pointers,
-sizes and the current HIP stream -- every step of the computation runs in the
-library's HIP kernels.  There is no CPU fallback: if the library is missing
+Binding over the C ABI of ``libbfly.so`` (include/bfly.h): through ctypes, and
+for the norm, the adapters and the clipping through the native extension
+``_tensors``.  The functions carry the C names; they only check torch tensors
+and marshal them into pointers, sizes and the current HIP stream -- every step
+of the computation runs in the library's HIP kernels.  There is no CPU fallback: if the library is missing
 or no GPU is present the calls raise.
 
 Build the library with ``python -m learnable_butterfly_rotation_amd.build``.

@@ -489,7 +489,8 @@ hipError_t norm_bwd_run(const NormBwdParams& p, hipStream_t s) {
 // adding them costs 16384 x 5120 fp32 6 us at 256 slots and 18 at 1024
 // (182 and 194 us in all), while narrow rows need the workgroups to have
 // enough loads in flight.  With many rows more of them, so that a thread's
-// fp32 sum goes over about 128 rows.  A single one for two or three groups of
+// fp32 sum goes over about 128 rows, up to 2048 slots: beyond 262144 groups of
+// rows it grows with them (540000 x 4096: 264 rows).  A single one for two or three groups of
 // rows: it is the sum already, and a launch less (3 rows of 4096: 4.6 us in a
 // graph for 5.3, but 4 rows 5.4; 2 rows of 11008 5.7 for 6.6, 3 rows 7.0).
 int rmsnorm_bwd_slots(int64_t rows, int n) {
