@@ -307,3 +307,21 @@ def test_one_workspace_for_all_batches(rank):
         assert (ws[B.bfly_lora_matmul_workspace_bytes(rows, n_out, k, rank):] == 0x7F).all()
         if rows <= 700:
             c.check(y)
+
+
+@pytest.mark.parametrize("rank", [8, 40, 72, 256])
+@pytest.mark.parametrize("y", [F32, BF16])
+def test_adapters_of_nothing_but_infinities_or_nan(rank, y):
+    c = Case(300, 264, 136, rank, 4, y=y)
+    c.x, c.a = c.x.abs() + 0.01, c.a.abs() + 0.01   # t is positive
+    finite = c.run().cpu()
+    c.b[1], c.b[2] = float("inf"), float("nan")
+    c.b[3] = -float("inf")
+    c.b[3, ::2, rank - 1] = float("inf")
+    got = c.run().cpu()
+    keep = (c.ids != 1) & (c.ids != 2) & (c.ids != 3)
+    assert torch.equal(got[keep], finite[keep])
+    assert (got[c.ids == 1] == float("inf")).all() and torch.isnan(got[c.ids == 2]).all()
+    assert torch.isnan(got[c.ids == 3][:, ::2]).all()
+    assert (got[c.ids == 3][:, 1::2] == -float("inf")).all()
+    assert all((c.ids == i).any() for i in range(4))
