@@ -31,6 +31,8 @@
  *   bfly_rmsnorm, bfly_rmsnorm_backward          the norm in front of a rotated layer
  *   bfly_lora_matmul                             low-rank adapters beside a product
  *   bfly_grad_clip                               global gradient norm and clipping
+ *   bfly_cache_write, bfly_cache_read            a paged key-value cache in few bits
+ *   bfly_cache_attention                         one new token per sequence over it
  *   bfly_*_bytes, bfly_status_string, bfly_last_hip_error
  *   bfly_forward_quant_noalloc                   bfly_forward_quant with a fixed scratch
  *   bfly_time_next_forward                       kernel-only timing of the next forward
@@ -587,6 +589,129 @@ bfly_status bfly_grad_clip(int32_t count, const void* const* grads, void* const*
                            void* hip_stream);
 
 size_t bfly_grad_clip_workspace_bytes(int32_t count);
+
+/* ---- a paged key-value cache in few bits ------------------------------------- */
+
+/* How the rows of a cache are held.  A row is one head's key (or value) of one
+ * token, head_dim elements; it has one scale, an fp16 bit pattern:
+ *   scale = fp16(max |x| / top),  code = rnd(x / scale) clamped to +-top,
+ * round to nearest, ties to even, both from the exact quotients; a scale above
+ * 65504 saturates, a zero scale gives zero codes.
+ *   BFLY_KV_BF16 : bf16(x), no scale
+ *   BFLY_KV_INT8 : top = 127, two's-complement bytes
+ *   BFLY_KV_E4M3 : top = 448, OCP 8-bit floats
+ *   BFLY_KV_INT4 : top = 7, two's complement, element 2i in the low half of
+ *                  byte i (as the codes of bfly_forward_quant)
+ * With queries and keys rotated alike (bfly_forward over their heads: n =
+ * head_dim), q . k is what it was and a key's outliers are spread over its row
+ * before it is cut to few bits. */
+typedef enum {
+    BFLY_KV_BF16 = 0,
+    BFLY_KV_INT8 = 1,
+    BFLY_KV_E4M3 = 2,
+    BFLY_KV_INT4 = 3,
+    BFLY_KV_RANGE_LOW_ = -2147483647 - 1,
+    BFLY_KV_RANGE_HIGH_ = 2147483647
+} bfly_kv;
+
+/* A cache is four arrays of the caller:
+ *   k_cache, v_cache  : [pages][kv_heads][page_size] rows of head_dim elements
+ *                       (2, 1, 1 or 1/2 byte each)
+ *   k_scales, v_scales: fp16 [pages][kv_heads][page_size] (not looked at for
+ *                       BFLY_KV_BF16)
+ * A slot is the place of one token, page * page_size + place in the page.
+ * Sizes: head_dim 64, 128 or 256; page_size a power of two from 16 to 65536;
+ * kv_heads <= 4096; pages * page_size < 2^31.  k_cache and v_cache 16-byte
+ * aligned, scales 2-byte.
+ *
+ * bfly_cache_write: the keys and values of `tokens` tokens into their slots.
+ *   k, v    : [tokens] rows of kv_heads * head_dim elements of dt, k_stride
+ *             and v_stride elements apart (at least a row, multiples of 8:
+ *             parts of a projection's output are taken as they lie), 16-byte
+ *             aligned
+ *   slots   : int32 [tokens]; a token whose slot is outside
+ *             [0, pages * page_size) is left out (padded rows: -1).  The
+ *             others are distinct: of a slot given twice, what it holds
+ *             afterwards is unspecified (no other slot is touched)
+ * Slots that are not given keep what they hold.  A row with a NaN gets scale
+ * NaN and codes 0 and reads back as NaN; an infinity has code +-top and scale
+ * 65504.  tokens == 0 is a no-op.
+ *
+ * bfly_cache_read: k and v receive code * scale of the given slots, rounded
+ * once to dt; a token whose slot is outside the cache gets zeros.  Slots may
+ * be given any number of times.  k and v share no memory with each other or
+ * the cache.
+ *
+ * Errors of both: BFLY_ERR_NULL, BFLY_ERR_DTYPE, BFLY_ERR_QUANT (format),
+ * BFLY_ERR_SIZE (tokens < 0, another size below 1, a stride below a row),
+ * BFLY_ERR_UNSUPPORTED, BFLY_ERR_ALIGN, BFLY_ERR_HIP. */
+bfly_status bfly_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             bfly_dtype dt, const int32_t* slots, int64_t tokens, void* k_cache,
+                             void* v_cache, uint16_t* k_scales, uint16_t* v_scales, int32_t pages,
+                             int32_t kv_heads, int32_t page_size, int32_t head_dim, bfly_kv format,
+                             void* hip_stream);
+
+bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint16_t* k_scales,
+                            const uint16_t* v_scales, const int32_t* slots, int64_t tokens,
+                            void* k, int64_t k_stride, void* v, int64_t v_stride, bfly_dtype dt,
+                            int32_t pages, int32_t kv_heads, int32_t page_size, int32_t head_dim,
+                            bfly_kv format, void* hip_stream);
+
+/* Attention of one new token per sequence over its part of the cache:
+ *   s_t = scale * q . k_t,  y = sum_t e^(s_t) v_t / sum_t e^(s_t)
+ * over the tokens t in reach, k_t and v_t the cache's rows (code * scale).
+ * Query head h reads key-value head h / (heads / kv_heads).
+ *   q       : [rows] rows of heads * head_dim elements of q_dt, q_stride
+ *             elements apart (at least a row, a multiple of 8)
+ *   tables  : int32 [rows][table_width]; entry i is the page of tokens
+ *             i * page_size ... of the row's sequence.  Sequences may share
+ *             pages
+ *   lens    : int32 [rows], the tokens of each sequence, the new one included
+ *             (write it first); below 0 counts as 0, above max_len as max_len.
+ *             Table entries behind them are not read
+ *   window  : the last `window` of them are in reach, all for 0
+ *   max_len : a bound of the lengths, at most table_width * page_size, that
+ *             sizes the launch and the workspace: the closer it is, the better
+ *             the work is spread
+ *   y       : [rows][heads][head_dim] of y_dt, rounded once
+ *   lse     : fp32 [rows][heads], log(sum_t e^(s_t)) (it joins this result
+ *             with one over other tokens), or NULL
+ *   workspace: >= bfly_cache_attention_workspace_bytes(rows, heads, kv_heads,
+ *             head_dim, max_len) bytes of device scratch, 16-byte aligned (0:
+ *             may be NULL); what it holds does not matter; two calls that may
+ *             overlap need one each.  The size never falls with rows, heads,
+ *             head_dim or max_len: one for the largest call serves the others
+ * Tokens whose table entry is outside [0, pages) are out of reach.  A row with
+ * nothing in reach gives y = 0 and lse = -infinity, and so does one all of
+ * whose scores are -infinity.  What lies in a page behind a sequence's tokens
+ * has no influence, whatever its bits are.  A NaN in q, or in a row in reach,
+ * gives NaN in the results that use it and no others; an infinite q counts as
+ * a NaN.
+ * The sums are held in fp32.  With bf16 q and y the weights e^(s - m) enter the
+ * second product with 11 bits (quantized caches) or 16 (BFLY_KV_BF16); with an
+ * fp32 q or y both products take 22 bits (24) of q and of the weights.  In
+ * calls of the same sizes a row's result does not depend on the other rows',
+ * and is the same from run to run.
+ * y and lse share no memory with anything else.
+ * Sizes as above, and heads a multiple of kv_heads up to 65536, rows <= 2^24,
+ * rows * heads <= 2^28, max_len <= 2^30.  q and y 16-byte aligned, tables, lens
+ * and lse 4.  rows == 0 is a no-op.
+ * Errors: BFLY_ERR_NULL, BFLY_ERR_DTYPE, BFLY_ERR_QUANT (format), BFLY_ERR_SIZE
+ * (also: heads not a multiple of kv_heads, max_len beyond the tables, scale not
+ * finite, window < 0), BFLY_ERR_UNSUPPORTED, BFLY_ERR_WORKSPACE,
+ * BFLY_ERR_ALIGN, BFLY_ERR_HIP. */
+bfly_status bfly_cache_attention(const void* q, int64_t q_stride, bfly_dtype q_dt,
+                                 const void* k_cache, const void* v_cache,
+                                 const uint16_t* k_scales, const uint16_t* v_scales,
+                                 const int32_t* tables, int32_t table_width, const int32_t* lens,
+                                 void* y, bfly_dtype y_dt, float* lse, int64_t rows, int32_t heads,
+                                 int32_t pages, int32_t kv_heads, int32_t page_size,
+                                 int32_t head_dim, bfly_kv format, float scale, int32_t max_len,
+                                 int32_t window, void* workspace, size_t workspace_bytes,
+                                 void* hip_stream);
+
+size_t bfly_cache_attention_workspace_bytes(int64_t rows, int32_t heads, int32_t kv_heads,
+                                            int32_t head_dim, int32_t max_len);
 
 /* ---- diagnostics -------------------------------------------------------- */
 

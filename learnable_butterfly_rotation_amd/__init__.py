@@ -2,8 +2,8 @@
 rotation fused with round-to-nearest group quantization.
 
 Binding over the C ABI of ``libbfly.so`` (include/bfly.h): through ctypes, and
-for the norm, the adapters and the clipping through the native extension
-``_tensors``.  The functions carry the C names; they only check torch tensors
+for the norm, the adapters, the clipping and the cache through the native
+extension ``_tensors``.  The functions carry the C names; they only check torch tensors
 and marshal them into pointers, sizes and the current HIP stream -- every step
 of the computation runs in the library's HIP kernels.  There is no CPU fallback: if the library is missing
 or no GPU is present the calls raise.
@@ -29,6 +29,8 @@ __all__ = [
     "BFLY_Q8_INT8", "BFLY_Q8_E4M3", "bfly_rmsnorm", "bfly_rmsnorm_backward",
     "bfly_rmsnorm_backward_workspace_bytes", "bfly_lora_matmul",
     "bfly_lora_matmul_workspace_bytes", "bfly_grad_clip", "bfly_grad_clip_workspace_bytes",
+    "BFLY_KV_BF16", "BFLY_KV_INT8", "BFLY_KV_E4M3", "BFLY_KV_INT4", "bfly_cache_write",
+    "bfly_cache_read", "bfly_cache_attention", "bfly_cache_attention_workspace_bytes",
 ]
 
 BFLY_F32 = 0
@@ -37,6 +39,10 @@ BFLY_SYM_ABSMAX = 0
 BFLY_ASYM_MINMAX = 1
 BFLY_Q8_INT8 = 0
 BFLY_Q8_E4M3 = 1
+BFLY_KV_BF16 = 0
+BFLY_KV_INT8 = 1
+BFLY_KV_E4M3 = 2
+BFLY_KV_INT4 = 3
 
 STATUS_NAMES = {0: "BFLY_OK", 1: "BFLY_ERR_NULL", 2: "BFLY_ERR_SIZE", 3: "BFLY_ERR_DTYPE",
                 4: "BFLY_ERR_ALIGN", 5: "BFLY_ERR_QUANT", 6: "BFLY_ERR_WORKSPACE",
@@ -119,7 +125,17 @@ def lib():
         L.bfly_grad_clip.argtypes = [i32, vp, vp, vp, vp, f32, vp, vp, sz, vp]
         L.bfly_grad_clip_workspace_bytes.argtypes = [i32]
         L.bfly_grad_clip_workspace_bytes.restype = sz
-        for f in (L.bfly_rmsnorm, L.bfly_rmsnorm_backward, L.bfly_lora_matmul, L.bfly_grad_clip,
+        L.bfly_cache_write.argtypes = [vp, i64, vp, i64, ci, vp, i64, vp, vp, vp, vp, i32, i32, i32,
+                                       i32, ci, vp]
+        L.bfly_cache_read.argtypes = [vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, ci, i32, i32, i32,
+                                      i32, ci, vp]
+        L.bfly_cache_attention.argtypes = [vp, i64, ci, vp, vp, vp, vp, vp, i32, vp, vp, ci, vp,
+                                           i64, i32, i32, i32, i32, i32, ci, f32, i32, i32, vp, sz,
+                                           vp]
+        L.bfly_cache_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+        L.bfly_cache_attention_workspace_bytes.restype = sz
+        for f in (L.bfly_cache_write, L.bfly_cache_read, L.bfly_cache_attention,
+                  L.bfly_rmsnorm, L.bfly_rmsnorm_backward, L.bfly_lora_matmul, L.bfly_grad_clip,
                   L.bfly_prepare, L.bfly_prepare_hadamard, L.bfly_forward, L.bfly_forward_quant,
                   L.bfly_forward_quant_noalloc,
                   L.bfly_kron_forward, L.bfly_kron_forward_wide, L.bfly_quant_matmul,
@@ -186,9 +202,9 @@ _extension = _torch = None
 
 
 def _ext():
-    """The extension that takes the tensors of the norm, the adapters and the
-    clipping: it checks that they are contiguous, of the right types and
-    shapes and on one GPU, or raises, and gives the library's status."""
+    """The extension that takes the tensors of the norm, the adapters, the
+    clipping and the cache: it checks that they are contiguous, of the right
+    types and shapes and on one GPU, or raises, and gives the library's status."""
     global _extension, _torch
     if _extension is None:
         import importlib
@@ -201,6 +217,8 @@ def _ext():
         L = lib()
         ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             L.bfly_rmsnorm, L.bfly_rmsnorm_backward, L.bfly_lora_matmul, L.bfly_grad_clip)))
+        ext.bind_cache(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.bfly_cache_write, L.bfly_cache_read, L.bfly_cache_attention)))
         _torch, _extension = torch, ext
     return _extension
 
@@ -467,3 +485,54 @@ def bfly_grad_clip(grads, max_norm, norm, workspace, outs=None, stream=None) -> 
     two of the tensors that are written may overlap, nor an output a gradient
     other than its own."""
     _call(_ext().grad_clip, norm, stream, max_norm, norm, workspace, grads, outs)
+
+
+# ---------------------------------------------------------------------------
+# a paged key-value cache in few bits
+# ---------------------------------------------------------------------------
+
+def bfly_cache_write(k, v, slots, k_cache, v_cache, k_scales=None, v_scales=None,
+                     stream=None) -> None:
+    """The keys and values of tokens into their slots (page * page_size +
+    place; outside the cache: left out) of a paged cache, quantized.  k, v:
+    [tokens, kv_heads, head_dim] of one type, float32 or bfloat16, a token's
+    heads contiguous (views into a projection's output are taken as they are);
+    slots: [tokens] int32; k_cache, v_cache: [pages, kv_heads, page_size,
+    head_dim] bfloat16, int8 or float8_e4m3fn, or uint8 [..., head_dim / 2] for
+    two 4-bit codes to a byte; k_scales, v_scales: [pages, kv_heads, page_size]
+    float16 (None for bfloat16)."""
+    _call(_ext().cache_write, k, stream, k_cache, v_cache, k_scales, v_scales, k, v, slots)
+
+
+def bfly_cache_read(k_cache, v_cache, slots, k, v, k_scales=None, v_scales=None,
+                    stream=None) -> None:
+    """k, v <- what the given slots of a cache hold (zeros for a slot outside
+    it); the tensors as in bfly_cache_write."""
+    _call(_ext().cache_read, k, stream, k_cache, v_cache, k_scales, v_scales, k, v, slots)
+
+
+def bfly_cache_attention_workspace_bytes(rows: int, heads: int, kv_heads: int, head_dim: int,
+                                         max_len: int) -> int:
+    return lib().bfly_cache_attention_workspace_bytes(rows, heads, kv_heads, head_dim, max_len)
+
+
+def bfly_cache_attention(q, k_cache, v_cache, tables, lens, y, k_scales=None, v_scales=None,
+                         scale=None, max_len=None, window=0, lse=None, workspace=None,
+                         stream=None) -> None:
+    """y = sum_t softmax_t(scale * q . k_t) v_t for one new token per sequence
+    over the tokens of a paged cache.  q: [rows, heads, head_dim] float32 or
+    bfloat16, a row's heads contiguous; the cache as in bfly_cache_write;
+    tables: [rows, width] int32 pages; lens: [rows] int32 tokens (0: y = 0); y:
+    [rows, heads, head_dim] float32 or bfloat16; scale None: head_dim ** -0.5;
+    max_len: a bound of the lengths (None: what the tables can hold); window:
+    only the last so many tokens (0: all); lse: [rows, heads] float32 or None,
+    the logarithm of the weights' sum; workspace: a uint8 tensor of
+    bfly_cache_attention_workspace_bytes (None: a fresh one)."""
+    if workspace is None:
+        import torch
+        reach = tables.shape[1] * k_cache.shape[2] if max_len is None else max_len
+        nbytes = bfly_cache_attention_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[1],
+                                                      q.shape[2], reach)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    _call(_ext().cache_attention, q, stream, scale, max_len, window, k_cache, v_cache, k_scales,
+          v_scales, q, tables, lens, y, lse, workspace)

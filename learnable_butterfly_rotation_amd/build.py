@@ -31,7 +31,9 @@ SOURCES = [("bfly_api.hip", "bfly_api.o", []), ("bfly_bwd.hip", "bfly_bwd.o", []
            # these say what a NaN does: their comparisons have to honour it
            ("bfly_norm.hip", "bfly_norm.o", ["-fhonor-nans"]),
            ("bfly_clip.hip", "bfly_clip.o", ["-fhonor-nans"]),
-           ("bfly_lora.hip", "bfly_lora.o", ["-fhonor-nans"])] + \
+           ("bfly_lora.hip", "bfly_lora.o", ["-fhonor-nans"]),
+           ("bfly_cache.hip", "bfly_cache.o", ["-fhonor-nans"]),
+           ("bfly_attend.hip", "bfly_attend.o", ["-fhonor-nans"])] + \
           [("bfly_fwd_kron.hip", "bfly_fwd_kron_m%d.o" % m, ["-DKRON_M=%d" % m]) for m in range(2, 9)]
 
 FLAGS = [

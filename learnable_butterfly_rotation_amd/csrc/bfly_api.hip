@@ -12,6 +12,7 @@
 #include "bfly_common.h"
 #include "bfly_calib.h"
 #include "bfly_calib_w.h"
+#include "bfly_cache.h"
 #include "bfly_clip.h"
 #include "bfly_lora.h"
 #include "bfly_norm.h"
@@ -1108,6 +1109,175 @@ bfly_status bfly_grad_clip(int32_t count, const void* const* grads, void* const*
   p.norm = norm;
   p.workspace = workspace;
   const hipError_t e = bfly::launch_grad_clip(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? BFLY_OK : hip_fail(e);
+}
+
+// The sizes that the calls on a cache share.
+static bfly_status cache_sizes(int32_t pages, int32_t kv_heads, int32_t page_size,
+                               int32_t head_dim) {
+  if (pages < 1 || kv_heads < 1 || page_size < 1 || head_dim < 1) return BFLY_ERR_SIZE;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return BFLY_ERR_UNSUPPORTED;
+  if (page_size < 16 || page_size > bfly::kCacheMaxPage || log2_pow2(page_size) < 0 ||
+      kv_heads > 4096 || (int64_t)pages * page_size > INT32_MAX ||
+      !rows_fit((int64_t)pages * page_size, kv_heads * head_dim))
+    return BFLY_ERR_UNSUPPORTED;
+  return BFLY_OK;
+}
+static bool kv_ok(int32_t format) { return format >= BFLY_KV_BF16 && format <= BFLY_KV_INT4; }
+
+// bfly_cache_write's and bfly_cache_read's arguments into p.
+static bfly_status cache_args(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              bfly_dtype dt, const int32_t* slots, int64_t tokens,
+                              const void* k_cache, const void* v_cache, const uint16_t* k_scales,
+                              const uint16_t* v_scales, int32_t pages, int32_t kv_heads,
+                              int32_t page_size, int32_t head_dim, bfly_kv format,
+                              bfly::CacheParams* p) {
+  if (tokens > 0) {
+    if (!k || !v || !slots || !k_cache || !v_cache) return BFLY_ERR_NULL;
+    if (format != BFLY_KV_BF16 && (!k_scales || !v_scales)) return BFLY_ERR_NULL;
+  }
+  if (!dtype_ok(dt)) return BFLY_ERR_DTYPE;
+  if (!kv_ok(format)) return BFLY_ERR_QUANT;
+  if (tokens < 0) return BFLY_ERR_SIZE;
+  const bfly_status st = cache_sizes(pages, kv_heads, page_size, head_dim);
+  if (st != BFLY_OK) return st;
+  const int64_t row = (int64_t)kv_heads * head_dim;
+  if (k_stride < row || v_stride < row) return BFLY_ERR_SIZE;
+  if (k_stride > INT32_MAX || v_stride > INT32_MAX || tokens > (int64_t(1) << 31) / kv_heads ||
+      !rows_fit(tokens, (int32_t)k_stride) || !rows_fit(tokens, (int32_t)v_stride))
+    return BFLY_ERR_UNSUPPORTED;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+      !aligned(slots, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scales, 2) || !aligned(v_scales, 2))
+    return BFLY_ERR_ALIGN;
+  p->k = k;
+  p->v = v;
+  p->k_stride = k_stride;
+  p->v_stride = v_stride;
+  p->k_cache = const_cast<void*>(k_cache);
+  p->v_cache = const_cast<void*>(v_cache);
+  p->k_scales = const_cast<uint16_t*>(k_scales);
+  p->v_scales = const_cast<uint16_t*>(v_scales);
+  p->slots = slots;
+  p->tokens = tokens;
+  p->pages = pages;
+  p->kv_heads = kv_heads;
+  p->page_shift = log2_pow2(page_size);
+  p->head_dim = head_dim;
+  p->format = format;
+  p->x_bf16 = dt == BFLY_BF16;
+  return BFLY_OK;
+}
+
+bfly_status bfly_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             bfly_dtype dt, const int32_t* slots, int64_t tokens, void* k_cache,
+                             void* v_cache, uint16_t* k_scales, uint16_t* v_scales, int32_t pages,
+                             int32_t kv_heads, int32_t page_size, int32_t head_dim, bfly_kv format,
+                             void* hip_stream) {
+  bfly::CacheParams p;
+  const bfly_status st = cache_args(k, k_stride, v, v_stride, dt, slots, tokens, k_cache, v_cache,
+                                    k_scales, v_scales, pages, kv_heads, page_size, head_dim,
+                                    format, &p);
+  if (st != BFLY_OK || tokens == 0) return st;
+  const hipError_t e = bfly::launch_cache_write(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? BFLY_OK : hip_fail(e);
+}
+
+bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint16_t* k_scales,
+                            const uint16_t* v_scales, const int32_t* slots, int64_t tokens,
+                            void* k, int64_t k_stride, void* v, int64_t v_stride, bfly_dtype dt,
+                            int32_t pages, int32_t kv_heads, int32_t page_size, int32_t head_dim,
+                            bfly_kv format, void* hip_stream) {
+  bfly::CacheParams p;
+  const bfly_status st = cache_args(k, k_stride, v, v_stride, dt, slots, tokens, k_cache, v_cache,
+                                    k_scales, v_scales, pages, kv_heads, page_size, head_dim,
+                                    format, &p);
+  if (st != BFLY_OK || tokens == 0) return st;
+  const hipError_t e = bfly::launch_cache_read(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? BFLY_OK : hip_fail(e);
+}
+
+// By the bits: comparisons of a NaN mean nothing in this file's compilation.
+static bool finite_bits(float v) {
+  uint32_t bits;
+  memcpy(&bits, &v, sizeof(bits));
+  return (bits & 0x7F800000u) != 0x7F800000u;
+}
+
+static bfly_status attend_sizes(int64_t rows, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                int32_t max_len) {
+  if (rows < 0 || heads < 1 || kv_heads < 1 || head_dim < 1 || max_len < 1 || heads % kv_heads != 0)
+    return BFLY_ERR_SIZE;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return BFLY_ERR_UNSUPPORTED;
+  if (heads > 65536 || kv_heads > 4096 || rows > (int64_t(1) << 24) ||
+      rows * heads > (int64_t(1) << 28) || max_len > (1 << 30))
+    return BFLY_ERR_UNSUPPORTED;
+  return BFLY_OK;
+}
+
+size_t bfly_cache_attention_workspace_bytes(int64_t rows, int32_t heads, int32_t kv_heads,
+                                            int32_t head_dim, int32_t max_len) {
+  if (attend_sizes(rows, heads, kv_heads, head_dim, max_len) != BFLY_OK || rows == 0) return 0;
+  return bfly::attend_workspace_bytes(rows, heads, head_dim, max_len);
+}
+
+bfly_status bfly_cache_attention(const void* q, int64_t q_stride, bfly_dtype q_dt,
+                                 const void* k_cache, const void* v_cache,
+                                 const uint16_t* k_scales, const uint16_t* v_scales,
+                                 const int32_t* tables, int32_t table_width, const int32_t* lens,
+                                 void* y, bfly_dtype y_dt, float* lse, int64_t rows, int32_t heads,
+                                 int32_t pages, int32_t kv_heads, int32_t page_size,
+                                 int32_t head_dim, bfly_kv format, float scale, int32_t max_len,
+                                 int32_t window, void* workspace, size_t workspace_bytes,
+                                 void* hip_stream) {
+  if (rows > 0) {
+    if (!q || !k_cache || !v_cache || !tables || !lens || !y) return BFLY_ERR_NULL;
+    if (format != BFLY_KV_BF16 && (!k_scales || !v_scales)) return BFLY_ERR_NULL;
+  }
+  if (!dtype_ok(q_dt) || !dtype_ok(y_dt)) return BFLY_ERR_DTYPE;
+  if (!kv_ok(format)) return BFLY_ERR_QUANT;
+  bfly_status st = cache_sizes(pages, kv_heads, page_size, head_dim);
+  if (st != BFLY_OK) return st;
+  if ((st = attend_sizes(rows, heads, kv_heads, head_dim, max_len)) != BFLY_OK) return st;
+  if (table_width < 1 || max_len > (int64_t)table_width * page_size || window < 0 ||
+      !finite_bits(scale) || q_stride < (int64_t)heads * head_dim)
+    return BFLY_ERR_SIZE;
+  if (q_stride > INT32_MAX || !rows_fit(rows, (int32_t)q_stride) || !rows_fit(rows, table_width))
+    return BFLY_ERR_UNSUPPORTED;
+  const size_t need = bfly_cache_attention_workspace_bytes(rows, heads, kv_heads, head_dim, max_len);
+  if (need > 0 && !workspace) return BFLY_ERR_NULL;
+  if (workspace_bytes < need) return BFLY_ERR_WORKSPACE;
+  if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scales, 2) || !aligned(v_scales, 2) || !aligned(tables, 4) || !aligned(lens, 4) ||
+      !aligned(y, 16) || !aligned(lse, 4) || (need > 0 && !aligned(workspace, 16)))
+    return BFLY_ERR_ALIGN;
+  if (rows == 0) return BFLY_OK;
+  bfly::AttendParams p;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.tables = tables;
+  p.lens = lens;
+  p.y = y;
+  p.lse = lse;
+  p.partials = static_cast<float*>(workspace);
+  p.rows = rows;
+  p.heads = heads;
+  p.kv_heads = kv_heads;
+  p.head_dim = head_dim;
+  p.pages = pages;
+  p.page_shift = log2_pow2(page_size);
+  p.table_width = table_width;
+  p.max_len = max_len;
+  p.window = window;
+  p.format = format;
+  p.q_bf16 = q_dt == BFLY_BF16;
+  p.y_bf16 = y_dt == BFLY_BF16;
+  p.scale = scale;
+  const hipError_t e = bfly::launch_attend(p, (hipStream_t)hip_stream);
   return e == hipSuccess ? BFLY_OK : hip_fail(e);
 }
 

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <exception>
 #include <initializer_list>
@@ -24,6 +25,9 @@ struct Library {
   decltype(&bfly_rmsnorm_backward) rmsnorm_backward;
   decltype(&bfly_lora_matmul) lora_matmul;
   decltype(&bfly_grad_clip) grad_clip;
+  decltype(&bfly_cache_write) cache_write;
+  decltype(&bfly_cache_read) cache_read;
+  decltype(&bfly_cache_attention) cache_attention;
 } library;
 
 // A Python error has been set.
@@ -120,8 +124,30 @@ class Args {
     bytes = x.nbytes();
     return x.data_ptr();
   }
+  // The heads of tokens, [tokens, heads, head_dim]: a token's are contiguous,
+  // the tokens any multiple of elements apart (`stride`).
+  struct Heads {
+    const at::Tensor* t;
+    int64_t stride;
+  };
+  Heads heads(const char* name, int kinds, std::initializer_list<int64_t> shape) {
+    PyObject* const item = *next_++;
+    if (!THPVariable_Check(item)) fail(PyExc_TypeError, "%s is not a tensor", name);
+    const at::Tensor& x = THPVariable_Unpack(item);
+    if (!(kind_of(x.scalar_type()) & kinds)) fail(PyExc_TypeError, "%s has the wrong type", name);
+    if (x.layout() != at::kStrided || x.sizes() != at::IntArrayRef(shape))
+      fail(PyExc_ValueError, "%s has the wrong shape", name);
+    const int64_t tokens = x.size(0), n = x.size(1), d = x.size(2);
+    if ((d > 1 && x.stride(2) != 1) || (n > 1 && x.stride(1) != d))
+      fail(PyExc_ValueError, "the heads of a token of %s have to be contiguous", name);
+    on_gpu(name, x);
+    return {&x, tokens > 1 ? x.stride(0) : n * d};
+  }
   void contiguous(const char* name, const at::Tensor& x) {
     if (!x.is_contiguous()) fail(PyExc_ValueError, "%s has to be contiguous", name);
+    on_gpu(name, x);
+  }
+  void on_gpu(const char* name, const at::Tensor& x) {
     if (!elsewhere_ && (!x.is_cuda() || x.get_device() != device_)) elsewhere_ = name;
   }
   // Last: whether all tensors are on the call's GPU.
@@ -249,6 +275,103 @@ PyObject* lora_matmul(PyObject*, PyObject* const* args, Py_ssize_t count) {
                                  static_cast<const float*>(scaling), address(base),
                                  dtype_of(base), address(y), dtype_of(y), rows, n32, k32, num32,
                                  rank32, workspace, bytes, a.stream);
+    });
+  });
+}
+
+// A cache's four tensors, from which its sizes and format are taken.
+struct Cache {
+  const at::Tensor *k, *v;
+  void *k_scales, *v_scales;
+  int32_t pages, kv_heads, page_size, head_dim;
+  bfly_kv format;
+
+  // k_cache, v_cache, k_scales, v_scales
+  explicit Cache(Args& a) {
+    const at::Tensor& like = a.sized("k_cache", 4);
+    const int64_t p = like.size(0), h = like.size(1), s = like.size(2), d = like.size(3);
+    const int kind = kind_of(like.scalar_type());
+    format = kind == kBF16 ? BFLY_KV_BF16 : kind == kI8 ? BFLY_KV_INT8
+             : kind == kE4M3 ? BFLY_KV_E4M3 : BFLY_KV_INT4;  // bytes hold two codes
+    k = a.tensor("k_cache", kBF16 | kI8 | kE4M3 | kBytes, {p, h, s, d});
+    v = a.tensor("v_cache", kind, {p, h, s, d});
+    if (!v) fail(PyExc_TypeError, "v_cache is not a tensor");
+    k_scales = a.at("k_scales", kF16, {p, h, s});
+    v_scales = a.at("v_scales", kF16, {p, h, s});
+    pages = Args::narrow("the number of pages", p);
+    kv_heads = Args::narrow("the number of heads", h);
+    page_size = Args::narrow("a page", s);
+    head_dim = Args::narrow("a head", format == BFLY_KV_INT4 ? 2 * d : d);
+  }
+  const uint16_t* ks() const { return static_cast<const uint16_t*>(k_scales); }
+  const uint16_t* vs() const { return static_cast<const uint16_t*>(v_scales); }
+};
+
+// cache_write(stream, device, k_cache, v_cache, k_scales, v_scales, k, v, slots);
+// cache_read takes the same.
+template <bool WRITE>
+PyObject* cache_rows(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  return guarded([&] {
+    Args a(args, count, 9);
+    const Cache c(a);
+    const int64_t tokens = a.sized("k", 3).size(0);
+    const Args::Heads k = a.heads("k", kRows, {tokens, c.kv_heads, c.head_dim});
+    const Args::Heads v = a.heads("v", kind_of(k.t->scalar_type()), {tokens, c.kv_heads, c.head_dim});
+    const int32_t* const slots = static_cast<const int32_t*>(a.at("slots", kI32, {tokens}));
+    a.on_the_gpu();
+    return released([&] {
+      if constexpr (WRITE)
+        return library.cache_write(k.t->data_ptr(), k.stride, v.t->data_ptr(), v.stride,
+                                   dtype_of(k.t), slots, tokens, c.k->data_ptr(), c.v->data_ptr(),
+                                   static_cast<uint16_t*>(c.k_scales),
+                                   static_cast<uint16_t*>(c.v_scales), c.pages, c.kv_heads,
+                                   c.page_size, c.head_dim, c.format, a.stream);
+      else
+        return library.cache_read(c.k->data_ptr(), c.v->data_ptr(), c.ks(), c.vs(), slots, tokens,
+                                  k.t->data_ptr(), k.stride, v.t->data_ptr(), v.stride,
+                                  dtype_of(k.t), c.pages, c.kv_heads, c.page_size, c.head_dim,
+                                  c.format, a.stream);
+    });
+  });
+}
+
+// cache_attention(stream, device, scale, max_len, window, k_cache, v_cache,
+// k_scales, v_scales, q, tables, lens, y, lse, workspace); scale None:
+// head_dim^(-1/2); max_len None: all that the tables can hold.
+PyObject* cache_attention(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  return guarded([&] {
+    Args a(args, count, 15);
+    const bool root = a.none();
+    float scale = 0.f;
+    if (root) a.skip();
+    else scale = a.real();
+    const bool all = a.none();
+    int32_t max_len = 0;
+    if (all) a.skip();
+    else max_len = a.int32("max_len");
+    const int32_t window = a.int32("window");
+    const Cache c(a);
+    const at::Tensor& like = a.sized("q", 3);
+    const int64_t rows = like.size(0), heads = like.size(1);
+    const int32_t heads32 = Args::narrow("the number of heads", heads);
+    const Args::Heads q = a.heads("q", kRows, {rows, heads, c.head_dim});
+    const int64_t width = a.sized("tables", 2).size(1);
+    const int32_t width32 = Args::narrow("a table", width);
+    const int32_t* const tables = static_cast<const int32_t*>(a.at("tables", kI32, {rows, width}));
+    const int32_t* const lens = static_cast<const int32_t*>(a.at("lens", kI32, {rows}));
+    const at::Tensor* const y = a.tensor("y", kRows, {rows, heads, c.head_dim});
+    void* const lse = a.at("lse", kF32, {rows, heads});
+    size_t bytes;
+    void* const workspace = a.scratch(bytes);
+    a.on_the_gpu();
+    if (root) scale = 1.f / std::sqrt((float)c.head_dim);
+    if (all) max_len = Args::narrow("a table", width * c.page_size);
+    return released([&] {
+      return library.cache_attention(q.t->data_ptr(), q.stride, dtype_of(q.t), c.k->data_ptr(),
+                                     c.v->data_ptr(), c.ks(), c.vs(), tables, width32, lens,
+                                     address(y), dtype_of(y), static_cast<float*>(lse), rows,
+                                     heads32, c.pages, c.kv_heads, c.page_size, c.head_dim,
+                                     c.format, scale, max_len, window, workspace, bytes, a.stream);
     });
   });
 }
@@ -392,6 +515,19 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t count) {
   Py_RETURN_NONE;
 }
 
+// bind_cache(cache_write, cache_read, cache_attention): theirs.
+PyObject* bind_cache(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  void* at[3];
+  if (count != 3) return PyErr_Format(PyExc_TypeError, "bind_cache() takes three addresses");
+  for (int i = 0; i < 3; ++i)
+    if (!(at[i] = PyLong_AsVoidPtr(args[i])))
+      return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "a null address");
+  library.cache_write = reinterpret_cast<decltype(library.cache_write)>(at[0]);
+  library.cache_read = reinterpret_cast<decltype(library.cache_read)>(at[1]);
+  library.cache_attention = reinterpret_cast<decltype(library.cache_attention)>(at[2]);
+  Py_RETURN_NONE;
+}
+
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -401,6 +537,10 @@ PyMethodDef methods[] = {
     {"rmsnorm_backward", fast(rmsnorm_backward), METH_FASTCALL, "bfly_rmsnorm_backward's status"},
     {"lora_matmul", fast(lora_matmul), METH_FASTCALL, "bfly_lora_matmul's status"},
     {"grad_clip", fast(grad_clip), METH_FASTCALL, "bfly_grad_clip's status"},
+    {"bind_cache", fast(bind_cache), METH_FASTCALL, "the library's functions on a cache"},
+    {"cache_write", fast(cache_rows<true>), METH_FASTCALL, "bfly_cache_write's status"},
+    {"cache_read", fast(cache_rows<false>), METH_FASTCALL, "bfly_cache_read's status"},
+    {"cache_attention", fast(cache_attention), METH_FASTCALL, "bfly_cache_attention's status"},
     {"overlaps", overlaps, METH_VARARGS, "what grad_clip would refuse in a list"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
