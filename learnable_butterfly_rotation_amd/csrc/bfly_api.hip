@@ -1218,7 +1218,7 @@ static bfly_status attend_sizes(int64_t rows, int32_t heads, int32_t kv_heads, i
 size_t bfly_cache_attention_workspace_bytes(int64_t rows, int32_t heads, int32_t kv_heads,
                                             int32_t head_dim, int32_t max_len) {
   if (attend_sizes(rows, heads, kv_heads, head_dim, max_len) != BFLY_OK || rows == 0) return 0;
-  return bfly::attend_workspace_bytes(rows, heads, head_dim, max_len);
+  return bfly::attend_workspace_bytes(rows, heads, kv_heads, head_dim, max_len);
 }
 
 bfly_status bfly_cache_attention(const void* q, int64_t q_stride, bfly_dtype q_dt,

@@ -8,7 +8,7 @@
 //   s_t = (q . code_t) ks_t,   y = sum_t (p_t vs_t) code_t / sum_t p_t,
 // so that a row of d elements costs one product per query head and not d.
 #include "bfly_cache.h"
-#include "bfly_common.h"
+#include "bfly_rows.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -21,14 +21,13 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 4, kStep = 32;         // tokens of a wave's step: two tiles of 16
-constexpr int kRound = kWaves * kStep;        // tokens of a workgroup's round
+constexpr int kStep = 32;                     // tokens of a wave's step: two tiles of 16
 constexpr int kHeads = 16;                    // query heads a workgroup takes (matrix-core columns)
 constexpr float kNone = -3.0e38f;             // below every score: nothing seen yet
 constexpr float kLog2e = 1.44269504088896341f;
 
 // Eight operand values of a matrix-core instruction's lane.
-struct Operand {
+struct __align__(16) Operand {
   uint32_t w[4];
 };
 template <int FMT>
@@ -44,17 +43,22 @@ __device__ __forceinline__ f32x4 product(const Operand& a, const Operand& b, f32
 __device__ __forceinline__ f16x2 halves(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
 __device__ __forceinline__ uint32_t bits_of(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
 
-// Nibbles 0 and 4 (or 1 and 5, `odd`) of a word of int4 codes with their signs
-// flipped, c + 8, as fp16 pairs: with the bits of 1024 above them they read as
-// 1024 + (c + 8), or 1024 + 16 (c + 8); one exact operation leaves c.
+// Nibbles 0 and 4 (or 1 and 5, ODD) of a word of int4 codes as fp16 pairs.  The
+// mask and the bits of 1024 with the sign's flip, in one operation, leave
+// 1024 + (c + 8), or 1024 + 16 (c + 8); one exact operation more leaves c.  The
+// second constant of the first has to be in a register (Magic).
+struct Magic {
+  uint32_t even = 0x64086408u, odd = 0x64806480u;
+  __device__ __forceinline__ void keep() { asm("" : "+v"(even), "+v"(odd)); }
+};
 template <bool ODD>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
+__device__ __forceinline__ uint32_t nibbles(uint32_t w, const Magic& g) {
   if constexpr (ODD) {
-    const f16x2 v = halves((w & 0x00F000F0u) | 0x64006400u);
+    const f16x2 v = halves((w & 0x00F000F0u) ^ g.odd);
     const f16x2 k = {(_Float16)0.0625f, (_Float16)0.0625f}, z = {(_Float16)-72.f, (_Float16)-72.f};
     return bits_of(__builtin_elementwise_fma(v, k, z));
   } else {
-    const f16x2 v = halves((w & 0x000F000Fu) | 0x64006400u);
+    const f16x2 v = halves((w & 0x000F000Fu) ^ g.even);
     const f16x2 z = {(_Float16)-1032.f, (_Float16)-1032.f};
     return bits_of(v + z);
   }
@@ -80,12 +84,13 @@ template <int FMT>
 constexpr int kWords8 = FMT == kCacheBF16 ? 4 : FMT == kCacheInt4 ? 1 : 2;
 
 template <int FMT>
-__device__ __forceinline__ Operand key_operand(const uint32_t* w) {
+__device__ __forceinline__ Operand key_operand(const uint32_t* w, const Magic& g) {
   if constexpr (FMT == kCacheBF16) {
     return Operand{{w[0], w[1], w[2], w[3]}};
   } else if constexpr (FMT == kCacheInt4) {
-    const uint32_t a = w[0] ^ 0x88888888u, b = a >> 8;
-    return Operand{{nibbles<false>(a), nibbles<true>(a), nibbles<false>(b), nibbles<true>(b)}};
+    const uint32_t a = w[0], b = a >> 8;
+    return Operand{{nibbles<false>(a, g), nibbles<true>(a, g), nibbles<false>(b, g),
+                    nibbles<true>(b, g)}};
   } else if constexpr (FMT == kCacheInt8) {
     const uint32_t a = w[0] ^ 0x80808080u, b = w[1] ^ 0x80808080u;
     return Operand{{byte_pair(a, 0x04010400u), byte_pair(a, 0x04030402u),
@@ -97,50 +102,45 @@ __device__ __forceinline__ Operand key_operand(const uint32_t* w) {
 }
 
 // The values' operands: a lane holds E = D / 16 consecutive elements of eight
-// tokens; operand i is element i of the eight.  w[t] are token t's words.
-template <int FMT, int E, int W>
-__device__ __forceinline__ void value_operands(const uint32_t (&w)[8][W], Operand (&out)[E]) {
+// tokens, w[t] token t's words, and operand i is element i of the eight.  Run
+// `h` of operands: those of a word's half (int4) or word.
+template <int FMT>
+constexpr int kRun = FMT == kCacheBF16 ? 2 : 4;
+template <int FMT, int W>
+__device__ __forceinline__ void value_operands(const uint32_t (&w)[8][W], int h,
+                                               Operand (&out)[kRun<FMT>], const Magic& g) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const uint32_t(&a)[W] = w[2 * p];
     const uint32_t(&b)[W] = w[2 * p + 1];
     if constexpr (FMT == kCacheInt4) {
       // 16-bit halves of both tokens side by side: four nibbles of each
-#pragma unroll
-      for (int h = 0; h < E / 4; ++h) {
-        const uint32_t x = 0x88888888u ^ __builtin_amdgcn_perm(b[h / 2], a[h / 2],
-                                                               h % 2 ? 0x07060302u : 0x05040100u);
-        const uint32_t y = x >> 8;
-        out[4 * h].w[p] = nibbles<false>(x);
-        out[4 * h + 1].w[p] = nibbles<true>(x);
-        out[4 * h + 2].w[p] = nibbles<false>(y);
-        out[4 * h + 3].w[p] = nibbles<true>(y);
-      }
+      const uint32_t x = __builtin_amdgcn_perm(b[h / 2], a[h / 2],
+                                               h % 2 ? 0x07060302u : 0x05040100u);
+      const uint32_t y = x >> 8;
+      out[0].w[p] = nibbles<false>(x, g);
+      out[1].w[p] = nibbles<true>(x, g);
+      out[2].w[p] = nibbles<false>(y, g);
+      out[3].w[p] = nibbles<true>(y, g);
     } else if constexpr (FMT == kCacheBF16) {
-#pragma unroll
-      for (int h = 0; h < E / 2; ++h) {
-        out[2 * h].w[p] = __builtin_amdgcn_perm(b[h], a[h], 0x05040100u);
-        out[2 * h + 1].w[p] = __builtin_amdgcn_perm(b[h], a[h], 0x07060302u);
-      }
+      out[0].w[p] = __builtin_amdgcn_perm(b[h], a[h], 0x05040100u);
+      out[1].w[p] = __builtin_amdgcn_perm(b[h], a[h], 0x07060302u);
     } else {
       // bytes a0 b0 a1 b1 and a2 b2 a3 b3
-#pragma unroll
-      for (int h = 0; h < E / 4; ++h) {
-        uint32_t x = __builtin_amdgcn_perm(b[h], a[h], 0x05010400u);
-        uint32_t y = __builtin_amdgcn_perm(b[h], a[h], 0x07030602u);
-        if constexpr (FMT == kCacheInt8) {
-          x ^= 0x80808080u;
-          y ^= 0x80808080u;
-          out[4 * h].w[p] = byte_pair(x, 0x04010400u);
-          out[4 * h + 1].w[p] = byte_pair(x, 0x04030402u);
-          out[4 * h + 2].w[p] = byte_pair(y, 0x04010400u);
-          out[4 * h + 3].w[p] = byte_pair(y, 0x04030402u);
-        } else {
-          out[4 * h].w[p] = e4m3_pair<false>(x);
-          out[4 * h + 1].w[p] = e4m3_pair<true>(x);
-          out[4 * h + 2].w[p] = e4m3_pair<false>(y);
-          out[4 * h + 3].w[p] = e4m3_pair<true>(y);
-        }
+      uint32_t x = __builtin_amdgcn_perm(b[h], a[h], 0x05010400u);
+      uint32_t y = __builtin_amdgcn_perm(b[h], a[h], 0x07030602u);
+      if constexpr (FMT == kCacheInt8) {
+        x ^= 0x80808080u;
+        y ^= 0x80808080u;
+        out[0].w[p] = byte_pair(x, 0x04010400u);
+        out[1].w[p] = byte_pair(x, 0x04030402u);
+        out[2].w[p] = byte_pair(y, 0x04010400u);
+        out[3].w[p] = byte_pair(y, 0x04030402u);
+      } else {
+        out[0].w[p] = e4m3_pair<false>(x);
+        out[1].w[p] = e4m3_pair<true>(x);
+        out[2].w[p] = e4m3_pair<false>(y);
+        out[3].w[p] = e4m3_pair<true>(y);
       }
     }
   }
@@ -227,12 +227,52 @@ constexpr int kWeightParts = (FMT == kCacheBF16 ? 2 : 1) + (EXACT ? 1 : 0);
 struct Reach {
   int first, end, base;
 };
-__device__ __forceinline__ Reach reach_of(const AttendParams& P, int64_t row) {
+// Words that no one writes during the call, at a uniform index: a scalar load,
+// which does not wait for the vector loads in flight.
+__device__ __forceinline__ int uniform_word(const int32_t* p, int64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t* Constant;
+  return ((Constant)(uintptr_t)p)[i];
+}
+__device__ __forceinline__ Reach reach_of(const AttendParams& P, int len) {
   Reach r;
-  r.end = min(max(P.lens[row], 0), P.max_len);
+  r.end = min(max(len, 0), P.max_len);
   r.first = P.window > 0 ? max(0, r.end - P.window) : 0;
   r.base = r.first & ~(kStep - 1);
   return r;
+}
+
+// Sum of v over the lanes up to this one.
+__device__ __forceinline__ int lanes_before(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // the lane before in its 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // the last of the 16 before
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // lane 31 to the upper half
+  return v;
+}
+// Chunk `at` of all rows' chunks, rows one after the other: its row and which
+// of the row's it is; false past the last.
+__device__ __forceinline__ bool find_chunk(const AttendParams& P, int chunk, int at, int& row,
+                                           int& split) {
+  const int lane = threadIdx.x & 63;
+  for (int r0 = 0; r0 < (int)P.rows; r0 += 64) {
+    int mine = 0;
+    if (r0 + lane < (int)P.rows) {
+      const Reach r = reach_of(P, P.lens[r0 + lane]);
+      mine = (r.end - r.base + chunk - 1) / chunk;
+    }
+    const int upto = lanes_before(mine);
+    const uint64_t past = __ballot(upto > at);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      row = r0 + l;
+      split = at - __builtin_amdgcn_readlane(upto - mine, l);
+      return true;
+    }
+    at -= __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
 }
 
 // One head of the partial results of a call whose length is split: the
@@ -258,9 +298,15 @@ __device__ __forceinline__ float log_sum(float top, float l) {
   return l == 0.f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(l)) / kLog2e;
 }
 
+// More registers than two waves to a SIMD may have.
 template <int FMT, int D, bool EXACT>
-__global__ void __launch_bounds__(256) attend_kernel(AttendParams P, int splits, int chunk,
-                                                     int blocks) {
+constexpr bool kLarge = FMT == kCacheBF16 && D == 256 && EXACT;
+
+// A workgroup of W waves: one row, up to 16 query heads of a key-value head,
+// one chunk of the length.  Its waves take steps of 32 tokens in turn.
+template <int FMT, int D, bool EXACT, int W>
+__global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 : 1))
+    attend_kernel(AttendParams P, int share, int blocks, int splits, int chunk, int packed) {
   constexpr int E = D / 16;                     // a lane's elements of a value
   constexpr int QN = kQueryParts<FMT, EXACT>, WN = kWeightParts<FMT, EXACT>;
   constexpr int KB = cache_bytes(FMT, D / 4);   // a lane's bytes of a key
@@ -268,117 +314,95 @@ __global__ void __launch_bounds__(256) attend_kernel(AttendParams P, int splits,
   constexpr int KW = KB / 4, VW = VB < 4 ? 1 : VB / 4;
   constexpr int ROW = cache_bytes(FMT, D);
   constexpr bool SCALED = FMT != kCacheBF16;
-  __shared__ float factors[kWaves][3][kStep];   // of a step's tokens: ks, log2 vs, 1 / vs
-  __shared__ float stats[kWaves][2][kHeads];
-  constexpr int PARTS = D > 128 ? 2 : 1, DP = D / PARTS;   // of the waves' results, one at a time
-  __shared__ float sums[kWaves][kHeads][DP + 4];
+  constexpr int ROUND = W * kStep;
+  // heads whose results are joined at a time
+  constexpr int COLS = W * D > 512 ? kHeads * 512 / (W * D) : kHeads;
+  constexpr int SUMS = W * COLS * (D + 4) * 4, QUERIES = QN * (D / 32) * 64 * 16;
+  __shared__ float factors[W][3][kStep];        // of a step's tokens: ks, log2 vs, 1 / vs
+  __shared__ float tops[W][kHeads], totals[W][4][kHeads], query_scales[kHeads];
+  __shared__ __align__(16) char room[SUMS > QUERIES ? SUMS : QUERIES];
+  float(*const sums)[COLS][D + 4] = reinterpret_cast<float(*)[COLS][D + 4]>(room);
+  Operand(*const queries)[D / 32][64] = reinterpret_cast<Operand(*)[D / 32][64]>(room);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int col = lane & 15, group = lane >> 4;
-  const int share = P.heads / P.kv_heads;
-  int at = (int)blockIdx.x;
-  const int split = at % splits;
-  at /= splits;
-  const int block = at % blocks;
-  at /= blocks;
-  const int kvh = at % P.kv_heads;
-  const int64_t row = at / P.kv_heads;
+  // packed: the y axis counts the chunks that there are, else x goes over the
+  // rows too and y over the chunks that there may be
+  int x = blockIdx.x, row32 = 0, split = blockIdx.y;
+  if (packed) {
+    if (!find_chunk(P, chunk, blockIdx.y, row32, split)) return;
+  } else if (P.rows > 1) {
+    row32 = x / (P.kv_heads * blocks);
+    x -= row32 * (P.kv_heads * blocks);
+  }
+  const int64_t row = row32;
+  const int kvh = blocks == 1 ? x : x / blocks, block = x - kvh * blocks;
   const int head0 = kvh * share + block * kHeads;            // the block's first query head
   const int heads = min(kHeads, share - block * kHeads);     // and how many it has
-  const Reach R = reach_of(P, row);
+  const int shift = P.page_shift, in_page = (1 << shift) - 1;
+  const int32_t* const table = P.tables + row * P.table_width;
+  // without a window the first pages are known before the length is
+  int early[2] = {0, 0};
+  if (P.window == 0) {
+    const int t = split * chunk + wave * kStep;
+    early[0] = uniform_word(table, min(t >> shift, P.table_width - 1));
+    early[1] = uniform_word(table, min((t + 16) >> shift, P.table_width - 1));
+  }
+  // the queries' elements, eight to a thread: D / 8 lanes to a head
+  constexpr int QL = D / 8, QC = (kHeads * QL + 64 * W - 1) / (64 * W);
+  uint32_t raw_q[QC][8];
+#pragma unroll
+  for (int n = 0; n < QC; ++n) {
+    const int c = threadIdx.x + n * 64 * W, h = c / QL;
+    const int64_t from = row * P.q_stride + (int64_t)(head0 + h) * D + c % QL * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw_q[n][i] = 0;
+    if (h < heads) {
+      if (!EXACT || P.q_bf16) fetch<16>(static_cast<const char*>(P.q) + from * 2, raw_q[n]);
+      else fetch<32>(static_cast<const char*>(P.q) + from * 4, raw_q[n]);
+    }
+  }
+  const Reach R = reach_of(P, uniform_word(P.lens, row));
   const int t0 = R.base + split * chunk, t1 = min(R.end, t0 + chunk);
   if (t0 >= t1 && splits > 1) return;           // nothing to add: the join does not look here
 
-  // the queries: column `col` is head head0 + col, a lane holds its D / 4 elements
-  Operand q[QN][D / 32];
-  float qscale;
-  {
-    float f[D / 4];
-    const bool mine = col < heads;
-    const int64_t from = row * P.q_stride + (int64_t)(head0 + (mine ? col : 0)) * D + group * (D / 4);
-    if (P.q_bf16) {
-      uint32_t w[D / 8];
-      fetch<D / 2>(static_cast<const char*>(P.q) + from * 2, w);
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) f[i] = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-    } else {
-      uint32_t w[D / 4];
-      fetch<D>(static_cast<const char*>(P.q) + from * 4, w);
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) f[i] = __uint_as_float(w[i]);
-    }
-    qscale = P.scale * kLog2e;
-    float by = 1.f;
-    if constexpr (SCALED) {
-      // a power of two that brings the largest element to [2^14, 2^15): fp16
-      // then holds every element down to 2^-29 of it with all its bits
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(f[i]));
-      top = across_groups(top, [](float a, float b) { return fmaxf(a, b); });
-      int e = top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
-      e = min(max(e, -120), 120);
-      by = top < __builtin_inff() ? ldexpf(1.f, e) : __builtin_nanf("");
-      qscale = ldexpf(qscale, -e);
-    }
-#pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = mine ? f[8 * s + key_order<FMT>(j)] * by : 0.f;
-#pragma unroll
-      for (int n = 0; n < QN; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (SCALED) {
-            const f32x2_t pair = {v[2 * i], v[2 * i + 1]};
-            const f16x2 h = __builtin_convertvector(pair, f16x2);
-            q[n][s].w[i] = bits_of(h);
-            v[2 * i] -= (float)h.x;
-            v[2 * i + 1] -= (float)h.y;
-          } else {
-            const uint32_t h = pack_bf16(v[2 * i], v[2 * i + 1]);
-            q[n][s].w[i] = h;
-            v[2 * i] -= bf16_lo(h);
-            v[2 * i + 1] -= bf16_hi(h);
-          }
-        }
-    }
-  }
-
-  const int shift = P.page_shift, in_page = (1 << shift) - 1;
-  const int32_t* const table = P.tables + row * P.table_width;
-  // page of the tile of 16 tokens at t, or -1: past the end, or none in the table
-  const auto page_of = [&](int t) {
-    if (t >= t1) return -1;
-    const int id = __builtin_amdgcn_readfirstlane(table[t >> shift]);
-    return (uint32_t)id < (uint32_t)P.pages ? id : -1;
+  // page of the tile of 16 tokens at t from its table entry, or -1: past the
+  // end, or none in the cache
+  const auto page_of = [&](int t, int id) {
+    return t < t1 && (uint32_t)id < (uint32_t)P.pages ? id : -1;
   };
-  const int64_t head_rows = (int64_t)1 << shift;
+  const auto entry = [&](int t) { return t < t1 ? uniform_word(table, t >> shift) : -1; };
   // a page's first row of this head; page 0 stands in where there is none
   const auto row_of = [&](int page, int t) {
-    return ((int64_t)max(page, 0) * P.kv_heads + kvh) * head_rows + (t & in_page);
+    return (((int64_t)max(page, 0) * P.kv_heads + kvh) << shift) + (t & in_page);
   };
   const char* const kc = static_cast<const char*>(P.k_cache);
   const char* const vc = static_cast<const char*>(P.v_cache);
 
+  // row r of a tile's product is its token 4 (r % 4) + r / 4 (and the other way
+  // round), so that the tokens 4 i + group that a lane weighs lie, for each i,
+  // next to each other in memory
+  const int token = col;
+  // what a step needs: the next step's keys go out as soon as this one's are
+  // used, its values likewise
   uint32_t k[2][KW], v[8][VW];
-  uint16_t raw_ks = 0, raw_vs = 0;   // lane t: token t of the step (the tile of a lane above 31 is not used)
-  const int my_tile = (lane >> 4) & 1;
-  const auto load_keys = [&](int t, const int (&page)[2]) {
+  uint16_t raw_ks, raw_vs;    // lane t: token t's scales (lanes above 31 repeat them)
+  int page[2];
+  const bool upper = lane & 16;
+  const auto load_keys = [&](int t) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const char* const p = kc + row_of(page[j], t + 16 * j) * ROW;
-      fetch<KB>(p + (uint32_t)(col * ROW + group * KB), k[j]);
+      fetch<KB>(p + (uint32_t)(token * ROW + group * KB), k[j]);
     }
     if constexpr (SCALED) {
       const int64_t r0 = row_of(page[0], t), r1 = row_of(page[1], t + 16);
-      const int64_t r = (my_tile ? r1 : r0) + col;
+      const int64_t r = (upper ? r1 : r0) + col;
       raw_ks = P.k_scales[r];
       raw_vs = P.v_scales[r];
     }
   };
-  const auto load_values = [&](int t, const int (&page)[2]) {
+  const auto load_values = [&](int t) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const char* const p = vc + row_of(page[j], t + 16 * j) * ROW;
@@ -387,22 +411,81 @@ __global__ void __launch_bounds__(256) attend_kernel(AttendParams P, int splits,
         fetch<VB>(p + (uint32_t)((4 * group + i) * ROW + col * VB), v[4 * j + i]);
     }
   };
+  int t = t0 + wave * kStep;
+  if (t < t1) {
+    page[0] = page_of(t, P.window == 0 ? early[0] : entry(t));
+    page[1] = page_of(t + 16, P.window == 0 ? early[1] : entry(t + 16));
+    load_keys(t);
+    load_values(t);
+  }
 
+  // from each thread's eight elements to the operands of the waves
+#pragma unroll
+  for (int n = 0; n < QC; ++n) {
+    const int c = threadIdx.x + n * 64 * W, h = c / QL, chunk8 = c % QL;
+    if (64 * W > kHeads * QL && h >= kHeads) break;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      f[i] = EXACT && !P.q_bf16 ? __uint_as_float(raw_q[n][i])
+             : (i & 1) ? bf16_hi(raw_q[n][i >> 1]) : bf16_lo(raw_q[n][i >> 1]);
+    if constexpr (SCALED) {
+      // a power of two that brings the largest element to [2^14, 2^15): fp16
+      // then holds every element down to 2^-29 of it with all its bits
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+      top = run_max(top, QL);
+      int e = top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+      e = min(max(e, -120), 120);
+      const float by = top < __builtin_inff() ? ldexpf(1.f, e) : __builtin_nanf("");
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= by;
+      if (chunk8 == 0) query_scales[h] = ldexpf(P.scale * kLog2e, -e);
+    }
+    // elements 8 chunk8 ... of a head belong to lane group chunk8 / (D / 32)
+#pragma unroll
+    for (int part = 0; part < QN; ++part) {
+      Operand o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float &x = f[key_order<FMT>(2 * i)], &y = f[key_order<FMT>(2 * i + 1)];
+        if constexpr (SCALED) {
+          const f32x2_t pair = {x, y};
+          const f16x2 r = __builtin_convertvector(pair, f16x2);
+          o.w[i] = bits_of(r);
+          x -= (float)r.x;
+          y -= (float)r.y;
+        } else {
+          o.w[i] = pack_bf16(x, y);
+          x -= bf16_lo(o.w[i]);
+          y -= bf16_hi(o.w[i]);
+        }
+      }
+      queries[part][chunk8 % (D / 32)][chunk8 / (D / 32) * 16 + h] = o;
+    }
+  }
+  __syncthreads();
+  Operand q[QN][D / 32];
+#pragma unroll
+  for (int part = 0; part < QN; ++part)
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) q[part][c] = queries[part][c][lane];
+  const float qscale = SCALED ? query_scales[col] : P.scale * kLog2e;
+
+  Magic magic;
+  magic.keep();
   float m = kNone, total = 0.f;
   f32x4 acc[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  int t = t0 + wave * kStep;
-  int page[2], next[2];
-  if (t < t1) {
-    page[0] = page_of(t), page[1] = page_of(t + 16);
-    load_keys(t, page);
-    load_values(t, page);
-  }
-  for (; t < t1; t += kRound) {
-    const int tn = t + kRound;
-    if (tn < t1) next[0] = page_of(tn), next[1] = page_of(tn + 16);
+  // the table's entries of the step to load next
+  int ids[2] = {entry(t + ROUND), entry(t + ROUND + 16)};
+  for (; t < t1; t += ROUND) {
+    const int tn = t + ROUND, id[2] = {ids[0], ids[1]};
+    ids[0] = entry(tn + ROUND);
+    ids[1] = entry(tn + ROUND + 16);
     // a step that has tokens nobody may look at
     const bool edge = t < R.first || t + kStep > t1 || page[0] < 0 || page[1] < 0;
 
@@ -412,16 +495,11 @@ __global__ void __launch_bounds__(256) attend_kernel(AttendParams P, int splits,
       s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        const Operand a = key_operand<FMT>(&k[j][c * kWords8<FMT>]);
+        const Operand a = key_operand<FMT>(&k[j][c * kWords8<FMT>], magic);
 #pragma unroll
         for (int n = 0; n < QN; ++n) s[j] = product<FMT>(a, q[n][c], s[j]);
       }
     }
-    // a token of the step that may be looked at
-    const auto seen = [&](int i) {
-      const int at_t = t + i;
-      return at_t >= R.first && at_t < t1 && (i < 16 ? page[0] : page[1]) >= 0;
-    };
     float u[8], inv[8];
     if constexpr (SCALED) {
       if (lane < kStep) {
@@ -429,9 +507,10 @@ __global__ void __launch_bounds__(256) attend_kernel(AttendParams P, int splits,
         // a value scale of 0 stands for a row of codes 0: any scale will do
         float vs = (float)__builtin_bit_cast(_Float16, raw_vs);
         vs = vs == 0.f ? 1.f : vs;
-        factors[wave][0][lane] = ks;
-        factors[wave][1][lane] = __builtin_amdgcn_logf(vs);
-        factors[wave][2][lane] = __builtin_amdgcn_rcpf(vs);
+        const int at = (lane & 16) + token;
+        factors[wave][0][at] = ks;
+        factors[wave][1][at] = __builtin_amdgcn_logf(vs);
+        factors[wave][2][at] = __builtin_amdgcn_rcpf(vs);
       }
       wave_lds_sync();
 #pragma unroll
@@ -455,7 +534,8 @@ __global__ void __launch_bounds__(256) attend_kernel(AttendParams P, int splits,
       // finite, so that a weight of 0 is enough for them)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool ok = seen(16 * (i >> 2) + 4 * group + (i & 3));
+        const int at = t + 16 * (i >> 2) + 4 * group + (i & 3);
+        const bool ok = at >= R.first && at < t1 && page[i >> 2] >= 0;
         u[i] = ok ? u[i] : -__builtin_inff();
         if constexpr (SCALED) inv[i] = ok ? inv[i] : 0.f;
         if constexpr (FMT == kCacheBF16 || FMT == kCacheE4M3)
@@ -463,13 +543,13 @@ __global__ void __launch_bounds__(256) attend_kernel(AttendParams P, int splits,
           for (int h = 0; h < VW; ++h) v[i][h] = ok ? v[i][h] : 0u;
       }
     }
-    float top = fmaxf(fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])),
-                      fmaxf(fmaxf(u[4], u[5]), fmaxf(u[6], u[7])));
-    top = across_groups(top, [](float a, float b) { return fmaxf(a, b); });
     // weights are 2^(u - m) with m between 15 below the largest u and 8 below
     // it, so that it seldom moves and fp16 holds them down to 2^-22 of the
     // largest with all bits
+    float top = fmaxf(fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])),
+                      fmaxf(fmaxf(u[4], u[5]), fmaxf(u[6], u[7])));
     if (__any(top > m + 15.f)) {
+      top = across_groups(top, [](float a, float b) { return fmaxf(a, b); });
       const float to = top > m + 15.f ? top - 8.f : m;
       const float fade = __builtin_amdgcn_exp2f(m - to);
       m = to;
@@ -483,138 +563,212 @@ __global__ void __launch_bounds__(256) attend_kernel(AttendParams P, int splits,
       w[i] = __builtin_amdgcn_exp2f(u[i] - m);
       total = SCALED ? fmaf(w[i], inv[i], total) : total + w[i];
     }
-    if (tn < t1) load_keys(tn, next);
-
+    if (tn < t1) {
+      page[0] = page_of(tn, id[0]);
+      page[1] = page_of(tn + 16, id[1]);
+      load_keys(tn);
+    }
     Operand p[WN];
     weight_parts<FMT, WN>(w, p);
-    Operand x[E];
-    value_operands<FMT, E, VW>(v, x);
+    constexpr int RUN = kRun<FMT>;
 #pragma unroll
-    for (int i = 0; i < E; ++i)
+    for (int h = 0; h < E / RUN; ++h) {
+      Operand x[RUN];
+      value_operands<FMT, VW>(v, h, x, magic);
 #pragma unroll
-      for (int n = 0; n < WN; ++n) acc[i] = product<FMT>(x[i], p[n], acc[i]);
-    if (tn < t1) load_values(tn, next);
-    page[0] = next[0], page[1] = next[1];
+      for (int i = 0; i < RUN; ++i)
+#pragma unroll
+        for (int n = 0; n < WN; ++n)
+          acc[h * RUN + i] = product<FMT>(x[i], p[n], acc[h * RUN + i]);
+    }
+    if (tn < t1) load_values(tn);
   }
 
-  // the waves' results joined
-  total = across_groups(total, [](float a, float b) { return a + b; });
-  if (group == 0) {
-    stats[wave][0][col] = m;
-    stats[wave][1][col] = total;
-  }
-  __syncthreads();
-  float top = stats[0][0][col];
+  // the waves' results joined, COLS heads at a time
+#pragma unroll 1
+  for (int c0 = 0; c0 < heads; c0 += COLS) {
+    if (c0 > 0) __syncthreads();
+    if (c0 == 0) {
+      if (group == 0) tops[wave][col] = m;
+      totals[wave][group][col] = total;
+    }
+    // operand i's row 4 group + r of the product is element (4 group + r) E + i
+    if ((uint32_t)(col - c0) < (uint32_t)COLS)
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) top = fmaxf(top, stats[i][0][col]);
-  const float fade = __builtin_amdgcn_exp2f(m - top);
-  // operand i's row 4 group + r of the product is element (4 group + r) E + i
-  constexpr int RP = 4 / PARTS;
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-  for (int part = 0; part < PARTS; ++part) {
-    if (part > 0) __syncthreads();
-#pragma unroll
-    for (int r = 0; r < RP; ++r)
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        sums[wave][col][(RP * group + r) * E + i] = acc[i][RP * part + r] * fade;
+        for (int i = 0; i < E; ++i) sums[wave][col - c0][(4 * group + r) * E + i] = acc[i][r];
     __syncthreads();
-    for (int i = threadIdx.x; i < heads * (DP / 4); i += 256) {
-      const int h = i / (DP / 4), x = i % (DP / 4) * 4, r = x / E;
-      const int d = (r / RP * 4 + RP * part + r % RP) * E + x % E;
-      float all = stats[0][0][h], l = 0.f;
+    const int here = min(COLS, heads - c0);
+    for (int i = threadIdx.x; i < here * (D / 4); i += 64 * W) {
+      const int x = i / (D / 4), h = c0 + x, d = i % (D / 4) * 4;
+      float top = tops[0][h], l = 0.f;
 #pragma unroll
-      for (int n = 1; n < kWaves; ++n) all = fmaxf(all, stats[n][0][h]);
+      for (int n = 1; n < W; ++n) top = fmaxf(top, tops[n][h]);
       f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int n = 0; n < kWaves; ++n) {
-        l = fmaf(stats[n][1][h], __builtin_amdgcn_exp2f(stats[n][0][h] - all), l);
-        o += *reinterpret_cast<const f32x4*>(&sums[n][h][x]);
+      for (int n = 0; n < W; ++n) {
+        const float by = __builtin_amdgcn_exp2f(tops[n][h] - top);
+        const float sum = (totals[n][0][h] + totals[n][1][h]) + (totals[n][2][h] + totals[n][3][h]);
+        l = fmaf(sum, by, l);
+        o += *reinterpret_cast<const f32x4*>(&sums[n][x][d]) * by;
       }
       const int64_t to = row * P.heads + head0 + h;
       if (splits > 1) {
         Partial<D>* const result = reinterpret_cast<Partial<D>*>(P.partials) + to * splits + split;
         *reinterpret_cast<f32x4*>(&result->y[d]) = o;
-        if (d == 0) result->top = all, result->total = l;
+        if (d == 0) result->top = top, result->total = l;
       } else {
         put_result(P, to * D + d, o, l);
-        if (P.lse && d == 0) P.lse[to] = log_sum(all, l);
+        if (P.lse && d == 0) P.lse[to] = log_sum(top, l);
       }
     }
   }
 }
 
-// The partial results of a row's head joined: a workgroup to each.
-template <int D>
-__global__ void __launch_bounds__(256) join_kernel(AttendParams P, int splits, int chunk) {
-  constexpr int L = D / 4, G = 256 / L;         // lanes to a partial result, results at a time
+// The partial results of a row's head joined: a workgroup of N threads to each,
+// D / 4 of them to a partial result.  A thread brings what it reads together
+// with a maximum of its own; all its loads go out before the length is known.
+template <int D, int N>
+__global__ void __launch_bounds__(N) join_kernel(AttendParams P, int splits, int chunk) {
+  constexpr int L = D / 4, G = N / L, AHEAD = 4;
   __shared__ f32x4 sums[G][L];
-  __shared__ float totals[G];
+  __shared__ float tops[G], totals[G];
   const int64_t to = blockIdx.x;
-  const Reach R = reach_of(P, to / P.heads);
-  const int used = (R.end - R.base + chunk - 1) / chunk;
   const Partial<D>* const part = reinterpret_cast<const Partial<D>*>(P.partials) + to * splits;
   const int g = threadIdx.x / L, d = threadIdx.x % L * 4;
-  float top = kNone;
-  for (int i = 0; i < used; ++i) top = fmaxf(top, part[i].top);
-  float l = 0.f;
+  int used = splits;
+  float top = kNone, l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int i = g; i < used; i += G) {
-    const float by = __builtin_amdgcn_exp2f(part[i].top - top);
-    l = fmaf(part[i].total, by, l);
-    o += *reinterpret_cast<const f32x4*>(&part[i].y[d]) * by;
+  for (int i0 = g; i0 < used; i0 += AHEAD * G) {
+    float2 s[AHEAD];
+    f32x4 y[AHEAD];
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) {
+      const int i = min(i0 + n * G, splits - 1);
+      s[n] = *reinterpret_cast<const float2*>(&part[i].top);
+      y[n] = *reinterpret_cast<const f32x4*>(&part[i].y[d]);
+    }
+    if (i0 == g) {
+      const Reach R = reach_of(P, uniform_word(P.lens, to / P.heads));
+      used = (R.end - R.base + chunk - 1) / chunk;
+    }
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) {
+      if (i0 + n * G >= used) break;
+      const float all = fmaxf(top, s[n].x);
+      const float was = __builtin_amdgcn_exp2f(top - all), is = __builtin_amdgcn_exp2f(s[n].x - all);
+      l = fmaf(s[n].y, is, l * was);
+      o = o * was + y[n] * is;
+      top = all;
+    }
   }
   sums[g][threadIdx.x % L] = o;
-  if (threadIdx.x % L == 0) totals[g] = l;
+  if (threadIdx.x % L == 0) tops[g] = top, totals[g] = l;
   __syncthreads();
   if (g != 0) return;
+  float all = tops[0];
 #pragma unroll
-  for (int i = 1; i < G; ++i) {
-    o += sums[i][threadIdx.x % L];
-    l += totals[i];
+  for (int i = 1; i < G; ++i) all = fmaxf(all, tops[i]);
+  l = 0.f;
+  o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const float by = __builtin_amdgcn_exp2f(tops[i] - all);
+    l = fmaf(totals[i], by, l);
+    o += sums[i][threadIdx.x % L] * by;
   }
   put_result(P, to * D + d, o, l);
-  if (P.lse && threadIdx.x == 0) P.lse[to] = log_sum(top, l);
+  if (P.lse && threadIdx.x == 0) P.lse[to] = log_sum(all, l);
 }
 
-constexpr int kWorkgroups = 1024;    // that fill the card
-constexpr int kLeast = 256;          // tokens that are worth a workgroup
-
-int most_splits(int max_len) { return (max_len + kStep - 1 + kLeast - 1) / kLeast; }
+// How a call's lengths, up to `reach`, are cut: into chunks, or not at all.
+//   Up to 512 tokens (1024 where there are 128 items or more, each a row's
+// key-value head) the second launch costs more than it spreads: 32 rows of 8
+// heads of 1024 tokens int8 12.9 us in one chunk, 13.6 in 256s.
+//   One row is as long as it is known to be: 512 workgroups (131072 tokens of
+// e4m3 56 us, 62 with 1024).
+//   Rows of lengths that only the device knows: a card full of chunks as short
+// as pays, since no workgroup may last much longer than the average.  128
+// tokens, while there are at most 2048 workgroups (8 rows of 1024: 8.6 us, 256
+// tokens 10.0), up to 512 (32 rows of 4096: 128 tokens 31.7 us, 256 24.1, 512
+// 21.7, 1024 26.0; 64 ragged rows of up to 8192 int4: 512 50.5, 1024 52.5, 2048
+// 56), more where that would be above 8192 workgroups.  256 instead of 128
+// where a chunk's partial results, 16 heads of 256, are large (18.0 for 19.9).
+struct Cut {
+  int chunk, splits;
+};
+constexpr int kOneChunk = 512, kAlone = 512, kMost = 8192;
+Cut cut_of(int64_t rows, int64_t items, int share, int head_dim, int reach) {
+  if (reach <= kOneChunk || (reach <= 2 * kOneChunk && items >= 128)) return {reach, 1};
+  const auto whole = [](int64_t v) { return (int)((v + 127) / 128 * 128); };
+  const int least = std::min(share, kHeads) * head_dim >= 2048 ? 256 : 128;
+  const auto splits = [&](int chunk) { return (reach + chunk - 1) / chunk; };
+  int chunk = least;
+  if (rows == 1) {
+    chunk = std::max(chunk, whole((items * reach + kAlone - 1) / kAlone));
+  } else {
+    while (chunk < 512 && items * splits(chunk) > 2048) chunk *= 2;
+    if (items * splits(chunk) > kMost)
+      chunk = std::max(chunk, whole((items * reach + kMost - 1) / kMost));
+  }
+  return {chunk, splits(chunk)};
+}
 
 }  // namespace
 
-size_t attend_workspace_bytes(int64_t rows, int heads, int head_dim, int max_len) {
-  const int64_t results = rows * heads, most = most_splits(max_len);
-  if (most <= 1) return 0;
-  // splits <= min(most, 1 + kWorkgroups / items), and 16 items cover 16 heads each
-  const int64_t parts = std::min(results * most, results + (int64_t)kHeads * kWorkgroups);
+size_t attend_workspace_bytes(int64_t rows, int heads, int kv_heads, int head_dim, int max_len) {
+  if (max_len <= kOneChunk) return 0;
+  // no call has more than items + kMost chunks, of up to 16 heads each, nor
+  // more than one for every 128 tokens
+  const int share = heads / kv_heads, blocks = (share + kHeads - 1) / kHeads;
+  const int64_t items = rows * kv_heads * blocks;
+  const int64_t parts = std::min(rows * heads * ((max_len + 127) / 128),
+                                 (items + kMost) * std::min(share, kHeads));
   return (size_t)parts * (size_t)(head_dim + 4) * sizeof(float);
 }
 
 hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   const int share = p.heads / p.kv_heads, blocks = (share + kHeads - 1) / kHeads;
   const int64_t items = p.rows * p.kv_heads * blocks;
-  const int reach = p.window > 0 ? std::min(p.max_len, p.window + kStep - 1) : p.max_len;
-  const int64_t want = 1 + (kWorkgroups - 1) / items;   // rounded up
-  int splits = (int)std::max<int64_t>(1, std::min<int64_t>((reach + kLeast - 1) / kLeast, want));
-  const int chunk = std::max(kRound, ((reach + splits - 1) / splits + kRound - 1) / kRound * kRound);
-  splits = std::max(1, (reach + chunk - 1) / chunk);
-  const dim3 grid((unsigned)(items * splits));
-  const auto go = [&](auto d, auto f) {
+  const int reach = p.window > 0 ? (int)std::min<int64_t>(p.max_len, (int64_t)p.window + kStep - 1)
+                                 : p.max_len;
+  const Cut cut = cut_of(p.rows, items, share, p.head_dim, reach);
+  const int chunk = cut.chunk, splits = cut.splits;
+  // a chunk each of up to 256 rows is looked for among their lengths, so that no
+  // workgroup is there for what a short row does not have (64 ragged rows of up
+  // to 8192: 50.5 us, 57 without)
+  const bool packed = splits > 1 && p.rows > 1 && p.rows <= 256 && p.rows * splits < 65536;
+  const unsigned across = (unsigned)(p.kv_heads * blocks);
+  const dim3 grid = packed ? dim3(across, (unsigned)(p.rows * splits))
+                           : dim3((unsigned)items, (unsigned)splits);
+  // eight waves where one chunk has to do and the card is not full of them (8
+  // heads of 512 tokens int8 7.8 us, four waves 8.5; 1024 items 24 and 17)
+  const bool wide = splits == 1 && items <= 512;
+  const auto go = [&](auto d, auto f, auto exact) {
     constexpr int D = decltype(d)::value, F = decltype(f)::value;
-    if (p.q_bf16 && p.y_bf16) attend_kernel<F, D, false><<<grid, 256, 0, s>>>(p, splits, chunk, blocks);
-    else attend_kernel<F, D, true><<<grid, 256, 0, s>>>(p, splits, chunk, blocks);
+    constexpr bool X = decltype(exact)::value;
+    constexpr int W = kLarge<F, D, X> ? 4 : 8;
+    if (wide) attend_kernel<F, D, X, W><<<grid, 64 * W, 0, s>>>(p, share, blocks, splits, chunk, packed);
+    else attend_kernel<F, D, X, 4><<<grid, 256, 0, s>>>(p, share, blocks, splits, chunk, packed);
+  };
+  const auto by_type = [&](auto d, auto f) {
+    if (p.q_bf16 && p.y_bf16) go(d, f, std::false_type{});
+    else go(d, f, std::true_type{});
   };
   const auto by_format = [&](auto d) {
     constexpr int D = decltype(d)::value;
     switch (p.format) {
-      case kCacheBF16: go(d, std::integral_constant<int, kCacheBF16>{}); break;
-      case kCacheInt8: go(d, std::integral_constant<int, kCacheInt8>{}); break;
-      case kCacheE4M3: go(d, std::integral_constant<int, kCacheE4M3>{}); break;
-      default: go(d, std::integral_constant<int, kCacheInt4>{}); break;
+      case kCacheBF16: by_type(d, std::integral_constant<int, kCacheBF16>{}); break;
+      case kCacheInt8: by_type(d, std::integral_constant<int, kCacheInt8>{}); break;
+      case kCacheE4M3: by_type(d, std::integral_constant<int, kCacheE4M3>{}); break;
+      default: by_type(d, std::integral_constant<int, kCacheInt4>{}); break;
     }
-    if (splits > 1) join_kernel<D><<<(unsigned)(p.rows * p.heads), 256, 0, s>>>(p, splits, chunk);
+    if (splits > 1) {
+      const unsigned results = (unsigned)(p.rows * p.heads);
+      if (splits > 16) join_kernel<D, 1024><<<results, 1024, 0, s>>>(p, splits, chunk);
+      else join_kernel<D, 256><<<results, 256, 0, s>>>(p, splits, chunk);
+    }
   };
   switch (p.head_dim) {
     case 64: by_format(std::integral_constant<int, 64>{}); break;
