@@ -83,6 +83,17 @@ __host__ __device__ constexpr int key_order(int j) {
 template <int FMT>
 constexpr int kWords8 = FMT == kCacheBF16 ? 4 : FMT == kCacheInt4 ? 1 : 2;
 
+// Which elements a lane holds.  Of a key its group of 16 lanes takes every
+// fourth piece of up to 16 bytes, so that a load of the wave covers 64
+// consecutive bytes of each of 16 tokens: kKeyRuns runs of eight elements to a
+// piece.  Of a value it takes pieces of up to 16 bytes, the 16 lanes' side by
+// side: kValueRun elements to a piece.
+template <int FMT, int D>
+constexpr int kKeyRuns = (cache_bytes(FMT, D / 4) < 16 ? cache_bytes(FMT, D / 4) : 16) /
+                         cache_bytes(FMT, 8);
+template <int FMT, int D>
+constexpr int kValueRun = cache_bytes(FMT, D / 16) > 16 ? D / 32 : D / 16;
+
 template <int FMT>
 __device__ __forceinline__ Operand key_operand(const uint32_t* w, const Magic& g) {
   if constexpr (FMT == kCacheBF16) {
@@ -146,20 +157,27 @@ __device__ __forceinline__ void value_operands(const uint32_t (&w)[8][W], int h,
   }
 }
 
-// `bytes` (2 to 64) from memory into words; two bytes leave a word's upper half 0.
-template <int BYTES>
+// BYTES from memory into words, 16 at a time STRIDE bytes apart; two bytes
+// leave a word's upper half 0.  NT: memory that is read once.
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+template <bool NT, typename T>
+__device__ __forceinline__ T fetched(const char* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+  else return *reinterpret_cast<const T*>(p);
+}
+template <int BYTES, int STRIDE = 16, bool NT = false>
 __device__ __forceinline__ void fetch(const char* p, uint32_t* w) {
   if constexpr (BYTES == 2) {
-    w[0] = *reinterpret_cast<const uint16_t*>(p);
+    w[0] = fetched<NT, uint16_t>(p);
   } else if constexpr (BYTES == 4) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
+    w[0] = fetched<NT, uint32_t>(p);
   } else if constexpr (BYTES == 8) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    const u32x2_t a = fetched<NT, u32x2_t>(p);
     w[0] = a.x, w[1] = a.y;
   } else {
 #pragma unroll
     for (int i = 0; i < BYTES / 16; ++i) {
-      const uint4 a = reinterpret_cast<const uint4*>(p)[i];
+      const u32x4_t a = fetched<NT, u32x4_t>(p + i * STRIDE);
       w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
     }
   }
@@ -304,10 +322,11 @@ constexpr bool kLarge = FMT == kCacheBF16 && D == 256 && EXACT;
 
 // A workgroup of W waves: one row, up to 16 query heads of a key-value head,
 // one chunk of the length.  Its waves take steps of 32 tokens in turn.
-template <int FMT, int D, bool EXACT, int W>
+template <int FMT, int D, bool EXACT, int W, bool NT>
 __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 : 1))
     attend_kernel(AttendParams P, int share, int blocks, int splits, int chunk, int packed) {
   constexpr int E = D / 16;                     // a lane's elements of a value
+  constexpr int VR = kValueRun<FMT, D>;
   constexpr int QN = kQueryParts<FMT, EXACT>, WN = kWeightParts<FMT, EXACT>;
   constexpr int KB = cache_bytes(FMT, D / 4);   // a lane's bytes of a key
   constexpr int VB = cache_bytes(FMT, E);       // and of a value
@@ -393,7 +412,7 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const char* const p = kc + row_of(page[j], t + 16 * j) * ROW;
-      fetch<KB>(p + (uint32_t)(token * ROW + group * KB), k[j]);
+      fetch<KB, 64, NT>(p + (uint32_t)(token * ROW + group * (KB < 16 ? KB : 16)), k[j]);
     }
     if constexpr (SCALED) {
       const int64_t r0 = row_of(page[0], t), r1 = row_of(page[1], t + 16);
@@ -408,7 +427,8 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
       const char* const p = vc + row_of(page[j], t + 16 * j) * ROW;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        fetch<VB>(p + (uint32_t)((4 * group + i) * ROW + col * VB), v[4 * j + i]);
+        fetch<VB, 256, NT>(p + (uint32_t)((4 * group + i) * ROW + col * (VB < 16 ? VB : 16)),
+                            v[4 * j + i]);
     }
   };
   int t = t0 + wave * kStep;
@@ -443,7 +463,9 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
       for (int i = 0; i < 8; ++i) f[i] *= by;
       if (chunk8 == 0) query_scales[h] = ldexpf(P.scale * kLog2e, -e);
     }
-    // elements 8 chunk8 ... of a head belong to lane group chunk8 / (D / 32)
+    // the operand and the lane that these eight belong to
+    constexpr int KR = kKeyRuns<FMT, D>;
+    const int operand = chunk8 / (4 * KR) * KR + chunk8 % KR, to_group = chunk8 / KR % 4;
 #pragma unroll
     for (int part = 0; part < QN; ++part) {
       Operand o;
@@ -462,7 +484,7 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
           y -= bf16_hi(o.w[i]);
         }
       }
-      queries[part][chunk8 % (D / 32)][chunk8 / (D / 32) * 16 + h] = o;
+      queries[part][operand][to_group * 16 + h] = o;
     }
   }
   __syncthreads();
@@ -592,12 +614,13 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
       if (group == 0) tops[wave][col] = m;
       totals[wave][group][col] = total;
     }
-    // operand i's row 4 group + r of the product is element (4 group + r) E + i
+    // row 4 group + r of operand i's product is a value's element
     if ((uint32_t)(col - c0) < (uint32_t)COLS)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int i = 0; i < E; ++i) sums[wave][col - c0][(4 * group + r) * E + i] = acc[i][r];
+        for (int i = 0; i < E; ++i)
+          sums[wave][col - c0][i / VR * 16 * VR + (4 * group + r) * VR + i % VR] = acc[i][r];
     __syncthreads();
     const int here = min(COLS, heads - c0);
     for (int i = threadIdx.x; i < here * (D / 4); i += 64 * W) {
@@ -745,12 +768,26 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   // eight waves where one chunk has to do and the card is not full of them (8
   // heads of 512 tokens int8 7.8 us, four waves 8.5; 1024 items 24 and 17)
   const bool wide = splits == 1 && items <= 512;
+  // What the last-level cache (256 MiB) cannot hold until the next call goes
+  // past it: 272 MB of one sequence 51.3 us, 55.9 through the caches; 64 ragged
+  // rows of up to 553 MB together, 178 as it was, 48.3 and 50.5.  Below, it costs
+  // what the cache would have kept (80 MB of up to 272 MB 24.8 us for 22.9).
+  // Lengths spread, so of several rows half of what there may be is counted.
+  const int64_t bytes = 2 * p.rows * p.kv_heads * (int64_t)reach *
+                        cache_bytes(p.format, p.head_dim);
+  const bool once = (p.rows > 1 ? bytes / 2 : bytes) >= int64_t(256) << 20;
   const auto go = [&](auto d, auto f, auto exact) {
     constexpr int D = decltype(d)::value, F = decltype(f)::value;
     constexpr bool X = decltype(exact)::value;
     constexpr int W = kLarge<F, D, X> ? 4 : 8;
-    if (wide) attend_kernel<F, D, X, W><<<grid, 64 * W, 0, s>>>(p, share, blocks, splits, chunk, packed);
-    else attend_kernel<F, D, X, 4><<<grid, 256, 0, s>>>(p, share, blocks, splits, chunk, packed);
+    const auto run = [&](auto w, auto nt) {
+      constexpr int W2 = decltype(w)::value;
+      attend_kernel<F, D, X, W2, decltype(nt)::value>
+          <<<grid, 64 * W2, 0, s>>>(p, share, blocks, splits, chunk, packed);
+    };
+    if (wide) run(std::integral_constant<int, W>{}, std::false_type{});
+    else if (once) run(std::integral_constant<int, 4>{}, std::true_type{});
+    else run(std::integral_constant<int, 4>{}, std::false_type{});
   };
   const auto by_type = [&](auto d, auto f) {
     if (p.q_bf16 && p.y_bf16) go(d, f, std::false_type{});
