@@ -522,7 +522,6 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
         for (int n = 0; n < QN; ++n) s[j] = product<FMT>(a, q[n][c], s[j]);
       }
     }
-    float u[8], inv[8];
     if constexpr (SCALED) {
       if (lane < kStep) {
         const float ks = (float)__builtin_bit_cast(_Float16, raw_ks);
@@ -534,6 +533,15 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
         factors[wave][1][at] = __builtin_amdgcn_logf(vs);
         factors[wave][2][at] = __builtin_amdgcn_rcpf(vs);
       }
+    }
+    const bool gone[2] = {page[0] < 0, page[1] < 0};
+    if (tn < t1) {
+      page[0] = page_of(tn, id[0]);
+      page[1] = page_of(tn + 16, id[1]);
+      load_keys(tn);
+    }
+    float u[8], inv[8];
+    if constexpr (SCALED) {
       wave_lds_sync();
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -557,7 +565,7 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int at = t + 16 * (i >> 2) + 4 * group + (i & 3);
-        const bool ok = at >= R.first && at < t1 && page[i >> 2] >= 0;
+        const bool ok = at >= R.first && at < t1 && !gone[i >> 2];
         u[i] = ok ? u[i] : -__builtin_inff();
         if constexpr (SCALED) inv[i] = ok ? inv[i] : 0.f;
         if constexpr (FMT == kCacheBF16 || FMT == kCacheE4M3)
@@ -584,11 +592,6 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
     for (int i = 0; i < 8; ++i) {
       w[i] = __builtin_amdgcn_exp2f(u[i] - m);
       total = SCALED ? fmaf(w[i], inv[i], total) : total + w[i];
-    }
-    if (tn < t1) {
-      page[0] = page_of(tn, id[0]);
-      page[1] = page_of(tn + 16, id[1]);
-      load_keys(tn);
     }
     Operand p[WN];
     weight_parts<FMT, WN>(w, p);
