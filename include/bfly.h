@@ -685,8 +685,9 @@ bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint
  * nothing in reach gives y = 0 and lse = -infinity, and so does one all of
  * whose scores are -infinity.  What lies in a page behind a sequence's tokens
  * has no influence, whatever its bits are.  A NaN in q, or in a row in reach,
- * gives NaN in the results that use it and no others; an infinite q counts as
- * a NaN.
+ * gives NaN in the results that use it and no others; an infinity in q counts
+ * as a NaN, one in a key makes the results that use it unspecified.  Scales are
+ * as bfly_cache_write leaves them: not negative, and 0 with codes of 0 only.
  * The sums are held in fp32.  With bf16 q and y the weights e^(s - m) enter the
  * second product with 11 bits (quantized caches) or 16 (BFLY_KV_BF16); with an
  * fp32 q or y both products take 22 bits (24) of q and of the weights.  In

@@ -533,6 +533,10 @@ def bfly_cache_attention(q, k_cache, v_cache, tables, lens, y, k_scales=None, v_
         reach = tables.shape[1] * k_cache.shape[2] if max_len is None else max_len
         nbytes = bfly_cache_attention_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[1],
                                                       q.shape[2], reach)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            if stream is not None:  # not the stream that it is allocated on
+                workspace.record_stream(torch.cuda.ExternalStream(stream, device=q.device)
+                                        if isinstance(stream, int) else stream)
     _call(_ext().cache_attention, q, stream, scale, max_len, window, k_cache, v_cache, k_scales,
           v_scales, q, tables, lens, y, lse, workspace)

@@ -462,6 +462,9 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] *= by;
       if (chunk8 == 0) query_scales[h] = ldexpf(P.scale * kLog2e, -e);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = fmaf(f[i], 0.f, f[i]);  // an infinity counts as NaN here too
     }
     // the operand and the lane that these eight belong to
     constexpr int KR = kKeyRuns<FMT, D>;

@@ -209,3 +209,31 @@ def test_the_binding_refuses_tensors_of_the_host():
         extension().bind_cache(0, 1, 2)
     with pytest.raises(TypeError):
         extension().bind_cache(1, 2)
+
+
+def test_the_attention_workspace_holds_its_chunks(L):
+    # how a call's lengths are cut, by itself: head_dim + 4 fp32 to a chunk of a head
+    def chunks(rows, heads, kv, d, reach):
+        share = heads // kv
+        items = rows * kv * -(-share // 16)
+        if reach <= 512 or (reach <= 1024 and items >= 128):
+            return 1
+        chunk = 256 if min(share, 16) * d >= 2048 else 128
+        if rows == 1:
+            chunk = max(chunk, -(-(-(-items * reach // 512)) // 128) * 128)
+        else:
+            while chunk < 512 and items * -(-reach // chunk) > 2048:
+                chunk *= 2
+            if items * -(-reach // chunk) > 8192:
+                chunk = max(chunk, -(-(-(-items * reach // 8192)) // 128) * 128)
+        return -(-reach // chunk)
+
+    for rows in (1, 2, 3, 7, 16, 33, 64, 100, 256, 257, 1000, 5000, 70000):
+        for heads, kv in ((1, 1), (4, 1), (16, 1), (17, 1), (32, 8), (32, 32), (64, 4), (40, 40)):
+            for d in (64, 256):
+                for most in (1, 100, 512, 513, 1000, 1025, 3000, 8192, 50000, 131072, 1 << 22):
+                    need = B.bfly_cache_attention_workspace_bytes(rows, heads, kv, d, most)
+                    for reach in {most, min(most, 700), min(most, 2000), min(most, 30000)}:
+                        n = chunks(rows, heads, kv, d, reach)
+                        used = 0 if n == 1 else 4 * (d + 4) * rows * heads * n
+                        assert used <= need, (rows, heads, kv, d, most, reach)
