@@ -316,14 +316,15 @@ __device__ __forceinline__ float log_sum(float top, float l) {
   return l == 0.f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(l)) / kLog2e;
 }
 
-// More registers than two waves to a SIMD may have.
-template <int FMT, int D, bool EXACT>
-constexpr bool kLarge = FMT == kCacheBF16 && D == 256 && EXACT;
+// Whether a step's registers leave none for the queries, which then stay in LDS
+// (24 rows of a window of 2047 15.7 us; 16.4 with 28 bytes a lane in scratch).
+template <int FMT, int D>
+constexpr bool kQueriesInLds = FMT == kCacheBF16 && D == 256;
 
 // A workgroup of W waves: one row, up to 16 query heads of a key-value head,
 // one chunk of the length.  Its waves take steps of 32 tokens in turn.
 template <int FMT, int D, bool EXACT, int W, bool NT>
-__global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 : 1))
+__global__ void __launch_bounds__(64 * W, 2)
     attend_kernel(AttendParams P, int share, int blocks, int splits, int chunk, int packed) {
   constexpr int E = D / 16;                     // a lane's elements of a value
   constexpr int VR = kValueRun<FMT, D>;
@@ -339,9 +340,11 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
   constexpr int SUMS = W * COLS * (D + 4) * 4, QUERIES = QN * (D / 32) * 64 * 16;
   __shared__ float factors[W][3][kStep];        // of a step's tokens: ks, log2 vs, 1 / vs
   __shared__ float tops[W][kHeads], totals[W][4][kHeads], query_scales[kHeads];
-  __shared__ __align__(16) char room[SUMS > QUERIES ? SUMS : QUERIES];
+  // a wave may join its results while another still reads queries from LDS
+  constexpr bool IN_LDS = kQueriesInLds<FMT, D>;
+  __shared__ __align__(16) char room[IN_LDS ? SUMS + QUERIES : SUMS > QUERIES ? SUMS : QUERIES];
   float(*const sums)[COLS][D + 4] = reinterpret_cast<float(*)[COLS][D + 4]>(room);
-  Operand(*const queries)[D / 32][64] = reinterpret_cast<Operand(*)[D / 32][64]>(room);
+  Operand(*const queries)[D / 32][64] = reinterpret_cast<Operand(*)[D / 32][64]>(room + (IN_LDS ? SUMS : 0));
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int col = lane & 15, group = lane >> 4;
@@ -491,11 +494,12 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
     }
   }
   __syncthreads();
-  Operand q[QN][D / 32];
+  Operand q[IN_LDS ? 1 : QN][IN_LDS ? 1 : D / 32];
+  if constexpr (!IN_LDS)
 #pragma unroll
-  for (int part = 0; part < QN; ++part)
+    for (int part = 0; part < QN; ++part)
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) q[part][c] = queries[part][c][lane];
+      for (int c = 0; c < D / 32; ++c) q[part][c] = queries[part][c][lane];
   const float qscale = SCALED ? query_scales[col] : P.scale * kLog2e;
 
   Magic magic;
@@ -514,16 +518,22 @@ __global__ void __launch_bounds__(64 * W, (W == 4 && !kLarge<FMT, D, EXACT> ? 2 
     // a step that has tokens nobody may look at
     const bool edge = t < R.first || t + kStep > t1 || page[0] < 0 || page[1] < 0;
 
-    f32x4 s[2];
+    if constexpr (IN_LDS) wave_lds_sync();      // read again in every step, not kept
+    f32x4 s[2] = {};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < D / 32; ++c) {
+      Operand a[2];
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const Operand a = key_operand<FMT>(&k[j][c * kWords8<FMT>], magic);
+      for (int j = 0; j < 2; ++j) a[j] = key_operand<FMT>(&k[j][c * kWords8<FMT>], magic);
 #pragma unroll
-        for (int n = 0; n < QN; ++n) s[j] = product<FMT>(a, q[n][c], s[j]);
+      for (int n = 0; n < QN; ++n) {
+        Operand with;
+        if constexpr (IN_LDS) with = queries[n][c][lane];
+        else with = q[n][c];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) s[j] = product<FMT>(a[j], with, s[j]);
       }
+      if constexpr (IN_LDS) __builtin_amdgcn_sched_barrier(0);  // nor all of them at once
     }
     if constexpr (SCALED) {
       if (lane < kStep) {
@@ -785,7 +795,7 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   const auto go = [&](auto d, auto f, auto exact) {
     constexpr int D = decltype(d)::value, F = decltype(f)::value;
     constexpr bool X = decltype(exact)::value;
-    constexpr int W = kLarge<F, D, X> ? 4 : 8;
+    constexpr int W = 8;
     const auto run = [&](auto w, auto nt) {
       constexpr int W2 = decltype(w)::value;
       attend_kernel<F, D, X, W2, decltype(nt)::value>
