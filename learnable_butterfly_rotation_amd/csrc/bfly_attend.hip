@@ -411,11 +411,20 @@ __global__ void __launch_bounds__(64 * W, 2)
   uint16_t raw_ks, raw_vs;    // lane t: token t's scales (lanes above 31 repeat them)
   int page[2];
   const bool upper = lane & 16;
-  const auto load_keys = [&](int t) {
+  // Of a wave's first tiles the rows in front of what is in reach and behind it
+  // are fetched as the first and the last of that: a short sequence touches no
+  // row that has no part in it (113 rows of up to 6 tokens of 18 heads of 256
+  // bf16 27.2 -> 20.1 us, with one wave to a workgroup).  A long one's last tiles are not worth the registers.
+  const auto inside = [&](auto first, int i, int t) {
+    if constexpr (!decltype(first)::value) return i;
+    return max(min(i, min(max(t1 - 1 - t, 0), 15)), min(max(R.first - t, 0), 15));
+  };
+  const auto load_keys = [&](auto first, int t) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const char* const p = kc + row_of(page[j], t + 16 * j) * ROW;
-      fetch<KB, 64, NT>(p + (uint32_t)(token * ROW + group * (KB < 16 ? KB : 16)), k[j]);
+      fetch<KB, 64, NT>(p + (uint32_t)(inside(first, token, t + 16 * j) * ROW +
+                                       group * (KB < 16 ? KB : 16)), k[j]);
     }
     if constexpr (SCALED) {
       const int64_t r0 = row_of(page[0], t), r1 = row_of(page[1], t + 16);
@@ -424,28 +433,29 @@ __global__ void __launch_bounds__(64 * W, 2)
       raw_vs = P.v_scales[r];
     }
   };
-  const auto load_values = [&](int t) {
+  const auto load_values = [&](auto first, int t) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const char* const p = vc + row_of(page[j], t + 16 * j) * ROW;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        fetch<VB, 256, NT>(p + (uint32_t)((4 * group + i) * ROW + col * (VB < 16 ? VB : 16)),
-                            v[4 * j + i]);
+        fetch<VB, 256, NT>(p + (uint32_t)(inside(first, 4 * group + i, t + 16 * j) * ROW +
+                                          col * (VB < 16 ? VB : 16)), v[4 * j + i]);
     }
   };
   int t = t0 + wave * kStep;
   if (t < t1) {
     page[0] = page_of(t, P.window == 0 ? early[0] : entry(t));
     page[1] = page_of(t + 16, P.window == 0 ? early[1] : entry(t + 16));
-    load_keys(t);
-    load_values(t);
+    load_keys(std::true_type{}, t);
+    load_values(std::true_type{}, t);
   }
 
   // from each thread's eight elements to the operands of the waves
 #pragma unroll
   for (int n = 0; n < QC; ++n) {
     const int c = threadIdx.x + n * 64 * W, h = c / QL, chunk8 = c % QL;
+    if (n * 64 * W >= heads * QL) break;        // columns behind the heads hold anything
     if (64 * W > kHeads * QL && h >= kHeads) break;
     float f[8];
 #pragma unroll
@@ -551,7 +561,7 @@ __global__ void __launch_bounds__(64 * W, 2)
     if (tn < t1) {
       page[0] = page_of(tn, id[0]);
       page[1] = page_of(tn + 16, id[1]);
-      load_keys(tn);
+      load_keys(std::false_type{}, tn);
     }
     float u[8], inv[8];
     if constexpr (SCALED) {
@@ -619,7 +629,7 @@ __global__ void __launch_bounds__(64 * W, 2)
         for (int n = 0; n < WN; ++n)
           acc[h * RUN + i] = product<FMT>(x[i], p[n], acc[h * RUN + i]);
     }
-    if (tn < t1) load_values(tn);
+    if (tn < t1) load_values(std::false_type{}, tn);
   }
 
   // the waves' results joined, COLS heads at a time
@@ -781,9 +791,6 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   const unsigned across = (unsigned)(p.kv_heads * blocks);
   const dim3 grid = packed ? dim3(across, (unsigned)(p.rows * splits))
                            : dim3((unsigned)items, (unsigned)splits);
-  // eight waves where one chunk has to do and the card is not full of them (8
-  // heads of 512 tokens int8 7.8 us, four waves 8.5; 1024 items 24 and 17)
-  const bool wide = splits == 1 && items <= 512;
   // What the last-level cache (256 MiB) cannot hold until the next call goes
   // past it: 272 MB of one sequence 51.3 us, 55.9 through the caches; 64 ragged
   // rows of up to 553 MB together, 178 as it was, 48.3 and 50.5.  Below, it costs
@@ -791,17 +798,27 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   // Lengths spread, so of several rows half of what there may be is counted.
   const int64_t bytes = 2 * p.rows * p.kv_heads * (int64_t)reach *
                         cache_bytes(p.format, p.head_dim);
-  const bool once = (p.rows > 1 ? bytes / 2 : bytes) >= int64_t(256) << 20;
+  const bool once = reach > 128 && (p.rows > 1 ? bytes / 2 : bytes) >= int64_t(256) << 20;
+  // Waves of a workgroup that has a row's whole length.  One where there are more
+  // rows and heads than the card has room for and their lengths are short: 904
+  // items of 32 tokens int8 5.1 us, with four waves 7.5, 4096 of 256 tokens 30 and
+  // 34; but 904 of 256 tokens 14.5 and 11.0.  Eight where each of up to 256 has a
+  // CU to itself and more than one round of four: 256 items of 512 tokens 9.2,
+  // with four 10.6, of 256 tokens 6.2 and 6.3; 800 items int4 14 and 9.
+  const int waves = splits > 1 || once                             ? 4
+                    : items > 8 * (int64_t)std::max(reach, kStep) ? 1
+                    : reach > 256 && items <= 256                 ? 8
+                                                                  : 4;
   const auto go = [&](auto d, auto f, auto exact) {
     constexpr int D = decltype(d)::value, F = decltype(f)::value;
     constexpr bool X = decltype(exact)::value;
-    constexpr int W = 8;
     const auto run = [&](auto w, auto nt) {
       constexpr int W2 = decltype(w)::value;
       attend_kernel<F, D, X, W2, decltype(nt)::value>
           <<<grid, 64 * W2, 0, s>>>(p, share, blocks, splits, chunk, packed);
     };
-    if (wide) run(std::integral_constant<int, W>{}, std::false_type{});
+    if (waves == 1) run(std::integral_constant<int, 1>{}, std::false_type{});
+    else if (waves == 8) run(std::integral_constant<int, 8>{}, std::false_type{});
     else if (once) run(std::integral_constant<int, 4>{}, std::true_type{});
     else run(std::integral_constant<int, 4>{}, std::false_type{});
   };
