@@ -621,8 +621,8 @@ typedef enum {
  *                       BFLY_KV_BF16)
  * A slot is the place of one token, page * page_size + place in the page.
  * Sizes: head_dim 64, 128 or 256; page_size a power of two from 16 to 65536;
- * kv_heads <= 4096; pages * page_size < 2^31.  k_cache and v_cache 16-byte
- * aligned, scales 2-byte.
+ * kv_heads <= 4096; pages * page_size < 2^31; tokens * kv_heads * head_dim of
+ * one call <= 2^34.  k_cache and v_cache 16-byte aligned, scales 2-byte.
  *
  * bfly_cache_write: the keys and values of `tokens` tokens into their slots.
  *   k, v    : [tokens] rows of kv_heads * head_dim elements of dt, k_stride
@@ -668,7 +668,7 @@ bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint
  *             pages
  *   lens    : int32 [rows], the tokens of each sequence, the new one included
  *             (write it first); below 0 counts as 0, above max_len as max_len.
- *             Table entries behind them are not read
+ *             What the table holds behind them has no influence
  *   window  : the last `window` of them are in reach, all for 0
  *   max_len : a bound of the lengths, at most table_width * page_size, that
  *             sizes the launch and the workspace: the closer it is, the better
@@ -689,13 +689,14 @@ bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint
  * as a NaN, one in a key makes the results that use it unspecified.  Scales are
  * as bfly_cache_write leaves them: not negative, and 0 with codes of 0 only.
  * The sums are held in fp32.  With bf16 q and y the weights e^(s - m) enter the
- * second product with 11 bits (quantized caches) or 16 (BFLY_KV_BF16); with an
- * fp32 q or y both products take 22 bits (24) of q and of the weights.  In
- * calls of the same sizes a row's result does not depend on the other rows',
- * and is the same from run to run.
+ * second product with 11 bits (quantized caches) or 15 (BFLY_KV_BF16); with an
+ * fp32 q or y with 22, and q enters the first with 22 (24).  Over a quantized
+ * cache a weight is held to 2^-33 of the largest at best.  In calls of the
+ * same sizes a row's result does not depend on the other rows', and is the same
+ * from run to run.
  * y and lse share no memory with anything else.
- * Sizes as above, and heads a multiple of kv_heads up to 65536, rows <= 2^24,
- * rows * heads <= 2^28, max_len <= 2^30.  q and y 16-byte aligned, tables, lens
+ * Sizes as above, and heads a multiple of kv_heads up to 65536, rows * heads
+ * below 2^24, max_len <= 2^30.  q and y 16-byte aligned, tables, lens
  * and lse 4.  rows == 0 is a no-op.
  * Errors: BFLY_ERR_NULL, BFLY_ERR_DTYPE, BFLY_ERR_QUANT (format), BFLY_ERR_SIZE
  * (also: heads not a multiple of kv_heads, max_len beyond the tables, scale not

@@ -1143,7 +1143,8 @@ static bfly_status cache_args(const void* k, int64_t k_stride, const void* v, in
   if (st != BFLY_OK) return st;
   const int64_t row = (int64_t)kv_heads * head_dim;
   if (k_stride < row || v_stride < row) return BFLY_ERR_SIZE;
-  if (k_stride > INT32_MAX || v_stride > INT32_MAX || tokens > (int64_t(1) << 31) / kv_heads ||
+  // (a grid's threads are fewer than 2^32)
+  if (k_stride > INT32_MAX || v_stride > INT32_MAX || tokens > (int64_t(1) << 34) / row ||
       !rows_fit(tokens, (int32_t)k_stride) || !rows_fit(tokens, (int32_t)v_stride))
     return BFLY_ERR_UNSUPPORTED;
   if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
@@ -1210,7 +1211,7 @@ static bfly_status attend_sizes(int64_t rows, int32_t heads, int32_t kv_heads, i
     return BFLY_ERR_SIZE;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return BFLY_ERR_UNSUPPORTED;
   if (heads > 65536 || kv_heads > 4096 || rows > (int64_t(1) << 24) ||
-      rows * heads > (int64_t(1) << 28) || max_len > (1 << 30))
+      rows * heads >= (int64_t(1) << 24) || max_len > (1 << 30))
     return BFLY_ERR_UNSUPPORTED;
   return BFLY_OK;
 }

@@ -230,11 +230,11 @@ __device__ __forceinline__ void weight_parts(const float (&w)[8], Operand (&out)
   }
 }
 
-// Parts of the queries and of the weights: with bf16 queries and results one
-// fp16 part of each is exact (queries) or rounds a weight by 2^-12 (a quarter
-// of what the result's own rounding does); a bf16 weight of one part would
-// round by 2^-9, as much as the result itself, so it has two.  fp32 results
-// take 22 (fp16) or 24 (bf16) bits of both.
+// Parts of the queries and of the weights.  With bf16 queries and results one
+// fp16 part of each is exact (queries) or off by 2^-11 (a weight, where the
+// result's own rounding is 2^-8); a bf16 weight of one part would be off by
+// 2^-8 as well, so it has two (2^-15).  fp32 queries or results: 2^-22 of a
+// weight, 2^-22 (fp16) or 2^-24 (bf16) of a query.
 template <int FMT, bool EXACT>
 constexpr int kQueryParts = !EXACT ? 1 : FMT == kCacheBF16 ? 3 : 2;
 template <int FMT, bool EXACT>
@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(64 * W, 2)
   constexpr bool IN_LDS = kQueriesInLds<FMT, D>;
   __shared__ __align__(16) char room[IN_LDS ? SUMS + QUERIES : SUMS > QUERIES ? SUMS : QUERIES];
   float(*const sums)[COLS][D + 4] = reinterpret_cast<float(*)[COLS][D + 4]>(room);
-  Operand(*const queries)[D / 32][64] = reinterpret_cast<Operand(*)[D / 32][64]>(room + (IN_LDS ? SUMS : 0));
+  Operand(*const queries)[D / 32][64] =
+      reinterpret_cast<Operand(*)[D / 32][64]>(room + (IN_LDS ? SUMS : 0));
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int col = lane & 15, group = lane >> 4;
@@ -354,11 +355,11 @@ __global__ void __launch_bounds__(64 * W, 2)
   if (packed) {
     if (!find_chunk(P, chunk, blockIdx.y, row32, split)) return;
   } else if (P.rows > 1) {
-    row32 = x / (P.kv_heads * blocks);
+    row32 = blockIdx.x / (uint32_t)(P.kv_heads * blocks);
     x -= row32 * (P.kv_heads * blocks);
   }
   const int64_t row = row32;
-  const int kvh = blocks == 1 ? x : x / blocks, block = x - kvh * blocks;
+  const int kvh = blocks == 1 ? x : (uint32_t)x / (uint32_t)blocks, block = x - kvh * blocks;
   const int head0 = kvh * share + block * kHeads;            // the block's first query head
   const int heads = min(kHeads, share - block * kHeads);     // and how many it has
   const int shift = P.page_shift, in_page = (1 << shift) - 1;
@@ -401,10 +402,6 @@ __global__ void __launch_bounds__(64 * W, 2)
   const char* const kc = static_cast<const char*>(P.k_cache);
   const char* const vc = static_cast<const char*>(P.v_cache);
 
-  // row r of a tile's product is its token 4 (r % 4) + r / 4 (and the other way
-  // round), so that the tokens 4 i + group that a lane weighs lie, for each i,
-  // next to each other in memory
-  const int token = col;
   // what a step needs: the next step's keys go out as soon as this one's are
   // used, its values likewise
   uint32_t k[2][KW], v[8][VW];
@@ -414,7 +411,8 @@ __global__ void __launch_bounds__(64 * W, 2)
   // Of a wave's first tiles the rows in front of what is in reach and behind it
   // are fetched as the first and the last of that: a short sequence touches no
   // row that has no part in it (113 rows of up to 6 tokens of 18 heads of 256
-  // bf16 27.2 -> 20.1 us, with one wave to a workgroup).  A long one's last tiles are not worth the registers.
+  // bf16 27.2 -> 20.1 us, with one wave to a workgroup).  A long one's last tiles
+  // are not worth the registers.
   const auto inside = [&](auto first, int i, int t) {
     if constexpr (!decltype(first)::value) return i;
     return max(min(i, min(max(t1 - 1 - t, 0), 15)), min(max(R.first - t, 0), 15));
@@ -423,7 +421,7 @@ __global__ void __launch_bounds__(64 * W, 2)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const char* const p = kc + row_of(page[j], t + 16 * j) * ROW;
-      fetch<KB, 64, NT>(p + (uint32_t)(inside(first, token, t + 16 * j) * ROW +
+      fetch<KB, 64, NT>(p + (uint32_t)(inside(first, col, t + 16 * j) * ROW +
                                        group * (KB < 16 ? KB : 16)), k[j]);
     }
     if constexpr (SCALED) {
@@ -505,11 +503,13 @@ __global__ void __launch_bounds__(64 * W, 2)
   }
   __syncthreads();
   Operand q[IN_LDS ? 1 : QN][IN_LDS ? 1 : D / 32];
-  if constexpr (!IN_LDS)
+  if constexpr (!IN_LDS) {
 #pragma unroll
     for (int part = 0; part < QN; ++part)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) q[part][c] = queries[part][c][lane];
+    if constexpr (W > 1) __syncthreads();       // a wave without tokens is at the joining next
+  }
   const float qscale = SCALED ? query_scales[col] : P.scale * kLog2e;
 
   Magic magic;
@@ -551,10 +551,9 @@ __global__ void __launch_bounds__(64 * W, 2)
         // a value scale of 0 stands for a row of codes 0: any scale will do
         float vs = (float)__builtin_bit_cast(_Float16, raw_vs);
         vs = vs == 0.f ? 1.f : vs;
-        const int at = (lane & 16) + token;
-        factors[wave][0][at] = ks;
-        factors[wave][1][at] = __builtin_amdgcn_logf(vs);
-        factors[wave][2][at] = __builtin_amdgcn_rcpf(vs);
+        factors[wave][0][lane] = ks;
+        factors[wave][1][lane] = __builtin_amdgcn_logf(vs);
+        factors[wave][2][lane] = __builtin_amdgcn_rcpf(vs);
       }
     }
     const bool gone[2] = {page[0] < 0, page[1] < 0};
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(N) join_kernel(AttendParams P, int splits, int
       y[n] = *reinterpret_cast<const f32x4*>(&part[i].y[d]);
     }
     if (i0 == g) {
-      const Reach R = reach_of(P, uniform_word(P.lens, to / P.heads));
+      const Reach R = reach_of(P, uniform_word(P.lens, blockIdx.x / (uint32_t)P.heads));
       used = (R.end - R.base + chunk - 1) / chunk;
     }
 #pragma unroll
@@ -795,10 +794,11 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   // past it: 272 MB of one sequence 51.3 us, 55.9 through the caches; 64 ragged
   // rows of up to 553 MB together, 178 as it was, 48.3 and 50.5.  Below, it costs
   // what the cache would have kept (80 MB of up to 272 MB 24.8 us for 22.9).
-  // Lengths spread, so of several rows half of what there may be is counted.
-  const int64_t bytes = 2 * p.rows * p.kv_heads * (int64_t)reach *
-                        cache_bytes(p.format, p.head_dim);
-  const bool once = reach > 128 && (p.rows > 1 ? bytes / 2 : bytes) >= int64_t(256) << 20;
+  // Lengths spread, so of several rows half of what there may be is counted; what
+  // several workgroups read, for more than 16 query heads, stays.
+  const double bytes = 2.0 * (double)p.rows * p.kv_heads * reach * cache_bytes(p.format, p.head_dim);
+  const bool once = blocks == 1 && reach > 128 &&
+                    (p.rows > 1 ? bytes / 2 : bytes) >= 256.0 * (1 << 20);
   // Waves of a workgroup that has a row's whole length.  One where there are more
   // rows and heads than the card has room for and their lengths are short: 904
   // items of 32 tokens int8 5.1 us, with four waves 7.5, 4096 of 256 tokens 30 and

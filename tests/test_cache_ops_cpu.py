@@ -53,7 +53,7 @@ def test_cache_rows_refusals(L, write):
         assert call(**{name: value}, **more) == UNSUPPORTED, (name, value)
     assert call(pages=1 << 15, page=65536) == UNSUPPORTED       # 2^31 slots
     assert call(tokens=0, pages=(1 << 15) - 1, page=65536) == OK
-    assert call(tokens=(1 << 28) + 1) == UNSUPPORTED            # 2^31 rows of 8 heads
+    assert call(tokens=(1 << 24) + 1) == UNSUPPORTED            # 2^34 elements of 8 * 128
     for name in ("k", "v", "kc", "vc"):
         assert call(**{name: 0x10008}) == ALIGN, name
     assert call(ks=1028) == ALIGN and call(vs=1025) == ALIGN
@@ -85,7 +85,7 @@ def test_cache_attention_refusals(L):
     for scale in (float("nan"), float("inf"), -float("inf")):
         assert call(scale=scale) == SIZE
     for name, value in (("d", 32), ("d", 96), ("page", 48), ("kv", 4097), ("rows", (1 << 24) + 1),
-                        ("heads", 1 << 17), ("rows", 1 << 24), ("qs", 1 << 32)):
+                        ("heads", 1 << 17), ("rows", 1 << 19), ("qs", 1 << 32)):
         more = {"heads": 4097, "qs": 1 << 24} if name == "kv" else {}
         assert call(**{name: value}, **more) == UNSUPPORTED, (name, value)
     assert call(most=(1 << 30) + 1, width=1 << 27) == UNSUPPORTED
@@ -110,7 +110,7 @@ def test_cache_attention_workspace(L):
     assert attend(L, **long, wsb=need, lens=0x10002) == ALIGN   # past the workspace's checks
     assert attend(L, ws=None, wsb=0, most=20, lens=0x10002) == ALIGN
     # one for the largest call serves the others
-    steps = list(range(1, 300)) + [1 << b for b in range(9, 21)]
+    steps = list(range(1, 300)) + [1 << b for b in range(9, 18)]
     for heads, kv, d, most in ((32, 8, 128, 8192), (32, 32, 64, 1000), (1, 1, 256, 1 << 20),
                                (40, 8, 128, 300), (64, 1, 256, 131072)):
         for sizes in ([size(r, heads, kv, d, most) for r in steps],

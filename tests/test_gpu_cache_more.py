@@ -326,3 +326,23 @@ def test_the_library_allocates_nothing():
         b.run(tables=t, lens=n, workspace=ws)
     torch.cuda.synchronize()
     assert (torch.cuda.mem_get_info()[0], torch.cuda.memory_stats()["allocation.all.allocated"]) == before
+
+
+def test_as_many_rows_as_there_may_be():
+    """2^24 - 1 rows of one head and one token or none: y is the token's value."""
+    rows, d, page, pages = (1 << 24) - 1, 64, 16, 10
+    c = Cache("int8", pages, 1, page, d, junk=False)
+    slots = torch.arange(pages * page, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((pages * page, 1, d), device="cuda") for _ in "kv")
+    c.write(k, v, slots)
+    c.read(slots, k, v)
+    at = torch.arange(rows, dtype=torch.int32, device="cuda")
+    tables, lens = (at % pages)[:, None].contiguous(), at // 3 % 2
+    q = torch.zeros((rows, 1, d), dtype=BF16, device="cuda")
+    y = torch.full_like(q, 7.0)
+    B.bfly_cache_attention(q, c.k, c.v, tables, lens, y, **c.scales)
+    first = v[::page].to(BF16)                       # of every page
+    for part in torch.arange(rows, device="cuda").split(1 << 22):
+        want = torch.where((lens[part] > 0)[:, None, None], first[tables[part, 0].long()], 0.0)
+        # 448 codes and one weight of 1 over itself: the result's rounding only
+        assert ((y[part] - want).abs() <= 2.0 ** -7 * want.abs()).all()
