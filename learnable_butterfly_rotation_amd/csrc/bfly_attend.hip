@@ -335,9 +335,13 @@ __global__ void __launch_bounds__(64 * W, 2)
   constexpr int ROW = cache_bytes(FMT, D);
   constexpr bool SCALED = FMT != kCacheBF16;
   constexpr int ROUND = W * kStep;
-  // heads whose results are joined at a time
-  constexpr int COLS = W * D > 512 ? kHeads * 512 / (W * D) : kHeads;
-  constexpr int SUMS = W * COLS * (D + 4) * 4, QUERIES = QN * (D / 32) * 64 * 16;
+  // heads whose results are joined at a time, as many as leave room for two
+  // workgroups in a CU's 160 KiB (24 rows of a window of 2047, 16 heads of 256:
+  // eight heads 16.2 us, sixteen 15.9), less of eight waves (321 tokens 6.33, 6.39)
+  constexpr int QUERIES = QN * (D / 32) * 64 * 16, EACH = W * (D + 4) * 4;
+  constexpr int MOST = ((W > 4 ? 48 : 77) * 1024 - QUERIES) / EACH;
+  constexpr int COLS = MOST >= kHeads ? kHeads : MOST >= kHeads / 2 ? kHeads / 2 : kHeads / 4;
+  constexpr int SUMS = COLS * EACH;
   __shared__ float factors[W][3][kStep];        // of a step's tokens: ks, log2 vs, 1 / vs
   __shared__ float tops[W][kHeads], totals[W][4][kHeads], query_scales[kHeads];
   // a wave may join its results while another has yet to read the queries: they
