@@ -184,11 +184,14 @@ __device__ __forceinline__ void fetch(const char* p, uint32_t* w) {
 }
 
 // The four groups of 16 lanes brought together: f of the lanes l, l ^ 16,
-// l ^ 32, l ^ 48.
+// l ^ 32, l ^ 48.  A swap of two copies leaves the even groups (the lower half)
+// in one and the odd ones (the upper half) in the other.
 template <typename F>
 __device__ __forceinline__ float across_groups(float v, F f) {
-  v = f(v, __shfl_xor(v, 16));
-  return f(v, __shfl_xor(v, 32));
+  const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = f(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 
 // N fp16 (bf16 for a bf16 cache) parts of eight values that add up to them.
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(64 * W, 2)
   constexpr int COLS = MOST >= kHeads ? kHeads : MOST >= kHeads / 2 ? kHeads / 2 : kHeads / 4;
   constexpr int SUMS = COLS * EACH;
   __shared__ float factors[W][3][kStep];        // of a step's tokens: ks, log2 vs, 1 / vs
-  __shared__ float tops[W][kHeads], totals[W][4][kHeads], query_scales[kHeads];
+  __shared__ float query_scales[kHeads];
   // a wave may join its results while another has yet to read the queries: they
   // share no memory (a barrier instead: 321 tokens 6.45 us for 6.30)
   constexpr bool IN_LDS = kQueriesInLds<FMT, D>;
@@ -635,37 +638,37 @@ __global__ void __launch_bounds__(64 * W, 2)
     if (tn < t1) load_values(std::false_type{}, tn);
   }
 
-  // the waves' results joined, COLS heads at a time
+  // the waves' results joined, COLS heads at a time; behind a head's sums its
+  // maximum and total
+  total = across_groups(total, [](float a, float b) { return a + b; });
 #pragma unroll 1
   for (int c0 = 0; c0 < heads; c0 += COLS) {
     if (c0 > 0) __syncthreads();
-    if (c0 == 0) {
-      if (group == 0) tops[wave][col] = m;
-      totals[wave][group][col] = total;
-    }
     // row 4 group + r of operand i's product is a value's element
-    if ((uint32_t)(col - c0) < (uint32_t)COLS)
+    if ((uint32_t)(col - c0) < (uint32_t)COLS) {
+      float* const to = sums[wave][col - c0];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int i = 0; i < E; ++i)
-          sums[wave][col - c0][i / VR * 16 * VR + (4 * group + r) * VR + i % VR] = acc[i][r];
+          to[i / VR * 16 * VR + (4 * group + r) * VR + i % VR] = acc[i][r];
+      if (group == 0) to[D] = m, to[D + 1] = total;
+    }
     __syncthreads();
     const int here = min(COLS, heads - c0);
     for (int i = threadIdx.x; i < here * (D / 4); i += 64 * W) {
-      const int x = i / (D / 4), h = c0 + x, d = i % (D / 4) * 4;
-      float top = tops[0][h], l = 0.f;
+      const int x = i / (D / 4), d = i % (D / 4) * 4;
+      float top = sums[0][x][D], l = 0.f;
 #pragma unroll
-      for (int n = 1; n < W; ++n) top = fmaxf(top, tops[n][h]);
+      for (int n = 1; n < W; ++n) top = fmaxf(top, sums[n][x][D]);
       f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int n = 0; n < W; ++n) {
-        const float by = __builtin_amdgcn_exp2f(tops[n][h] - top);
-        const float sum = (totals[n][0][h] + totals[n][1][h]) + (totals[n][2][h] + totals[n][3][h]);
-        l = fmaf(sum, by, l);
+        const float by = __builtin_amdgcn_exp2f(sums[n][x][D] - top);
+        l = fmaf(sums[n][x][D + 1], by, l);
         o += *reinterpret_cast<const f32x4*>(&sums[n][x][d]) * by;
       }
-      const int64_t to = row * P.heads + head0 + h;
+      const int64_t to = row * P.heads + head0 + c0 + x;
       if (splits > 1) {
         Partial<D>* const result = reinterpret_cast<Partial<D>*>(P.partials) + to * splits + split;
         *reinterpret_cast<f32x4*>(&result->y[d]) = o;
