@@ -756,7 +756,10 @@ struct Cut {
 constexpr int kOneChunk = 512, kAlone = 512, kMost = 8192;
 Cut cut_of(int64_t rows, int64_t items, int share, int head_dim, int reach) {
   if (reach <= kOneChunk || (reach <= 2 * kOneChunk && items >= 128)) return {reach, 1};
-  const auto whole = [](int64_t v) { return (int)((v + 127) / 128 * 128); };
+  // a multiple of 128 tokens; no more than all (items times reach passes 32 bits)
+  const auto whole = [&](int64_t v) {
+    return (int)((std::min<int64_t>(v, reach) + 127) / 128 * 128);
+  };
   const int least = std::min(share, kHeads) * head_dim >= 2048 ? 256 : 128;
   const auto splits = [&](int chunk) { return (reach + chunk - 1) / chunk; };
   int chunk = least;

@@ -346,3 +346,29 @@ def test_as_many_rows_as_there_may_be():
         want = torch.where((lens[part] > 0)[:, None, None], first[tables[part, 0].long()], 0.0)
         # 448 codes and one weight of 1 over itself: the result's rounding only
         assert ((y[part] - want).abs() <= 2.0 ** -7 * want.abs()).all()
+
+
+@pytest.mark.parametrize("rows,heads", [(512, 32), (1, 1024)])
+def test_tables_as_wide_as_they_may_be(rows, heads):
+    """Tables of 2^30 tokens, whose product with rows and heads passes 2^44, and
+    short sequences: no bound of their lengths is given."""
+    d, page, most = 64, 65536, 100
+    c = Cache("int4", 1, heads, page, d, junk=False)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    slots = torch.arange(most, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((most, heads, d), generator=g, device="cuda") for _ in "kv")
+    c.write(k, v, slots)
+    c.read(slots, k, v)
+    tables = torch.full((rows, 16384), -1, dtype=torch.int32, device="cuda")
+    tables[:, 0] = 0
+    lens = torch.arange(rows, dtype=torch.int32) * 37 % (most + 1)
+    lens[0] = most
+    q = torch.randn((rows, heads, d), generator=g, device="cuda")
+    y, lse = torch.full_like(q, 7.0), torch.empty((rows, heads), device="cuda")
+    B.bfly_cache_attention(q, c.k, c.v, tables, lens.cuda(), y, lse=lse, **c.scales)
+    for r in sorted({0, 1, rows // 2, rows - 1} & set(range(rows))):
+        want, wl = reference(q[r:r + 1], k[None], v[None], lens[r:r + 1], d ** -0.5)
+        size, _ = reference(q[r:r + 1], k[None], v[None].abs(), lens[r:r + 1], d ** -0.5)
+        # as for many rows: scores 2^-16, sums of 100 terms 2^-17
+        assert ((y[r:r + 1].double() - want).abs() <= 2.0 ** -13 * size + 2.0 ** -40).all(), r
+        assert (lse[r:r + 1].double() - wl).abs().max() <= 2.0 ** -13
