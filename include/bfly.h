@@ -691,7 +691,8 @@ bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint
  * The sums are held in fp32.  With bf16 q and y the weights e^(s - m) enter the
  * second product with 11 bits (quantized caches) or 15 (BFLY_KV_BF16); with an
  * fp32 q or y with 22, and q enters the first with 22 (24).  Over a quantized
- * cache a weight is held to 2^-33 of the largest at best.  In calls of the
+ * cache a weight times its value's scale is held to 2^-33 of the largest such
+ * product at best (a scale of 0 counts as 2^-60 there).  In calls of the
  * same sizes a row's result does not depend on the other rows', and is the same
  * from run to run.
  * y and lse share no memory with anything else.

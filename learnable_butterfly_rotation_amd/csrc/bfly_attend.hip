@@ -555,9 +555,14 @@ __global__ void __launch_bounds__(64 * W, 2)
     if constexpr (SCALED) {
       if (lane < kStep) {
         const float ks = (float)__builtin_bit_cast(_Float16, raw_ks);
-        // a value scale of 0 stands for a row of codes 0: any scale will do
+        // A value scale of 0 stands for a row of codes 0: any scale gives its part
+        // of the sums, but a large one raises the maximum that the others' fp16
+        // weights are held to.  With 2^-60 a weight has all of its bits while the
+        // zero row's is at most 2^82 vs times it: 47 nats beside values of 0.01 in
+        // int8 (22 with fp16's least scale, 2^-24, 6 with 1).  Its inverse, in
+        // the total, is far from fp32's ends.
         float vs = (float)__builtin_bit_cast(_Float16, raw_vs);
-        vs = vs == 0.f ? 1.f : vs;
+        vs = vs == 0.f ? 0x1p-60f : vs;
         factors[wave][0][lane] = ks;
         factors[wave][1][lane] = __builtin_amdgcn_logf(vs);
         factors[wave][2][lane] = __builtin_amdgcn_rcpf(vs);
