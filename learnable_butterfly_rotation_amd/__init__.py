@@ -242,6 +242,21 @@ def _call(f, like, stream, *args):
         raise BflyError(status, "bfly_" + f.__name__)
 
 
+def _scratch(nbytes, like, stream):
+    """A uint8 tensor on the GPU of `like` for a call on `stream`, of that
+    stream's memory: what used it before and what will use it afterwards is
+    then in order with the call, which the current stream's memory, where a
+    block is reused as soon as its tensor is gone, would not be."""
+    import torch
+    if stream is None or like.get_device() < 0:  # the call refuses tensors of the host
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=like.device) if stream
+                  else torch.cuda.default_stream(like.device))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
 def _table_ws(n, theta, coeffs, workspace, like):
     """The workspace of a forward call: the caller's, or -- when the call
     needs one (angles without a table; n = 8192 always) and none is given --
@@ -529,14 +544,10 @@ def bfly_cache_attention(q, k_cache, v_cache, tables, lens, y, k_scales=None, v_
     the logarithm of the weights' sum; workspace: a uint8 tensor of
     bfly_cache_attention_workspace_bytes (None: a fresh one)."""
     if workspace is None:
-        import torch
         reach = tables.shape[1] * k_cache.shape[2] if max_len is None else max_len
         nbytes = bfly_cache_attention_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[1],
                                                       q.shape[2], reach)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-            if stream is not None:  # not the stream that it is allocated on
-                workspace.record_stream(torch.cuda.ExternalStream(stream, device=q.device)
-                                        if isinstance(stream, int) else stream)
+            workspace = _scratch(nbytes, q, stream)
     _call(_ext().cache_attention, q, stream, scale, max_len, window, k_cache, v_cache, k_scales,
           v_scales, q, tables, lens, y, lse, workspace)
