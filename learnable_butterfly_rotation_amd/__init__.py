@@ -257,17 +257,15 @@ def _scratch(nbytes, like, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
 
 
-def _table_ws(n, theta, coeffs, workspace, like):
+def _table_ws(n, theta, coeffs, workspace, like, stream):
     """The workspace of a forward call: the caller's, or -- when the call
     needs one (angles without a table; n = 8192 always) and none is given --
     a fresh uint8 tensor of bfly_forward_workspace_bytes(rows, n) from
     torch's allocator on the device of `like` (torch supplies the device
-    memory; the library allocates none)."""
+    memory; the library allocates none), of the call's stream."""
     if workspace is not None or (n != 8192 and (coeffs is not None or theta is None)):
         return workspace
-    import torch
-    nbytes = bfly_forward_workspace_bytes(like.shape[0], n)
-    return torch.empty(max(1, nbytes), dtype=torch.uint8, device=like.device)
+    return _scratch(max(1, bfly_forward_workspace_bytes(like.shape[0], n)), like, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -297,7 +295,7 @@ def bfly_prepare_hadamard(n: int, coeffs, stream=None) -> None:
 def bfly_forward(x, y, theta=None, coeffs=None, workspace=None, stream=None) -> None:
     """y[r] = Q(theta) x[r]; x, y: [rows, n] float32/bfloat16 on the GPU."""
     rows, n = x.shape
-    ws = _table_ws(n, theta, coeffs, workspace, x)
+    ws = _table_ws(n, theta, coeffs, workspace, x, stream)
     _check(lib().bfly_forward(_ptr(x), _dt(x), _ptr(y), _dt(y), rows, n, _ptr(theta),
                               _ptr(coeffs), _ptr(ws), _nbytes(ws), _stream(stream)),
            "bfly_forward")
@@ -307,7 +305,7 @@ def bfly_forward_quant(x, y, codes, scales, zeros=None, theta=None, coeffs=None,
                        group=128, mode=BFLY_SYM_ABSMAX, workspace=None, stream=None) -> None:
     """Forward fused with per-group RTN quantization (y may be None)."""
     rows, n = x.shape
-    ws = _table_ws(n, theta, coeffs, workspace, x)
+    ws = _table_ws(n, theta, coeffs, workspace, x, stream)
     _check(lib().bfly_forward_quant(_ptr(x), _dt(x), _ptr(y), _dt(y) if y is not None else 0,
                                     _ptr(codes), _ptr(scales), _ptr(zeros), rows, n, _ptr(theta),
                                     _ptr(coeffs), bits, group, mode, _ptr(ws), _nbytes(ws),
@@ -332,7 +330,7 @@ def bfly_kron_forward(x, y, mix, codes=None, scales=None, zeros=None, theta_b=No
     """(O kron B) on rows of n = m * nb; mix: [m, m] float32 on the GPU."""
     rows, n = x.shape
     m = mix.shape[0]
-    ws = _table_ws(n // m, theta_b, coeffs_b, workspace, x)
+    ws = _table_ws(n // m, theta_b, coeffs_b, workspace, x, stream)
     _check(lib().bfly_kron_forward(_ptr(x), _dt(x), _ptr(y), _dt(y) if y is not None else 0,
                                    _ptr(codes), _ptr(scales), _ptr(zeros), rows, m, n // m,
                                    _ptr(theta_b), _ptr(coeffs_b), _ptr(mix), bits, group, mode,

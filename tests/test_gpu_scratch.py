@@ -55,3 +55,18 @@ def test_the_default_stream_by_its_handle():
     b.run(stream=0)
     torch.cuda.synchronize()
     assert torch.equal(b.y, want)
+
+
+def test_scratch_of_a_forward():
+    x = torch.randn((64, 8192), device="cuda")
+    theta = torch.randn((13, 4096), device="cuda")
+    want, y = torch.empty_like(x), torch.empty_like(x)
+    B.bfly_forward(x, want, theta=theta)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = bytes_of(s.cuda_stream)
+    B.bfly_forward(x, y, theta=theta, stream=s)
+    torch.cuda.synchronize()
+    assert bytes_of(s.cuda_stream) >= before + B.bfly_forward_workspace_bytes(64, 8192)
+    assert torch.equal(y, want)

@@ -66,3 +66,26 @@ def test_scratch_of_the_attention(made, monkeypatch):
     B.bfly_cache_attention(q, cache, cache, tables, None, None, max_len=20, stream=stream(77))
     B.bfly_cache_attention(q, cache, cache, tables, None, None, workspace="mine", stream=77)
     assert log == [] and calls[-1][1] == "mine"
+
+
+@pytest.mark.parametrize("call", ["forward", "forward_quant", "kron_forward"])
+def test_scratch_of_the_forwards(made, monkeypatch, call):
+    log, stream = made
+    got = []
+    library = SimpleNamespace(
+        bfly_forward_workspace_bytes=B.lib().bfly_forward_workspace_bytes,
+        **{"bfly_" + call: lambda *args: got.append(args[-1]) or 0})
+    monkeypatch.setattr(B, "lib", lambda: library)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: stream(1))
+    x, table = rows(6, 256), rows(8, 128, dtype=torch.float32)
+    need = B.bfly_forward_workspace_bytes(6, 256)
+    assert need > 0
+    for given, handle in ((None, 1), (stream(77), 77), (78, 78), (0, 0)):
+        log.clear(), got.clear()
+        if call == "forward":
+            B.bfly_forward(x, x, theta=table, stream=given)
+        elif call == "forward_quant":
+            B.bfly_forward_quant(x, x, x, x, theta=table, stream=given)
+        else:
+            B.bfly_kron_forward(rows(6, 512), x, rows(2, 2), theta_b=table, stream=given)
+        assert log == [(need, handle)] and got == [handle]
