@@ -686,8 +686,12 @@ bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint
  * whose scores are -infinity.  What lies in a page behind a sequence's tokens
  * has no influence, whatever its bits are.  A NaN in q, or in a row in reach,
  * gives NaN in the results that use it and no others; an infinity in q counts
- * as a NaN, one in a key makes the results that use it unspecified.  Scales are
- * as bfly_cache_write leaves them: not negative, and 0 with codes of 0 only.
+ * as a NaN, one in a key makes the results that use it unspecified.  One in a
+ * value (BFLY_KV_BF16) is its element's result, by its sign, where its weight is
+ * above 2^-100 of the largest, and that or NaN below.  Specified are results
+ * while |scale| is below 1e30, and max |q|, |scale| max |q| and 2 head_dim
+ * max(1, |scale|) max |q| max |k| are below 2e38.  The cache's scales are as
+ * bfly_cache_write leaves them: not negative, and 0 with codes of 0 only.
  * The sums are held in fp32.  With bf16 q and y the weights e^(s - m) enter the
  * second product with 11 bits (quantized caches) or 15 (BFLY_KV_BF16); with an
  * fp32 q or y with 22, and q enters the first with 22 (24).  Over a quantized

@@ -584,7 +584,9 @@ __global__ void __launch_bounds__(64 * W, 2)
         const f32x4 iv = *reinterpret_cast<const f32x4*>(&factors[wave][2][16 * j + 4 * group]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          u[4 * j + i] = fmaf(s[j][i] * qscale, ks[i], lv[i]);
+          // (the factors first: with the sum first a score within fp32 could pass
+          // through an infinity)
+          u[4 * j + i] = fmaf(s[j][i], qscale * ks[i], lv[i]);
           inv[4 * j + i] = iv[i];
         }
       }

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import learnable_butterfly_rotation_amd as B
-from test_gpu_cache import BF16, F32, TOP, Batch, gpu, np64  # noqa: F401
+from test_gpu_cache import BF16, F32, TOP, U, Batch, gpu, ints, np64  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,52 @@ def test_rows_of_zeros_only(fmt):
         b.run()
         b.check()
         assert (b.y == 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "e4m3", "int4"])
+@pytest.mark.parametrize("q,y", [(BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("n", [50, 3000])
+def test_scores_as_large_as_fp32_holds(fmt, q, y, n):
+    """Scores of 1e36 from queries of 1e38 and keys of 1e-3: the largest, five
+    times the others' standard deviations and more ahead of them, has all the
+    weight.  y is its value to the roundings of the scale's inverse and the
+    division (4 u) and its own, lse its score to those of 64 products of up to 24
+    bits and three factors (72 u of sum |q k|, 2^-22 of it for an fp32 query's)."""
+    rng = np.random.default_rng(n)
+    k = (1e-3 * rng.standard_normal((n, 2, 64))).astype(np.float32)
+    b = Batch(fmt, [n], 2, 2, 64, 16, q, y, seed=42)
+    b.q = (b.q.float() * 5e37).clamp(-2e38, 2e38).to(q)
+    aim = np64(b.q)[0]
+    k[7] = 2e-3 * aim / np.sqrt((aim * aim).mean(1, keepdims=True))
+    v = rng.standard_normal(k.shape).astype(np.float32)
+    b.cache.write(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), ints(b.slots))
+    b.run()
+    keys, values = b.cache.rows()
+    half = 2.0 ** -8 if y == BF16 else U
+    for h in range(2):
+        s = keys[b.slots, h] @ aim[h] / 8
+        a = (np.abs(keys[b.slots, h]) @ np.abs(aim[h])).max() / 8
+        off = (72 * U + (2.0 ** -22 if q == F32 else 0.0)) * a
+        assert np.argmax(s) == 7 and s[7] > 1e35 and s[7] - np.delete(s, 7).max() > 100 * off
+        want = values[b.slots[7], h]
+        assert (np.abs(np64(b.y)[0, h] - want) <= (4 * U + half) * np.abs(want)).all()
+        assert abs(np64(b.lse)[0, h] - s[7]) <= off + 4 * U * s[7]
+
+
+@pytest.mark.parametrize("y", [BF16, F32])
+@pytest.mark.parametrize("n", [300, 5000])
+def test_an_infinite_value_of_a_small_weight(y, n):
+    """A weight of 2^-90 of the largest and above makes an infinity the result's,
+    in the largest's wave and chunk and in others, before it and behind it."""
+    for token, score in ((5, 0.0), (38, 0.0), (n - 1, 0.0), (5, -4.0), (n - 2, -4.0)):
+        v = np.random.default_rng(n).standard_normal((n, 2, 64)).astype(np.float32)
+        v[token, :, 3], v[token, :, 4] = np.inf, -np.inf
+        same = dict(heads=2, kv=2, d=64, page=16, q=F32, y=y, seed=43)
+        b = Batch("bf16", [n], k=np.zeros_like(v), v=v, **same)
+        k = ahead(b, 37, 58.0)
+        k[token] = k[37] * np.float32(score / 58.0)
+        b = Batch("bf16", [n], k=k, v=v, **same)
+        b.run()
+        got = np64(b.y)[0]
+        assert (got[:, 3] == np.inf).all() and (got[:, 4] == -np.inf).all()
+        assert np.isfinite(np.delete(got, (3, 4), 1)).all()
