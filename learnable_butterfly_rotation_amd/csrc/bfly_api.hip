@@ -12,6 +12,7 @@
 #include "bfly_common.h"
 #include "bfly_calib.h"
 #include "bfly_calib_w.h"
+#include "bfly_attend_cut.h"
 #include "bfly_cache.h"
 #include "bfly_clip.h"
 #include "bfly_lora.h"

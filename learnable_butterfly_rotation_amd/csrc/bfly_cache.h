@@ -53,9 +53,6 @@ struct AttendParams {
   int32_t q_bf16, y_bf16;
   float scale;
 };
-// Workspace bytes of a call, over all windows: a function of the sizes only
-// that never falls with rows, heads, head_dim or max_len.
-size_t attend_workspace_bytes(int64_t rows, int heads, int kv_heads, int head_dim, int max_len);
 hipError_t launch_attend(const AttendParams& p, hipStream_t s);
 
 }  // namespace bfly
