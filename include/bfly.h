@@ -679,8 +679,10 @@ bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint
  *   workspace: >= bfly_cache_attention_workspace_bytes(rows, heads, kv_heads,
  *             head_dim, max_len) bytes of device scratch, 16-byte aligned (0:
  *             may be NULL); what it holds does not matter; two calls that may
- *             overlap need one each.  The size never falls with rows, heads,
- *             head_dim or max_len: one for the largest call serves the others
+ *             overlap need one each.  With the same kv_heads the size never
+ *             falls with rows, heads, head_dim or max_len: one for the largest
+ *             call serves the others.  With more kv_heads it may be smaller:
+ *             layers that differ in them take the largest of their sizes
  * Tokens whose table entry is outside [0, pages) are out of reach.  A row with
  * nothing in reach gives y = 0 and lse = -infinity, and so does one all of
  * whose scores are -infinity.  What lies in a page behind a sequence's tokens

@@ -526,6 +526,8 @@ def bfly_cache_read(k_cache, v_cache, slots, k, v, k_scales=None, v_scales=None,
 
 def bfly_cache_attention_workspace_bytes(rows: int, heads: int, kv_heads: int, head_dim: int,
                                          max_len: int) -> int:
+    """Never falls with rows, heads, head_dim or max_len while kv_heads stays;
+    layers that differ in kv_heads take the largest of their sizes."""
     return lib().bfly_cache_attention_workspace_bytes(rows, heads, kv_heads, head_dim, max_len)
 
 
