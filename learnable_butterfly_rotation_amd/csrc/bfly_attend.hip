@@ -611,12 +611,15 @@ __global__ void __launch_bounds__(64 * W, 2)
     }
     // weights are 2^(u - m) with m between 15 below the largest u and 8 below
     // it, so that it seldom moves and fp16 holds them down to 2^-22 of the
-    // largest with all bits
+    // largest with all bits.  Both are differences from top, exact where they
+    // matter: for scores from 2^24 on m + 15 may round to m + 16 and top - 8 to
+    // top - 16, and fp16 does not hold 2^16.
     float top = fmaxf(fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])),
                       fmaxf(fmaxf(u[4], u[5]), fmaxf(u[6], u[7])));
-    if (__any(top > m + 15.f)) {
+    if (__any(top - m > 15.f)) {
       top = across_groups(top, [](float a, float b) { return fmaxf(a, b); });
-      const float to = top > m + 15.f ? top - 8.f : m;
+      const float below = top - (top - 8.f) > 15.f ? top : top - 8.f;
+      const float to = top - m > 15.f ? below : m;
       const float fade = __builtin_amdgcn_exp2f(m - to);
       m = to;
       total *= fade;

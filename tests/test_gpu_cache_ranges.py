@@ -1,5 +1,7 @@
 """bfly_cache_attention where a value's scale or a score lies at an end of its
 range."""
+import math
+
 import numpy as np
 import pytest
 
@@ -102,3 +104,44 @@ def test_an_infinite_value_of_a_small_weight(y, n):
         got = np64(b.y)[0]
         assert (got[:, 3] == np.inf).all() and (got[:, 4] == -np.inf).all()
         assert np.isfinite(np.delete(got, (3, 4), 1)).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "e4m3", "int4"])
+@pytest.mark.parametrize("n", [300, 2000])
+def test_scores_whose_last_bit_is_more_than_one(fmt, n):
+    """Scores of up to 2^40, where fp32 has steps of 1, 2, 4 ... in the exponent of
+    a weight.  All alike, they give the values' mean: n weights of 1 exactly, their
+    sum and the values' scales (n + 64 u in all).  Over a quantized cache the
+    exponent is u = s + log2 vs, rounded once, by half a step of s: 2^(E - 25) for
+    |u| < 2^E, whatever the size of log2 vs.  Weights that should be 1 then lie
+    between 1 / f and f = 2^(2^(E - 25)), each over their sum between 1 / (n f^2)
+    and f^2 / n, so that y is off by up to f^2 - 1 of the largest value.  Apart by a
+    few steps, the larger ones later, they have no weights to compare with, but a
+    result between the values' least and largest, to the sums' roundings."""
+    d, kv, heads = 64, 2, 4
+    rng = np.random.default_rng(n)
+    v = rng.standard_normal((n, kv, d)).astype(np.float32)
+    alike = np.zeros((n, kv, d), np.float32)
+    alike[:, :, 0] = 7.0
+    apart = alike.copy()
+    apart[:, :, 1] = (np.arange(n) * 8 // n)[:, None]            # codes 0 ... 7 of int4 too
+    tol = (n + 64) * U
+    for k in (alike, apart):
+        b = Batch(fmt, [n], heads, kv, d, 16, F32, F32, seed=44, k=k, v=v)
+        values = b.cache.rows()[1][b.slots]
+        for power in range(18, 41):
+            for sign in (1.0, -1.0):
+                b.q.zero_()
+                b.q[:, :, 0], b.q[:, :, 1] = sign * 2.0 ** power, 8.0
+                for scale in (0.1, 0.125, 0.13):
+                    b.out()
+                    b.run(scale=scale)
+                    got = np64(b.y)[0].reshape(kv, heads // kv, d)
+                    size = np.abs(values).max(0)[:, None]
+                    assert (got >= values.min(0)[:, None] - tol * size).all(), (power, sign, scale)
+                    assert (got <= values.max(0)[:, None] + tol * size).all(), (power, sign, scale)
+                    if k is alike:
+                        e = math.ceil(math.log2(7 * 2.0 ** power * scale / math.log(2) + 32))
+                        more = 0.0 if fmt == "bf16" else 4.0 ** (2.0 ** min(e - 25, 3)) - 1
+                        off = np.abs(got - values.mean(0)[:, None])
+                        assert (off <= (tol + more) * size).all(), (power, sign, scale)
