@@ -672,7 +672,9 @@ bfly_status bfly_cache_read(const void* k_cache, const void* v_cache, const uint
  *   window  : the last `window` of them are in reach, all for 0
  *   max_len : a bound of the lengths, at most table_width * page_size, that
  *             sizes the launch and the workspace: the closer it is, the better
- *             the work is spread
+ *             the work is spread (sequences of 4096 tokens, 32 heads over 8 of
+ *             128 int8, bounds of 4096, 32768 and 131072: one sequence 8.4, 11.2
+ *             and 22.5 us, 32 of them 58.7, 58.0 and 67.9)
  *   y       : [rows][heads][head_dim] of y_dt, rounded once
  *   lse     : fp32 [rows][heads], log(sum_t e^(s_t)) (it joins this result
  *             with one over other tokens), or NULL

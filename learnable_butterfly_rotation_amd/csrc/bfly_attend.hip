@@ -320,7 +320,7 @@ __device__ __forceinline__ float log_sum(float top, float l) {
 }
 
 // Whether a step's registers leave none for the queries, which then stay in LDS
-// (24 rows of a window of 2047: 16.4 -> 15.7 us, without scratch).
+// (24 rows of a window of 2047: 15.8 us in registers, 15.3).
 template <int FMT, int D>
 constexpr bool kQueriesInLds = FMT == kCacheBF16 && D == 256;
 
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(64 * W, 2)
   constexpr int ROUND = W * kStep;
   // heads whose results are joined at a time, as many as leave room for two
   // workgroups in a CU's 160 KiB (24 rows of a window of 2047, 16 heads of 256:
-  // eight heads 16.2 us, sixteen 15.9), less of eight waves (321 tokens 6.33, 6.39)
+  // eight heads 15.7 us, sixteen 15.3); of eight waves less (the same: 321 tokens 6.05)
   constexpr int QUERIES = QN * (D / 32) * 64 * 16, EACH = W * (D + 4) * 4;
   constexpr int MOST = ((W > 4 ? 48 : 77) * 1024 - QUERIES) / EACH;
   constexpr int COLS = MOST >= kHeads ? kHeads : MOST >= kHeads / 2 ? kHeads / 2 : kHeads / 4;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(64 * W, 2)
   __shared__ float factors[W][3][kStep];        // of a step's tokens: ks, log2 vs, 1 / vs
   __shared__ float query_scales[kHeads];
   // a wave may join its results while another has yet to read the queries: they
-  // share no memory (a barrier instead: 321 tokens 6.45 us for 6.30)
+  // share no memory (a barrier instead: 321 tokens 6.28 us for 6.10)
   constexpr bool IN_LDS = kQueriesInLds<FMT, D>;
   constexpr bool APART = W > 1 || IN_LDS;
   __shared__ __align__(16) char room[APART ? SUMS + QUERIES : SUMS > QUERIES ? SUMS : QUERIES];
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(64 * W, 2)
   // Of a wave's first tiles the rows in front of what is in reach and behind it
   // are fetched as the first and the last of that: a short sequence touches no
   // row that has no part in it (113 rows of up to 6 tokens of 18 heads of 256
-  // bf16 27.2 -> 20.1 us, with one wave to a workgroup).  A long one's last tiles
+  // bf16 14.0 us without, 9.8).  A long one's last tiles
   // are not worth the registers.
   const auto inside = [&](auto first, int i, int t) {
     if constexpr (!decltype(first)::value) return i;
@@ -757,15 +757,15 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   const int chunk = cut.chunk, splits = cut.splits;
   // a chunk each of up to 256 rows is looked for among their lengths, so that no
   // workgroup is there for what a short row does not have (64 ragged rows of up
-  // to 8192: 50.5 us, 57 without)
+  // to 8192: 45.1 us, 52.8 without)
   const bool packed = splits > 1 && p.rows > 1 && p.rows <= 256 && p.rows * splits < 65536;
   const unsigned across = (unsigned)(p.kv_heads * blocks);
   const dim3 grid = packed ? dim3(across, (unsigned)(p.rows * splits))
                            : dim3((unsigned)items, (unsigned)splits);
   // What the last-level cache (256 MiB) cannot hold until the next call goes
-  // past it: 272 MB of one sequence 51.3 us, 55.9 through the caches; 64 ragged
-  // rows of up to 553 MB together, 178 as it was, 48.3 and 50.5.  Below, it costs
-  // what the cache would have kept (80 MB of up to 272 MB 24.8 us for 22.9).
+  // past it: 272 MB of one sequence 48.5 us, 53.8 through the caches; 64 ragged
+  // rows of up to 553 MB together, 178 as it was, 45.1 and 48.0.  Below, it costs
+  // what the cache would have kept (80 MB of up to 272 MB 22.0 us for 19.5).
   // Lengths spread, so of several rows half of what there may be is counted; what
   // several workgroups read, for more than 16 query heads, stays.
   const double bytes = 2.0 * (double)p.rows * p.kv_heads * reach * cache_bytes(p.format, p.head_dim);
@@ -773,10 +773,11 @@ hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
                     (p.rows > 1 ? bytes / 2 : bytes) >= 256.0 * (1 << 20);
   // Waves of a workgroup that has a row's whole length.  One where there are more
   // rows and heads than the card has room for and their lengths are short: 904
-  // items of 32 tokens int8 5.1 us, with four waves 7.5, 4096 of 256 tokens 30 and
-  // 34; but 904 of 256 tokens 14.5 and 11.0.  Eight where each of up to 256 has a
-  // CU to itself and more than one round of four: 256 items of 512 tokens 9.2,
-  // with four 10.6, of 256 tokens 6.2 and 6.3; 800 items int4 14 and 9.
+  // items of 32 tokens int8 4.8 us, with four waves 6.9; from 256 tokens on it is
+  // the same, 904 items 14.6 and 14.3, 4096 56.0 and 55.3.  Eight where each of up
+  // to 256 has a CU to itself and more than one round of four: 256 items of 512
+  // tokens 9.2, with four 10.0, of 256 tokens 7.0 and 7.1; but 800 items of 512
+  // tokens int4 16.4 and 14.2.  (Pages of their own, three sets of them in turn.)
   const int waves = splits > 1 || once                             ? 4
                     : items > 8 * (int64_t)std::max(reach, kStep) ? 1
                     : reach > 256 && items <= 256                 ? 8

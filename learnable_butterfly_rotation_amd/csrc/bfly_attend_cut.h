@@ -23,16 +23,23 @@ inline int attend_reach(int max_len, int window) {
 // How a call's lengths, up to `reach`, are cut: into chunks, or not at all.
 //   Up to 512 tokens (1024 where there are 128 items or more, each a row's
 // key-value head) the second launch costs more than it spreads: 32 rows of 8
-// heads of 1024 tokens int8 12.9 us in one chunk, 13.6 in 256s.
+// heads of 1024 tokens int8 13.9 us in one chunk, 18.7 in 256s, 16.5 in 512s; 4
+// rows of 512 tokens 7.3, in 128s 7.8, in 256s 8.8.
 //   One row is as long as it is known to be: 512 workgroups (131072 tokens of
-// e4m3 56 us, 62 with 1024).
+// e4m3 48.5 us; 55.0 with 1024, 61.8 with 256).
 //   Rows of lengths that only the device knows: a card full of chunks as short
 // as pays, since no workgroup may last much longer than the average.  128
-// tokens, while there are at most 2048 workgroups (8 rows of 1024: 8.6 us, 256
-// tokens 10.0), up to 512 (32 rows of 4096: 128 tokens 31.7 us, 256 24.1, 512
-// 21.7, 1024 26.0; 64 ragged rows of up to 8192 int4: 512 50.5, 1024 52.5, 2048
-// 56), more where that would be above 8192 workgroups.  256 instead of 128
-// where a chunk's partial results, 16 heads of 256, are large (18.0 for 19.9).
+// tokens, while there are at most 2048 workgroups (8 ragged rows of up to 1024:
+// 8.0 us, in 256s 9.1, in 512s 11.0), up to 512 (32 rows of 4096, and ragged ones
+// of up to 4096: 128 tokens 73.7 and 28.1 us, 256 64.4 and 21.7, 512 58.7 and
+// 19.4, 1024 60.5 and 22.3; 64 ragged rows of up to 8192 int4: 256 58.2, 512
+// 45.1, 1024 45.6, 2048 47.5), more where that would be above 8192 workgroups.
+// 256 instead of 128 where a chunk's partial results, 16 heads of 256, are large
+// (24 rows of a window of 2047: 15.2 for 16.5).
+//   All this goes by the bound, not by the lengths: a bound far above them makes
+// chunks long and workgroups few.  Sequences of 4096 tokens int8, 8 heads, with
+// a bound of 4096, 32768 and 131072: one 8.4, 11.2 and 22.5 us, 32 of them 58.7,
+// 58.0 and 67.9.
 struct Cut {
   int chunk, splits;
 };
